@@ -50,7 +50,7 @@ typedef enum moe_status {
                                 the kernel skipped its work */
 } moe_status;
 
-enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2 /* caches and attention only */ };
 
 /* Shapes and formats of one layer, fixed at create time. */
 typedef struct moe_decode_config {
@@ -286,6 +286,110 @@ void moe_stack_destroy(moe_stack_t *s);
  * alignment outside the above (nothing enqueued), or MOE_ERR_CUDA if the launch fails. */
 int moe_gemv_bf16(const void *W, const void *x, int64_t x_stride, float *y, int32_t n_mats,
                   int32_t m, int32_t n_out, int32_t n_in, void *stream);
+
+/* ---- the attention half of a decoder layer ----------------------------------------------------
+ * Between the q/k/v projections (moe_gemv_bf16) and the output projection: norms and rotation
+ * with the write into a cache of pages (moe_qk_norm_rope), attention of decoded or drafted tokens
+ * (moe_tree_attention) and of prompts (moe_prompt_attention) over those pages.  The pages this
+ * library follows measure the projections and the block but not this half; its formulas are the
+ * usual ones, written at each call.
+ *
+ * All three calls are asynchronous on `stream`, allocate nothing, keep nothing between calls and
+ * may be captured into a graph.  They run on the current device.  Strides are in elements.
+ * Arguments that the host can see to be wrong return a negative status and enqueue nothing;
+ * device data that is out of range (a slot or page outside the cache, a sequence outside its
+ * bounds) sets bit 1 of *device_error (MOE_ERR_BAD_ID's bit; int32 device, starts at 0, may be
+ * NULL) and is not read or written.  Bit 2 is the time-out of a bounded wait (never expected). */
+
+/* A cache of pages, borrowed: K of position `o` of page `n` for head `h` is the head_dim elements
+ * at k + n * page_stride + h * head_stride + o * token_stride, V likewise at v. */
+typedef struct moe_kv_cache {
+  void *k;                 /* device, 16-byte aligned */
+  void *v;
+  int64_t page_stride;     /* each a multiple of 8 */
+  int64_t head_stride;
+  int64_t token_stride;
+  int32_t n_pages;
+  int32_t page_size;       /* positions of a page; attention takes 16, 32, 64, ... 1024 */
+  int32_t n_kv_heads;
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t dtype;           /* MOE_DTYPE_BF16 or MOE_DTYPE_F16 */
+} moe_kv_cache;
+
+/* Norm, rotation and cache write of n_tokens tokens.
+ *   y = w * x / sqrt(mean(x^2) + eps)     per query and key head, where its weight is not NULL
+ *   (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position * inv_freq[i],
+ *   for i < rot_dim / 2 and (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved;
+ * fp32 throughout (angles reduced in fp64), rounded once.  Queries go to q_out; keys, and values
+ * only rounded, go to slots[t] = page * page_size + position in the page.  A token whose slot is
+ * negative is padding: nothing of it is read or written. Two tokens with one slot leave either. */
+typedef struct moe_norm_rope {
+  const void *q;           /* [n_tokens][n_q_heads][head_dim] by strides, in_dtype, 16-byte aligned */
+  const void *k;           /* [n_tokens][n_kv_heads][head_dim] */
+  const void *v;
+  int64_t q_row_stride, q_head_stride;   /* multiples of 16 bytes, like all strides here */
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  void *q_out;             /* cache dtype; may be q itself (same type and strides) */
+  int64_t q_out_row_stride, q_out_head_stride;
+  const void *q_weight;    /* [head_dim] in the cache's dtype, 16-byte aligned, or NULL: no norm */
+  const void *k_weight;
+  const double *inv_freq;  /* fp64 [rot_dim / 2] device: radians per position */
+  const int32_t *positions; /* int32 [n_tokens] device */
+  const int32_t *slots;    /* int32 [n_tokens] device */
+  int32_t *device_error;
+  int32_t n_tokens;
+  int32_t n_q_heads;
+  int32_t rot_dim;         /* 0 .. head_dim, a multiple of 16 */
+  int32_t interleaved;     /* 0 or 1 */
+  int32_t in_dtype;        /* MOE_DTYPE_F32 (the projections' outputs) or the cache's dtype */
+  float eps;               /* in [0, 1] */
+} moe_norm_rope;
+
+int moe_qk_norm_rope(const moe_kv_cache *cache, const moe_norm_rope *args, void *stream);
+
+/* A batch of sequences whose keys and values (those of the queries included) are in the cache.
+ * Sequence s has the rows cu_q[s] .. cu_q[s+1]-1 of q and out; its first query is at position
+ * ctx_len[s], its positions o = 0 .. ctx_len[s] + rows - 1 lie on page page_table[s][o / page_size].
+ * Query heads h * g .. h * g + g - 1 read key/value head h (g = n_q_heads / n_kv_heads <= 64).
+ *   out = softmax over the positions seen (scale * q . k) . v
+ * Scores, maxima, sums and the weighted sum are fp32; the weights enter the product with v in the
+ * cache's dtype; out is rounded once.  A query that sees nothing gets zeros.  Rows behind
+ * cu_q[n_seqs] are neither read nor written.  What pages hold beyond a sequence's positions may be
+ * anything; K and V of its positions have to be finite. */
+typedef struct moe_attention {
+  const void *q;           /* [n_rows][n_q_heads][head_dim], cache dtype, 16-byte aligned */
+  void *out;               /* likewise; must not overlap q */
+  int64_t q_row_stride, q_head_stride;       /* multiples of 8 */
+  int64_t out_row_stride, out_head_stride;
+  const int32_t *cu_q;     /* int32 [n_seqs + 1] device, ascending from >= 0 to <= n_rows */
+  const int32_t *ctx_len;  /* int32 [n_seqs] device */
+  const int32_t *page_table; /* int32 [n_seqs][table_stride] device; only used entries are read */
+  int64_t table_stride;
+  int32_t table_width;     /* pages a sequence may have */
+  int32_t n_seqs;
+  int32_t n_rows;
+  int32_t n_q_heads;
+  float scale;             /* > 0 */
+  int32_t *device_error;
+} moe_attention;
+
+/* Decoded tokens, or trees of drafted tokens: up to max_q <= MOE_TREE_MAX_Q rows a sequence.  A
+ * query sees every position before ctx_len, and position ctx_len + j when bit j of its tree_mask
+ * (uint64 [n_rows] device) is set; with tree_mask NULL, when j is not behind it.
+ * workspace: device, 16-byte aligned, of at least the bytes that moe_tree_attention_workspace gives
+ * for the same cache, args and max_q; its content is of no account, but two calls that may overlap
+ * on the GPU need one each. */
+#define MOE_TREE_MAX_Q 64
+int moe_tree_attention_workspace(const moe_kv_cache *cache, const moe_attention *args,
+                                 int32_t max_q, int64_t *bytes);
+int moe_tree_attention(const moe_kv_cache *cache, const moe_attention *args,
+                       const uint64_t *tree_mask, int32_t max_q, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Whole prompts, or chunks of them behind ctx_len cached positions, packed one after the other:
+ * causal, query i of a sequence sees the positions 0 .. ctx_len + i. */
+int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, void *stream);
 
 /* ---- canonical packing (host) ---------------------------------------------------------------
  * codes: uint8 [rows][cols], one code per byte, each < 2^bits; packed: [rows][cols*bits/8].
