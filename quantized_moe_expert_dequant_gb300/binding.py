@@ -7,7 +7,9 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
+import struct
 import threading
 
 import numpy as np
@@ -67,35 +69,11 @@ class LayerWeights(ctypes.Structure):
                 ("sh_down", Proj), ("gate_vec", ctypes.c_void_p)]
 
 
-class KvCacheStruct(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v")]
-                + [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")]
-                + [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim",
-                                                 "dtype")])
-
-
-class NormRopeStruct(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
-                + [(n, ctypes.c_int64) for n in (
-                    "q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
-                    "v_row_stride", "v_head_stride")]
-                + [("q_out", ctypes.c_void_p), ("q_out_row_stride", ctypes.c_int64),
-                   ("q_out_head_stride", ctypes.c_int64)]
-                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "inv_freq", "positions",
-                                                  "slots", "device_error")]
-                + [(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "rot_dim", "interleaved",
-                                                 "in_dtype")]
-                + [("eps", ctypes.c_float)])
-
-
-class AttentionStruct(ctypes.Structure):
-    _fields_ = ([("q", ctypes.c_void_p), ("out", ctypes.c_void_p)]
-                + [(n, ctypes.c_int64) for n in ("q_row_stride", "q_head_stride",
-                                                 "out_row_stride", "out_head_stride")]
-                + [(n, ctypes.c_void_p) for n in ("cu_q", "ctx_len", "page_table")]
-                + [("table_stride", ctypes.c_int64)]
-                + [(n, ctypes.c_int32) for n in ("table_width", "n_seqs", "n_rows", "n_q_heads")]
-                + [("scale", ctypes.c_float), ("device_error", ctypes.c_void_p)])
+# The structs of the attention calls as packed bytes (native alignment, the C layout): one pack() is
+# much cheaper than filling a ctypes.Structure field by field, and these calls take microseconds.
+_pack_kv_cache = struct.Struct("@2P3q5i").pack
+_pack_norm_rope = struct.Struct("@3P6qP2q6P5if").pack
+_pack_attention = struct.Struct("@2P4q3Pq4ifP").pack
 
 
 _lock = threading.Lock()
@@ -155,15 +133,10 @@ def lib() -> ctypes.CDLL:
                 "moe_router_topk": [vp, i32, i32, i32, vp, vp, vp],
                 "moe_debug_col_pieces": [i32, i32, i32, i32, i32, i32, i32, i32, vp, i32],
                 "moe_debug_col_plan": [ctypes.POINTER(Config), i32, i32, vp, vp],
-                "moe_qk_norm_rope": [ctypes.POINTER(KvCacheStruct), ctypes.POINTER(NormRopeStruct),
-                                     vp],
-                "moe_tree_attention_workspace": [ctypes.POINTER(KvCacheStruct),
-                                                 ctypes.POINTER(AttentionStruct), i32,
-                                                 ctypes.POINTER(i64)],
-                "moe_tree_attention": [ctypes.POINTER(KvCacheStruct),
-                                       ctypes.POINTER(AttentionStruct), vp, i32, vp, i64, vp],
-                "moe_prompt_attention": [ctypes.POINTER(KvCacheStruct),
-                                         ctypes.POINTER(AttentionStruct), vp],
+                "moe_qk_norm_rope": [vp, vp, vp],
+                "moe_tree_attention_workspace": [vp, vp, i32, vp],
+                "moe_tree_attention": [vp, vp, vp, i32, vp, i64, vp],
+                "moe_prompt_attention": [vp, vp, vp],
             }
             if _timeline:
                 sig["moe_stack_timeline"] = [vp, vp, i64, ctypes.POINTER(i32)]
@@ -533,25 +506,23 @@ def gemv_bf16(W, x, y=None, shared_x: bool = True, stream=None):
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.float16: DTYPE_F16}
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _vector(t, dtype, n, device, name) -> int | None:
-    """The address of a contiguous tensor of n elements (at least) that a kernel reads."""
+def _vector(t, dtype, n, dev, name) -> int:
+    """The address of a contiguous tensor of n elements (at least) on GPU `dev`; 0 for None."""
     if t is None:
-        return None
-    _need(t.dtype == dtype and t.is_contiguous() and t.numel() >= n and t.device == device,
-          f"{name}: contiguous {dtype} of {n} elements on {device} is wanted")
+        return 0
+    if t.dtype != dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements on cuda:{dev} is "
+                         f"wanted, not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, heads, dim, device, name):
+def _rows(t, shape, dtype, dev, name):
     """(address, row stride, head stride) of a tensor [rows, heads, dim]."""
-    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim and t.stride(2) == 1
-          and t.device == device, f"{name}: [rows, {heads}, {dim}] on {device} is wanted")
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0)
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or st[2] != 1:
+        raise ValueError(f"{name}: {dtype} {shape} on cuda:{dev} with elements side by side is "
+                         f"wanted, not {t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
 def _empty_on(shape, dtype, device, stream):
@@ -564,14 +535,24 @@ def _empty_on(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(fn: str, device, *args, stream) -> None:
-    """One library call with `device` current."""
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == device.index:
-        check(fn, f(*args, _stream(stream)))
+@functools.lru_cache(maxsize=None)
+def _entry(fn: str):
+    return getattr(lib(), fn)
+
+
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """One library call on `stream` (None: the current one of GPU `dev`) with that GPU current."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = _entry(fn)(*args, stream)
     else:
-        with torch.cuda.device(device):
-            check(fn, f(*args, _stream(stream)))
+        with torch.cuda.device(dev):
+            rc = _entry(fn)(*args, stream)
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
 
 
 class KvCache:
@@ -580,17 +561,19 @@ class KvCache:
     [n_pages, page_size, n_kv_heads, head_dim] does as well."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
-        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype
-              and k.stride() == v.stride() and k.stride(3) == 1 and k.device == v.device
-              and k.is_cuda, "k and v: [n_pages, n_kv_heads, page_size, head_dim] alike, on a GPU")
-        _need(k.dtype in (torch.bfloat16, torch.float16), "k and v: bf16 or fp16")
+        if not (k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype
+                and k.stride() == v.stride() and k.stride(3) == 1 and k.device == v.device
+                and k.is_cuda):
+            raise ValueError("k and v: [n_pages, n_kv_heads, page_size, head_dim] alike, on a GPU")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("k and v: bf16 or fp16")
         self.k, self.v = k, v
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.device, self.dtype = k.device, k.dtype
+        self._dev = k.get_device()
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
-        self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], *(
-            self.n_pages, self.page_size, self.n_kv_heads, self.head_dim), _DTYPES[k.dtype])
-        self._ref = ctypes.byref(self._struct)
+        self._c = _pack_kv_cache(k.data_ptr(), v.data_ptr(), *st, self.n_pages, self.page_size,
+                                 self.n_kv_heads, self.head_dim, _DTYPES[k.dtype])
 
 
 def qk_norm_rope(cache: KvCache, q, k, v, positions, slots, inv_freq, q_weight=None, k_weight=None,
@@ -601,52 +584,43 @@ def qk_norm_rope(cache: KvCache, q, k, v, positions, slots, inv_freq, q_weight=N
     the cache and returns q_out [T, Hq, D] in the cache's dtype.  positions int32 [T], inv_freq fp64
     [rot_dim / 2] (None: no rotation), weights [D] in the cache's dtype or None: no norm."""
     T, Hq, D = q.shape
-    g, dev = cache.n_kv_heads, cache.device
-    _need(k.shape[0] == T and v.shape[0] == T, "q, k and v: as many tokens each")
-    _need(q.dtype == k.dtype == v.dtype and q.dtype in _DTYPES, "q, k and v: one type")
+    dev, dt, to, kv = cache._dev, q.dtype, cache.dtype, (T, cache.n_kv_heads, cache.head_dim)
+    if D != cache.head_dim or dt not in _DTYPES:
+        raise ValueError(f"q: fp32 or {to} heads of {cache.head_dim} are wanted")
+    shape = (T, Hq, D)
     if q_out is None:
-        q_out = _empty_on((T, Hq, D), cache.dtype, dev, stream)
-    _need(q_out.dtype == cache.dtype and q_out.shape[0] == T, "q_out: the cache's dtype")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    D = cache.head_dim
-    a = NormRopeStruct()
-    a.q, a.q_row_stride, a.q_head_stride = _rows(q, Hq, D, dev, "q")
-    a.k, a.k_row_stride, a.k_head_stride = _rows(k, g, D, dev, "k")
-    a.v, a.v_row_stride, a.v_head_stride = _rows(v, g, D, dev, "v")
-    a.q_out, a.q_out_row_stride, a.q_out_head_stride = _rows(q_out, Hq, D, dev, "q_out")
-    a.q_weight = _vector(q_weight, cache.dtype, D, dev, "q_weight")
-    a.k_weight = _vector(k_weight, cache.dtype, D, dev, "k_weight")
-    a.inv_freq = _vector(inv_freq, torch.float64, 1, dev, "inv_freq")
-    a.positions = _vector(positions, torch.int32, T, dev, "positions")
-    a.slots = _vector(slots, torch.int32, T, dev, "slots")
-    a.device_error = _vector(device_error, torch.int32, 1, dev, "device_error")
-    a.n_tokens, a.n_q_heads, a.rot_dim, a.interleaved = T, Hq, rot, int(interleaved)
-    a.in_dtype, a.eps = _DTYPES[q.dtype], eps
-    _call("moe_qk_norm_rope", dev, cache._ref, ctypes.byref(a), stream=stream)
+        q_out = _empty_on(shape, to, cache.device, stream)
+    a, b, c = _rows(q, shape, dt, dev, "q"), _rows(k, kv, dt, dev, "k"), _rows(v, kv, dt, dev, "v")
+    qo = _rows(q_out, shape, to, dev, "q_out")
+    i32 = torch.int32
+    args = _pack_norm_rope(
+        a[0], b[0], c[0], a[1], a[2], b[1], b[2], c[1], c[2], *qo,
+        _vector(q_weight, to, D, dev, "q_weight"), _vector(k_weight, to, D, dev, "k_weight"),
+        _vector(inv_freq, torch.float64, 1, dev, "inv_freq"),
+        _vector(positions, i32, T, dev, "positions"), _vector(slots, i32, T, dev, "slots"),
+        _vector(device_error, i32, 1, dev, "device_error"), T, Hq,
+        0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, _DTYPES[dt], eps)
+    _call("moe_qk_norm_rope", dev, stream, cache._c, args)
     return q_out
 
 
 def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream):
-    dev, D = cache.device, cache.head_dim
-    _need(q.dim() == 3 and q.dtype == cache.dtype, "q: [rows, heads, head_dim], the cache's dtype")
-    T, Hq = q.shape[0], q.shape[1]
-    if out is None:
-        out = _empty_on((T, Hq, D), q.dtype, dev, stream)
-    _need(out.dtype == cache.dtype and out.shape[0] == T, "out: as q")
+    dev, D, dt, i32 = cache._dev, cache.head_dim, cache.dtype, torch.int32
+    T, Hq, _ = shape = q.shape
     n, width = page_table.shape
-    _need(page_table.dtype == torch.int32 and page_table.device == dev
-          and (page_table.stride(1) == 1 or width == 1), "page_table: int32 [n_seqs, width]")
-    a = AttentionStruct()
-    a.q, a.q_row_stride, a.q_head_stride = _rows(q, Hq, D, dev, "q")
-    a.out, a.out_row_stride, a.out_head_stride = _rows(out, Hq, D, dev, "out")
-    a.cu_q = _vector(cu_q, torch.int32, n + 1, dev, "cu_q")
-    a.ctx_len = _vector(ctx_len, torch.int32, n, dev, "ctx_len")
-    a.page_table = page_table.data_ptr()
-    a.table_stride = page_table.stride(0) if n > 1 else width
-    a.table_width, a.n_seqs, a.n_rows, a.n_q_heads = width, n, T, Hq
-    a.scale = D ** -0.5 if scale is None else scale
-    a.device_error = _vector(device_error, torch.int32, 1, dev, "device_error")
-    return a, out
+    if shape[2] != D:
+        raise ValueError(f"q: heads of {D} are wanted")
+    if out is None:
+        out = _empty_on(shape, dt, cache.device, stream)
+    st = page_table.stride()
+    if page_table.dtype != i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
+        raise ValueError(f"page_table: int32 [n_seqs, width] on cuda:{dev} is wanted")
+    a, b = _rows(q, shape, dt, dev, "q"), _rows(out, shape, dt, dev, "out")
+    return _pack_attention(
+        a[0], b[0], a[1], a[2], b[1], b[2], _vector(cu_q, i32, n + 1, dev, "cu_q"),
+        _vector(ctx_len, i32, n, dev, "ctx_len"), page_table.data_ptr(), st[0] if n > 1 else width,
+        width, n, T, Hq, D ** -0.5 if scale is None else scale,
+        _vector(device_error, i32, 1, dev, "device_error")), out
 
 
 def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tree_mask=None,
@@ -656,22 +630,21 @@ def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tre
     sequence.  q [T, Hq, D]; cu_q int32 [n + 1]; ctx_len int32 [n]; page_table int32 [n, width];
     tree_mask int64 [T], bit j of a row: it sees drafted token j of its sequence (None: causal);
     scale None: 1 / sqrt(D).  workspace: uint8 tensor to use instead of a new one."""
-    a, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream)
-    mask = None
+    dev = cache._dev
+    args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
+                                stream)
+    mask = 0
     if tree_mask is not None:
-        _need(tree_mask.dtype in (torch.int64, torch.uint64), "tree_mask: 64-bit")
-        mask = _vector(tree_mask, tree_mask.dtype, q.shape[0], cache.device, "tree_mask")
-    n = ctypes.c_int64()
-    check("moe_tree_attention_workspace", lib().moe_tree_attention_workspace(
-        cache._ref, ctypes.byref(a), max_q, ctypes.byref(n)))
+        if tree_mask.dtype not in (torch.int64, torch.uint64):
+            raise ValueError("tree_mask: 64-bit integers are wanted")
+        mask = _vector(tree_mask, tree_mask.dtype, q.shape[0], dev, "tree_mask")
     if workspace is None:
-        workspace = _empty_on((n.value,), torch.uint8, cache.device, stream) if n.value else None
-    else:
-        _need(workspace.is_contiguous() and workspace.device == cache.device,
-              "workspace: contiguous, on the cache's device")
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call("moe_tree_attention", cache.device, cache._ref, ctypes.byref(a), mask, max_q,
-          _p(workspace), size, stream=stream)
+        n = ctypes.c_int64()
+        check("moe_tree_attention_workspace", _entry("moe_tree_attention_workspace")(
+            cache._c, args, max_q, ctypes.byref(n)))
+        workspace = _empty_on((n.value,), torch.uint8, cache.device, stream)
+    _call("moe_tree_attention", dev, stream, cache._c, args, mask, max_q,
+          _vector(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
     return out
 
 
@@ -679,6 +652,7 @@ def prompt_attention(cache: KvCache, q, cu_q, ctx_len, page_table, scale: float 
                      out=None, device_error=None, stream=None):
     """moe_prompt_attention: causal attention of packed prompts, or of chunks behind ctx_len cached
     positions; arguments as for tree_attention, without a limit on the rows of a sequence."""
-    a, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream)
-    _call("moe_prompt_attention", cache.device, cache._ref, ctypes.byref(a), stream=stream)
+    args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
+                                stream)
+    _call("moe_prompt_attention", cache._dev, stream, cache._c, args)
     return out

@@ -261,35 +261,6 @@ static cudaError_t launch_any(const moe_kv_cache *c, const Params &p, int max_q,
 
 }  // namespace attn
 
-extern "C" int moe_tree_attention_workspace(const moe_kv_cache *cache, const moe_attention *a,
-                                            int32_t max_q, int64_t *bytes) {
-  attn::Params p;
-  const int rc = attn::check_attention(cache, a, &p);
-  if (rc != MOE_OK) return rc;
-  if (max_q < 1 || !bytes) return MOE_ERR_INVALID_ARG;
-  if (max_q > MOE_TREE_MAX_Q) return MOE_ERR_UNSUPPORTED;
-  *bytes = 0;
-  return MOE_OK;
-}
-
-extern "C" int moe_tree_attention(const moe_kv_cache *cache, const moe_attention *a,
-                                  const uint64_t *tree_mask, int32_t max_q, void *workspace,
-                                  int64_t workspace_bytes, void *stream) {
-  attn::Params p;
-  const int rc = attn::check_attention(cache, a, &p);
-  if (rc != MOE_OK) return rc;
-  if (max_q < 1 || !attn::aligned(tree_mask, 8) || workspace_bytes < 0 ||
-      !attn::aligned(workspace, 16))
-    return MOE_ERR_INVALID_ARG;
-  if (max_q > MOE_TREE_MAX_Q || p.n_seqs > 65535 || p.hkv > 65535) return MOE_ERR_UNSUPPORTED;
-  if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
-  p.mask = tree_mask;
-  p.max_q = max_q;
-  return attn::launch_any(cache, p, max_q, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
-}
-
 extern "C" int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *a,
                                     void *stream) {
   attn::Params p;

@@ -50,6 +50,13 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int s, bool report) {
   return r;
 }
 
+__device__ __forceinline__ void pdl_launch() {  // the next kernel may be set up
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {  // the kernel before this one has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -1,0 +1,512 @@
+// moe_tree.cu -- attention of decoded tokens, or of trees of drafted tokens, over the pages of a
+// cache (moe_tree_attention).
+//
+//   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
+//   that row r sees, m_r their largest score: one pass over K and V with the running maximum and
+//   sum; what was summed before a larger maximum is scaled down to it.
+//
+// Bound by the bytes of K and V, so what matters is that every SM streams all the time, whatever
+// the lengths are.  An item is one sequence, one key/value head and one tile of rows (row R is query
+// R / group, head R % group); its positions are cut into tiles of 64.  All tiles of all items, in
+// order, form one line that the CTAs share evenly: CTA c takes the tiles [c W / G, (c + 1) W / G).
+// The lengths are read on the device, so a captured graph balances whatever it is replayed on.  An
+// item that ends up in one CTA is written by it; one that several CTAs share leaves its partial
+// maxima, sums and outputs in the workspace, and join_kernel adds them in order.
+//
+// A CTA is four warps over 16 WR rows: WR warps split the rows, 4 / WR warps the positions of a
+// tile, so a single decoded token (group <= 16 rows) still uses all four.
+#include <algorithm>
+
+#include "moe_attention.cuh"
+
+namespace attn {
+
+constexpr int kTile = 64;  // positions of a tile
+constexpr int kThreads = 128;
+
+template <int D>
+struct Tree {
+  // 16 or 32 KB a stage; with two CTAs an SM there are 96 to 128 KB in flight, more than the 35 KB
+  // that latency times bandwidth asks for
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSmem = kStages * 2 * kTileBytes;
+};
+constexpr int kCtasPerSm = 2;
+constexpr int kMinTiles = 4;  // tiles that a CTA takes at least: below it joining costs more
+
+// What one CTA leaves for join_kernel: the item that begins in it and goes on in the next ones.
+struct Shared {
+  int pieces;  // CTAs that hold a part; 0: nothing to join
+  int row0;    // the sequence's first row
+  int kvh, R0, rows;
+  int slot;    // 0 or 1: which of its CTA's parts is its first
+};
+
+struct Work {
+  Params p;
+  float *part;      // [2 G][ROWS][D] partial outputs: slot 2c the CTA's first item, 2c + 1 its last
+  float2 *part_ml;  // [2 G][ROWS] (maximum, sum)
+  Shared *shared;   // [G]
+};
+
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {  // byte offset in a [64][D] tile
+  return static_cast<uint32_t>(row * D * 2 + ((chunk ^ (row & 7)) << 4));
+}
+
+// The pages of a tile's four quarters (a page has at least 16 positions); -1: nothing there.
+__device__ __forceinline__ void load_pages(const Params &p, const int32_t *pages, int len, int tile,
+                                           int (&pg)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int pos = tile * kTile + 16 * e;
+    pg[e] = pos < len ? pages[pos >> p.page_shift] : -1;
+  }
+}
+
+// Copies positions [64 t, 64 t + 64) of K and V into shared memory; rows past the sequence and on
+// a page outside the cache are zeros (what stale pages hold, NaN included, is never multiplied).
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(const Params &p, int len, const int (&pg)[4],
+                                          int64_t head_off, int tile, uint32_t k_smem,
+                                          uint32_t v_smem) {
+  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
+  const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+#pragma unroll
+  for (int i = 0; i < kTile / kStep; ++i) {
+    const int r = r0 + i * kStep, pos = tile * kTile + r;
+    const int page = pg[i * kStep / 16];
+    const bool valid = pos < len && static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+    const int64_t off = valid ? page * p.page_stride + head_off +
+                                    (pos & ((1 << p.page_shift) - 1)) * p.tok_stride + 8 * c
+                              : 0;
+    const uint32_t d = swizzled<D>(r, c);
+    cp_async16(k_smem + d, static_cast<const T *>(p.k) + off, valid);
+    cp_async16(v_smem + d, static_cast<const T *>(p.v) + off, valid);
+  }
+  if (threadIdx.x < 4) {  // a used page outside the cache is reported
+    const int page = threadIdx.x == 0 ? pg[0] : threadIdx.x == 1 ? pg[1] : threadIdx.x == 2 ? pg[2]
+                                                                                            : pg[3];
+    if (tile * kTile + 16 * static_cast<int>(threadIdx.x) < len &&
+        static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages) && p.err)
+      atomicOr(p.err, kDevErrBadId);
+  }
+}
+
+// Sums v over the block (every thread gets the sum) and gives each thread the sum before it.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_t *before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += s_warp[w];
+    all += s_warp[w];
+  }
+  *before = base + x - v;
+  return all;
+}
+
+template <typename T, int D, int WR>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w) {
+  constexpr int ROWS = 16 * WR, WT = 4 / WR, TW = kTile / WT;  // TW positions of a warp per tile
+  constexpr int kStages = Tree<D>::kStages, kTileBytes = Tree<D>::kTileBytes;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[4][16], s_l[4][16];
+  __shared__ int64_t s_warp[4], s_before;
+  __shared__ int s_seq;
+  const Params &p = w.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+  const int wr = warp % WR, wt = warp / WR;
+
+  pdl_launch();
+  // all tiles, and the sequence in which this CTA's part of them begins
+  const auto weight = [&](const Seq &s) {
+    const int64_t rt = (static_cast<int64_t>(s.nq) * p.group + ROWS - 1) / ROWS;
+    return rt * p.hkv * ((s.len + kTile - 1) / kTile);
+  };
+  const bool first_cta = blockIdx.x == 0;
+  int64_t total = 0, before, mine = 0;
+  for (int b = 0; b < p.n_seqs; b += kThreads) {
+    const int i = b + threadIdx.x;
+    mine = i < p.n_seqs ? weight(load_seq(p, i, first_cta)) : 0;
+    total += block_scan(mine, s_warp, &before);
+  }
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
+  if (threadIdx.x == 0) w.shared[blockIdx.x].pieces = 0;
+  if (blockIdx.x >= ctas) return;
+  int64_t at = blockIdx.x * total / ctas;
+  const int64_t end = (blockIdx.x + 1) * total / ctas;
+  if (p.n_seqs <= kThreads) {
+    if (before <= at && at < before + mine) s_seq = threadIdx.x, s_before = before;
+  } else {
+    int64_t sum = 0;
+    for (int b = 0; sum <= at; b += kThreads) {
+      const int i = b + threadIdx.x;
+      mine = i < p.n_seqs ? weight(load_seq(p, i, false)) : 0;
+      const int64_t all = block_scan(mine, s_warp, &before);
+      before += sum;
+      if (before <= at && at < before + mine) s_seq = i, s_before = before;
+      sum += all;
+    }
+  }
+  __syncthreads();
+  int seq = s_seq;
+  int64_t seq_at = s_before;  // tiles before the sequence
+  const int64_t begin = at;
+
+  const uint32_t base = smem_u32(smem);
+  Seq s = load_seq(p, seq, false);
+  while (at < end) {
+    while (at >= seq_at + weight(s)) {
+      seq_at += weight(s);
+      if (++seq >= p.n_seqs) return;  // never, unless the lengths change under the kernel
+      s = load_seq(p, seq, false);
+    }
+    const int nt = (s.len + kTile - 1) / kTile;
+    const int item = static_cast<int>((at - seq_at) / nt);  // (head, row tile)
+    const int rts = (s.nq * p.group + ROWS - 1) / ROWS;
+    const int kvh = item / rts, R0 = (item - kvh * rts) * ROWS, rows = s.nq * p.group;
+    const int64_t item_at = seq_at + static_cast<int64_t>(item) * nt;
+    const int t0 = static_cast<int>(at - item_at);
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(nt), end - item_at));
+    const int32_t *pages = p.table + seq * p.table_stride;
+    const int64_t head_off = kvh * p.head_stride;
+
+    int pg[kStages][4];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) load_pages(p, pages, s.len, t0 + i, pg[i]);
+    // this lane's two rows: queries, heads, masks
+    int row_q[2];
+    uint64_t row_mask[2];
+    bool row_ok[2];
+    const uint32_t *qp[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int R = R0 + wr * 16 + g + 8 * h;
+      row_ok[h] = R < rows;
+      row_q[h] = row_ok[h] ? R / p.group : 0;
+      const int head = kvh * p.group + (row_ok[h] ? R - row_q[h] * p.group : 0);
+      qp[h] = reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) +
+                                                 (s.row0 + row_q[h]) * p.q_row + head * p.q_head);
+      // without masks: bits 0 .. query
+      row_mask[h] = p.mask ? p.mask[s.row0 + row_q[h]] : ~0ull >> (63 - row_q[h]);
+    }
+    uint32_t qa[D / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][0] = row_ok[0] ? qp[0][8 * kk + q4] : 0u;
+      qa[kk][1] = row_ok[1] ? qp[1][8 * kk + q4] : 0u;
+      qa[kk][2] = row_ok[0] ? qp[0][8 * kk + 4 + q4] : 0u;
+      qa[kk][3] = row_ok[1] ? qp[1][8 * kk + 4 + q4] : 0u;
+    }
+
+    float o[D / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+    // tile t waits in stage (t - t0) % kStages; the pages of a tile are read one tile ahead
+    const auto issue = [&](int t, const int (&page)[4]) {
+      if (t < t1) {
+        const uint32_t st = base + ((t - t0) % kStages) * 2 * kTileBytes;
+        load_tile<T, D>(p, s.len, page, head_off, t, st, st + kTileBytes);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(t0 + i, pg[i]);
+    int (&next)[4] = pg[kStages - 1];
+    for (int t = t0; t < t1; ++t) {
+      cp_async_wait<kStages - 2>();
+      __syncthreads();  // tile t is there, and every warp is done with tile t - 1
+      issue(t + kStages - 1, next);
+      load_pages(p, pages, s.len, t + kStages, next);
+      const uint32_t ks = base + ((t - t0) % kStages) * 2 * kTileBytes, vs = ks + kTileBytes;
+
+      float sc[TW / 8][4];
+#pragma unroll
+      for (int j = 0; j < TW / 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int j = 0; j < TW / 16; ++j) {
+          uint32_t b[4];
+          const int mi = lane >> 3;
+          ldmatrix_x4(b, ks + swizzled<D>(wt * TW + 16 * j + (lane & 7) + 8 * (mi >> 1),
+                                          2 * kk + (mi & 1)));
+          Half<T>::mma(sc[2 * j], qa[kk], b[0], b[1]);
+          Half<T>::mma(sc[2 * j + 1], qa[kk], b[2], b[3]);
+        }
+      if ((t + 1) * kTile > s.ctx) {  // drafted positions, and those behind the sequence
+        const int pos0 = t * kTile + wt * TW + 2 * q4;
+#pragma unroll
+        for (int j = 0; j < TW / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d = pos0 + 8 * j + (e & 1) - s.ctx;
+            if (d >= 0 && (d >= s.nq || !((row_mask[e >> 1] >> d) & 1))) sc[j][e] = kNegInf;
+          }
+      }
+      float scale[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = m[h];
+#pragma unroll
+        for (int j = 0; j < TW / 8; ++j) top = fmaxf(top, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float ref = top == kNegInf ? 0.f : top;  // no position seen so far
+        scale[h] = exp2_approx((m[h] - ref) * p.scale_log2);
+        m[h] = top;
+        const float off = ref * p.scale_log2;
+        float add = 0.f;
+#pragma unroll
+        for (int j = 0; j < TW / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = exp2_approx(fmaf(sc[j][2 * h + e], p.scale_log2, -off));
+            sc[j][2 * h + e] = x;
+            add += x;
+          }
+        l[h] = l[h] * scale[h] + add;
+      }
+      if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= scale[0], o[j][1] *= scale[0];
+          o[j][2] *= scale[1], o[j][3] *= scale[1];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TW / 16; ++j) {
+        // p enters the product in the cache's type (as v is): half a step of it relative to p, the
+        // size of the output's own rounding
+        const uint32_t a[4] = {Half<T>::pack(sc[2 * j][0], sc[2 * j][1]),
+                               Half<T>::pack(sc[2 * j][2], sc[2 * j][3]),
+                               Half<T>::pack(sc[2 * j + 1][0], sc[2 * j + 1][1]),
+                               Half<T>::pack(sc[2 * j + 1][2], sc[2 * j + 1][3])};
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t b[4];
+          const int mi = lane >> 3;
+          ldmatrix_x4_trans(b, vs + swizzled<D>(wt * TW + 16 * j + (lane & 7) + 8 * (mi & 1),
+                                                2 * d + (mi >> 1)));
+          Half<T>::mma(o[2 * d], a, b[0], b[1]);
+          Half<T>::mma(o[2 * d + 1], a, b[2], b[3]);
+        }
+      }
+    }
+
+    // join the warps that split the positions, and the rows' sums over their four lanes
+    cp_async_wait<0>();
+    __syncthreads();
+    float *s_o = reinterpret_cast<float *>(smem);  // [4][16][D]
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int r = g + 8 * h;
+      if (q4 == 0) s_m[warp][r] = m[h], s_l[warp][r] = l[h];
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<float2 *>(s_o + (warp * 16 + r) * D + 8 * j + 2 * q4) =
+            make_float2(o[j][2 * h], o[j][2 * h + 1]);
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == nt;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (at == begin ? 0 : 1);
+    if (threadIdx.x == 0 && t0 == 0 && t1 < nt) {
+      Shared &r = w.shared[blockIdx.x];
+      r.pieces = static_cast<int>(((item_at + nt) * ctas - 1) / total) - blockIdx.x + 1;
+      r.row0 = s.row0, r.kvh = kvh, r.R0 = R0, r.rows = rows, r.slot = at == begin ? 0 : 1;
+    }
+    for (int i = threadIdx.x; i < ROWS * D / 8; i += kThreads) {
+      const int r = i / (D / 8), c = i % (D / 8), R = R0 + r;
+      if (R >= rows) break;
+      float top = kNegInf;
+#pragma unroll
+      for (int v = 0; v < WT; ++v) top = fmaxf(top, s_m[v * WR + r / 16][r % 16]);
+      const float ref = top == kNegInf ? 0.f : top;
+      float total_l = 0.f, x[8] = {};
+#pragma unroll
+      for (int v = 0; v < WT; ++v) {
+        const int ww = v * WR + r / 16;
+        const float f = exp2_approx((s_m[ww][r % 16] - ref) * p.scale_log2);
+        total_l += f * s_l[ww][r % 16];
+        const float *src = s_o + (ww * 16 + r % 16) * D + 8 * c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(f, src[e], x[e]);
+      }
+      if (whole) {
+        const float inv = total_l > 0.f ? 1.f / total_l : 0.f;  // a row that sees nothing is zeros
+        const int tok = R / p.group, head = kvh * p.group + R - tok * p.group;
+        uint4 v;
+        v.x = Half<T>::pack(x[0] * inv, x[1] * inv);
+        v.y = Half<T>::pack(x[2] * inv, x[3] * inv);
+        v.z = Half<T>::pack(x[4] * inv, x[5] * inv);
+        v.w = Half<T>::pack(x[6] * inv, x[7] * inv);
+        *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (s.row0 + tok) * p.o_row +
+                                   head * p.o_head + 8 * c) = v;
+      } else {
+        float4 *dst = reinterpret_cast<float4 *>(w.part + (slot * ROWS + r) * D + 8 * c);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (c == 0) w.part_ml[slot * ROWS + r] = make_float2(top, total_l);
+      }
+    }
+    __syncthreads();  // the next item's tiles go where s_o is
+    at = item_at + t1;
+  }
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x and ends in a later one; a warp takes a
+// row.  The parts are added in the order of the positions: repeat calls give the same bytes.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) join_kernel(const Work w) {
+  const Params &p = w.p;
+  pdl_wait();
+  const Shared sh = w.shared[blockIdx.x];
+  const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int R = sh.R0 + r;
+  if (sh.pieces == 0 || R >= sh.rows) return;
+  const int64_t c0 = blockIdx.x;
+  const int64_t first = 2 * c0 + sh.slot;
+  const auto slot = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
+  float top = kNegInf;
+  for (int i = lane; i < sh.pieces; i += 32) top = fmaxf(top, w.part_ml[slot(i) * ROWS + r].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == kNegInf ? 0.f : top;
+  constexpr int V = D / 32;
+  float x[V] = {}, sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < sh.pieces; ++i) {
+    const int64_t at = slot(i) * ROWS + r;
+    const float2 ml = w.part_ml[at];
+    const float f = exp2_approx((ml.x - ref) * p.scale_log2);
+    sum = fmaf(f, ml.y, sum);
+    const float *src = w.part + at * D + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = fmaf(f, src[e], x[e]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int tok = R / p.group, head = sh.kvh * p.group + R - tok * p.group;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (sh.row0 + tok) * p.o_row +
+                                               head * p.o_head + V * lane);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) dst[e] = Half<T>::pack(x[2 * e] * inv, x[2 * e + 1] * inv);
+}
+
+struct Plan {
+  int grid, rows;  // CTAs, rows of a tile
+  int64_t part, ml, shared, bytes;  // offsets in the workspace
+};
+
+static int make_plan(const moe_kv_cache *c, const Params &p, int max_q, Plan *plan) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(max_q) * p.group;
+  plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  // no more CTAs than the largest batch that the arguments allow has work for
+  const int64_t len = (static_cast<int64_t>(p.table_width) << p.page_shift) / kTile + 1;
+  const int64_t items =
+      (static_cast<int64_t>(p.n_rows) * p.group / plan->rows + p.n_seqs) * p.hkv;
+  const int64_t most = len >= INT32_MAX || items >= INT32_MAX ? INT64_MAX : items * len;
+  plan->grid = static_cast<int>(std::min<int64_t>(sms * kCtasPerSm, most / kMinTiles + 1));
+  plan->part = 0;
+  plan->ml = plan->part + 8ll * plan->grid * plan->rows * c->head_dim;
+  plan->shared = plan->ml + 16ll * plan->grid * plan->rows;
+  plan->bytes = plan->shared + static_cast<int64_t>(sizeof(Shared)) * plan->grid;
+  return MOE_OK;
+}
+
+template <typename T, int D, int WR>
+static cudaError_t launch(const Work &w, int grid, cudaStream_t stream) {
+  const auto kern = tree_kernel<T, D, WR>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tree<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the joining blocks are set up while the kernel runs and wait for its end
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 16 * WR / (kThreads / 32));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, 16 * WR>, w);
+}
+
+template <typename T, int D>
+static cudaError_t launch_rows(const Work &w, const Plan &plan, cudaStream_t stream) {
+  if (plan.rows == 16) return launch<T, D, 1>(w, plan.grid, stream);
+  if (plan.rows == 32) return launch<T, D, 2>(w, plan.grid, stream);
+  return launch<T, D, 4>(w, plan.grid, stream);
+}
+
+}  // namespace attn
+
+extern "C" int moe_tree_attention_workspace(const moe_kv_cache *cache, const moe_attention *a,
+                                            int32_t max_q, int64_t *bytes) {
+  attn::Params p;
+  int rc = attn::check_attention(cache, a, &p);
+  if (rc != MOE_OK) return rc;
+  if (max_q < 1 || !bytes) return MOE_ERR_INVALID_ARG;
+  if (max_q > MOE_TREE_MAX_Q) return MOE_ERR_UNSUPPORTED;
+  if (p.n_seqs == 0 || p.n_rows == 0) {
+    *bytes = 0;
+    return MOE_OK;
+  }
+  attn::Plan plan;
+  rc = attn::make_plan(cache, p, max_q, &plan);
+  if (rc == MOE_OK) *bytes = plan.bytes;
+  return rc;
+}
+
+extern "C" int moe_tree_attention(const moe_kv_cache *cache, const moe_attention *a,
+                                  const uint64_t *tree_mask, int32_t max_q, void *workspace,
+                                  int64_t workspace_bytes, void *stream) {
+  attn::Work w;
+  int rc = attn::check_attention(cache, a, &w.p);
+  if (rc != MOE_OK) return rc;
+  if (max_q < 1 || !attn::aligned(tree_mask, 8) || workspace_bytes < 0 ||
+      !attn::aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (max_q > MOE_TREE_MAX_Q) return MOE_ERR_UNSUPPORTED;
+  if (w.p.n_seqs == 0 || w.p.n_rows == 0) return MOE_OK;
+  attn::Plan plan;
+  rc = attn::make_plan(cache, w.p, max_q, &plan);
+  if (rc != MOE_OK) return rc;
+  if (!workspace || workspace_bytes < plan.bytes) return MOE_ERR_INVALID_ARG;
+  w.p.mask = tree_mask;
+  w.p.max_q = max_q;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  w.part = reinterpret_cast<float *>(ws + plan.part);
+  w.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
+  w.shared = reinterpret_cast<attn::Shared *>(ws + plan.shared);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == MOE_DTYPE_BF16)
+    e = cache->head_dim == 64 ? attn::launch_rows<__nv_bfloat16, 64>(w, plan, st)
+                              : attn::launch_rows<__nv_bfloat16, 128>(w, plan, st);
+  else
+    e = cache->head_dim == 64 ? attn::launch_rows<__half, 64>(w, plan, st)
+                              : attn::launch_rows<__half, 128>(w, plan, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

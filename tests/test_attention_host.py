@@ -10,6 +10,30 @@ from quantized_moe_expert_dequant_gb300 import binding as Bn
 INV, UNS = Bn.MOE_ERR_INVALID_ARG, Bn.MOE_ERR_UNSUPPORTED
 
 
+def _struct(*groups):
+    return type("Struct", (ctypes.Structure,), {"_fields_": [
+        (n, t) for names, t in groups for n in names.split()]})
+
+
+# the structs as the header declares them, field by field
+KvCacheStruct = _struct(("k v", ctypes.c_void_p),
+                        ("page_stride head_stride token_stride", ctypes.c_int64),
+                        ("n_pages page_size n_kv_heads head_dim dtype", ctypes.c_int32))
+NormRopeStruct = _struct(
+    ("q k v", ctypes.c_void_p),
+    ("q_row_stride q_head_stride k_row_stride k_head_stride v_row_stride v_head_stride",
+     ctypes.c_int64), ("q_out", ctypes.c_void_p),
+    ("q_out_row_stride q_out_head_stride", ctypes.c_int64),
+    ("q_weight k_weight inv_freq positions slots device_error", ctypes.c_void_p),
+    ("n_tokens n_q_heads rot_dim interleaved in_dtype", ctypes.c_int32), ("eps", ctypes.c_float))
+AttentionStruct = _struct(
+    ("q out", ctypes.c_void_p),
+    ("q_row_stride q_head_stride out_row_stride out_head_stride", ctypes.c_int64),
+    ("cu_q ctx_len page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+    ("table_width n_seqs n_rows n_q_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+    ("device_error", ctypes.c_void_p))
+
+
 @pytest.fixture(scope="module")
 def L():
     import __graft_entry__
@@ -21,7 +45,7 @@ def cache(**kw):
     base = dict(k=0x1000, v=0x2000, page_stride=8192, head_stride=1024, token_stride=64, n_pages=4,
                 page_size=16, n_kv_heads=8, head_dim=64, dtype=Bn.DTYPE_BF16)
     base.update(kw)
-    return Bn.KvCacheStruct(**base)
+    return KvCacheStruct(**base)
 
 
 def rope(**kw):
@@ -29,14 +53,14 @@ def rope(**kw):
                 inv_freq=0x7000, n_tokens=1, n_q_heads=8, rot_dim=64, interleaved=0,
                 in_dtype=Bn.DTYPE_F32, eps=1e-6)
     base.update(kw)
-    return Bn.NormRopeStruct(**base)
+    return NormRopeStruct(**base)
 
 
 def attention(**kw):
     base = dict(q=0x1000, out=0x2000, cu_q=0x3000, ctx_len=0x4000, page_table=0x5000,
                 table_stride=4, table_width=4, n_seqs=1, n_rows=1, n_q_heads=8, scale=0.125)
     base.update(kw)
-    return Bn.AttentionStruct(**base)
+    return AttentionStruct(**base)
 
 
 BAD_CACHE = [
@@ -133,3 +157,13 @@ def test_the_binding_checks_tensors():
     meta = torch.zeros((2, 2, 16, 64), dtype=torch.bfloat16, device="meta")
     with pytest.raises(ValueError):
         Bn.KvCache(meta, meta)
+
+
+@pytest.mark.parametrize("pack,S", [(Bn._pack_kv_cache, KvCacheStruct),
+                                    (Bn._pack_norm_rope, NormRopeStruct),
+                                    (Bn._pack_attention, AttentionStruct)])
+def test_packed_bytes_have_the_layout_of_the_struct(pack, S):
+    vals = [i + 1 for i in range(len(S._fields_))]
+    b = pack(*vals)
+    s = S.from_buffer_copy(b + bytes(max(0, ctypes.sizeof(S) - len(b))))
+    assert [getattr(s, n) for n, _ in S._fields_] == vals
