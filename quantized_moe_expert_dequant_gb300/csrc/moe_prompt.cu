@@ -240,74 +240,89 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else if (warp == kSoftmaxWarps) {
     // ---------------------------------------------------------------- products
-    constexpr uint32_t i_s = tc::instr(std::is_same<T, __nv_bfloat16>::value, false,
-                                       128, kPos);
-    constexpr uint32_t i_o = tc::instr(std::is_same<T, __nv_bfloat16>::value, true, 128, D);
-    const int n[2] = {n0, n1};
-    const auto issue_s = [&](int i, uint32_t k) {  // lane 0
+    // Everything here is the same for all lanes (the shuffles say so to the compiler); `one` issues.
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t i_s = tc::instr(kBf16, false, 128, kPos);
+    constexpr uint32_t i_o = tc::instr(kBf16, true, 128, D);
+    constexpr uint32_t hi = tc::desc_hi(1024);
+    const auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t one = tc::elect();
+    const uint32_t tm = uniform(tmem), ub = uniform(base);
+    const int u0 = uniform(n0), u1 = uniform(n1), last = uniform(steps), len = uniform(s.len);
+    const uint32_t q_lo = tc::desc_lo(ub, 16);
+    int st = 0, phase = 0;  // the ring's next stage
+    const auto wait = [&](uint32_t b, int parity) {
+      return __all_sync(0xffffffffu, tc::bar_wait(b, parity, &s_gone)) != 0;
+    };
+    const auto stage = [&](int i) { return ub + (2 + i) * C::kTileBytes; };
+    const auto issue_s = [&](int i, uint32_t k) {
+      const uint32_t k_lo = tc::desc_lo(k, 16);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * kPos * 128 + (kk % 4) * 32;
-        tc::mma_smem(tmem + i * kPos, tc::smem_desc(base + i * C::kTileBytes + off, 16, 1024),
-                     tc::smem_desc(k + off, 16, 1024), i_s, kk > 0);
+        const uint32_t off = ((kk / 4) * kPos * 128 + (kk % 4) * 32) / 16;
+        tc::mma_smem(one, tm + i * kPos, q_lo + i * (C::kTileBytes / 16) + off, hi, k_lo + off, hi,
+                     i_s, kk > 0);
       }
-      tc::mma_commit(bar(s_s[i]));
+      tc::mma_commit(one, bar(s_s[i]));
     };
-    const auto full = [&](int it) {
-      return tc::bar_wait(bar(s_full[it % C::kStages]), (it / C::kStages) & 1, &s_gone);
+    const auto next = [&]() {
+      if (++st == C::kStages) st = 0, phase ^= 1;
     };
-    const auto at = [&](int it) { return ring + (it % C::kStages) * C::kTileBytes; };
-    bool ok = tc::bar_wait(bar(s_q[0]), 0, &s_gone) && full(0);
-    if (ok && lane == 0) issue_s(0, at(0));
-    if (ok && n1 > 0) {
-      ok = tc::bar_wait(bar(s_q[1]), 0, &s_gone);
-      if (ok && lane == 0) issue_s(1, at(0));
+    bool ok = wait(bar(s_q[0]), 0) && wait(bar(s_full[0]), 0);
+    if (ok) issue_s(0, stage(0));
+    if (ok && u1 > 0) {
+      ok = wait(bar(s_q[1]), 0);
+      if (ok) issue_s(1, stage(0));
     }
-    if (ok && lane == 0) tc::mma_commit(bar(s_empty[0]));
-    ok = __all_sync(0xffffffffu, ok);
-    for (int t = 0; ok && t < steps; ++t) {
-      const int vi = 2 * t + 1, ki = 2 * t + 2;
-      ok = full(vi);
-      const int valid = s.len - t * kPos;
+    if (ok) tc::mma_commit(one, bar(s_empty[0]));
+    next();
+    for (int t = 0; ok && t < last; ++t) {
+      const int v_st = st, v_phase = phase;
+      next();
+      const int k_st = st, k_phase = phase;
+      next();
+      const uint32_t v = stage(v_st);
+      ok = wait(bar(s_full[v_st]), v_phase);
+      const int valid = len - t * kPos;
       if (valid < kPos) {
         // positions behind the sequence have weight 0, but what their page holds may be NaN
         for (int x = valid * 128 + lane * 16; x < kPos * 128; x += 512)
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(vi) + h * kPos * 128 + x),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * kPos * 128 + x),
                          "r"(0)
                          : "memory");
         tc::fence_async_proxy();
         __syncwarp();
       }
+      const uint32_t v_lo = tc::desc_lo(v, kPos * 128);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (ok && t < n[i]) {
-          ok = tc::bar_wait(bar(s_p[i]), t & 1, &s_gone);
+        const int n = i ? u1 : u0;
+        if (ok && t < n) {
+          ok = wait(bar(s_p[i]), t & 1);
           tc::fence_after();
-          if (ok && lane == 0) {
+          if (ok) {
 #pragma unroll
             for (int kk = 0; kk < kPos / 16; ++kk)
-              tc::mma_tmem(tmem + 2 * kPos + i * D, tmem + i * kPos + kk * 8,
-                           tc::smem_desc(at(vi) + kk * 2048, kPos * 128, 1024), i_o,
-                           t > 0 || kk > 0);
-            if (t == n[i] - 1) tc::mma_commit(bar(s_o[i]));
+              tc::mma_tmem(one, tm + 2 * kPos + i * D, tm + i * kPos + kk * 8, v_lo + kk * 128, hi,
+                           i_o, t > 0 || kk > 0);
+            if (t == n - 1) tc::mma_commit(one, bar(s_o[i]));
           }
         }
-        if (ok && t + 1 < n[i]) {
-          ok = full(ki);
-          if (ok && lane == 0) issue_s(i, at(ki));
+        if (ok && t + 1 < n) {
+          ok = wait(bar(s_full[k_st]), k_phase);
+          if (ok) issue_s(i, stage(k_st));
         }
       }
-      if (ok && lane == 0) {
-        tc::mma_commit(bar(s_empty[vi % C::kStages]));
-        if (t + 1 < steps) tc::mma_commit(bar(s_empty[ki % C::kStages]));
+      if (ok) {
+        tc::mma_commit(one, bar(s_empty[v_st]));
+        if (t + 1 < last) tc::mma_commit(one, bar(s_empty[k_st]));
       }
-      ok = __all_sync(0xffffffffu, ok);  // the lanes leave together
     }
     if (s_gone) {  // let the products under way end before TMEM goes
       volatile int never = 0;
-      if (lane == 0) tc::mma_commit(bar(s_end));
+      tc::mma_commit(one, bar(s_end));
       tc::bar_wait(bar(s_end), 0, &never);
     }
   } else if (warp < kSoftmaxWarps) {
@@ -343,12 +358,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int e = 0; e < 32; ++e)
             if (32 * c + e >= see) x[c][e] = __float_as_uint(kNegInf);
       }
-      float top = kNegInf;
+      float tops[4];  // four chains: one of 64 dependent maxima took 500 cycles
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
+        tops[c] = kNegInf;
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
-          top = fmaxf(top, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+          tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+      }
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       // every row sees position 0, so after the first step m is finite
       const float up = fmaxf(m, top);
       if (t == 0) {

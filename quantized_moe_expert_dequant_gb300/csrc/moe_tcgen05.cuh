@@ -157,28 +157,48 @@ __device__ __forceinline__ void regs_down() {
 }
 
 // ------------------------------------------------------------------ the matrix product
-// D[128 x N] (+)= A[128 x 16] B[16 x N], 16-bit inputs of one type, fp32 in TMEM.
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool add) {
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one;
+}
+
+// D[128 x N] (+)= A[128 x 16] B[16 x N], 16-bit inputs of one type, fp32 in TMEM.  The whole warp
+// executes these with uniform arguments and one lane issues: inside a branch that one lane takes,
+// every descriptor would be moved to the uniform registers by itself, about 100 cycles a product
+// (measured), more than the product takes.
+__device__ __forceinline__ void mma_smem(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t a_hi,
+                                         uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(add)),
+      "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                         bool add) {
+__device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, uint32_t b_lo,
+                                         uint32_t b_hi, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(one)
       : "memory");
 }
-// The barrier gets one arrival when every product that this thread has issued is complete.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
+// The barrier gets one arrival when every product that this lane has issued is complete.
+__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(one)
+      : "memory");
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B of one type, A with K innermost.
@@ -189,9 +209,13 @@ __host__ __device__ constexpr uint32_t instr(bool bf16, bool b_n_innermost, int 
 // Shared-memory descriptor with the 128-byte swizzle (version 1 of the format; layout type 2).
 //   K innermost: rows of 128 bytes in groups of 8 (1024 bytes) `stride` apart; `lead` unused
 //   N innermost: 64-element blocks of N `lead` apart, groups of 8 k `stride` apart
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low word holds the address and `lead`, the high word the rest; the low word of an address x
+// bytes further (inside 256 KB) is x / 16 more.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
+}
+__device__ constexpr uint32_t desc_hi(uint32_t stride) {
+  return (stride >> 4) | (1u << 14) | (2u << 29);
 }
 
 // ------------------------------------------------------------------ host: tensor maps
