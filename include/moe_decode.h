@@ -388,8 +388,13 @@ int moe_tree_attention(const moe_kv_cache *cache, const moe_attention *args,
                        int64_t workspace_bytes, void *stream);
 
 /* Whole prompts, or chunks of them behind ctx_len cached positions, packed one after the other:
- * causal, query i of a sequence sees the positions 0 .. ctx_len + i. */
-int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, void *stream);
+ * causal, query i of a sequence sees the positions 0 .. ctx_len + i.  workspace as for
+ * moe_tree_attention, of moe_prompt_attention_workspace bytes (0 for short page tables; then NULL
+ * will do). */
+int moe_prompt_attention_workspace(const moe_kv_cache *cache, const moe_attention *args,
+                                   int64_t *bytes);
+int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, void *workspace,
+                         int64_t workspace_bytes, void *stream);
 
 /* ---- canonical packing (host) ---------------------------------------------------------------
  * codes: uint8 [rows][cols], one code per byte, each < 2^bits; packed: [rows][cols*bits/8].

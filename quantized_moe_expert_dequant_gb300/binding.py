@@ -44,7 +44,7 @@ EXPORTS = ["moe_decode_create", "moe_decode_forward", "moe_decode_get_error", "m
            "moe_synth_codes", "moe_synth_scales", "moe_synth_biases", "moe_route_invert_device",
            "moe_debug_wait_timeout", "moe_router_topk", "moe_debug_col_pieces",
            "moe_debug_col_plan", "moe_qk_norm_rope", "moe_tree_attention_workspace",
-           "moe_tree_attention", "moe_prompt_attention"]
+           "moe_tree_attention", "moe_prompt_attention_workspace", "moe_prompt_attention"]
 
 
 class MoeError(RuntimeError):
@@ -136,7 +136,8 @@ def lib() -> ctypes.CDLL:
                 "moe_qk_norm_rope": [vp, vp, vp],
                 "moe_tree_attention_workspace": [vp, vp, i32, vp],
                 "moe_tree_attention": [vp, vp, vp, i32, vp, i64, vp],
-                "moe_prompt_attention": [vp, vp, vp],
+                "moe_prompt_attention_workspace": [vp, vp, vp],
+                "moe_prompt_attention": [vp, vp, vp, i64, vp],
             }
             if _timeline:
                 sig["moe_stack_timeline"] = [vp, vp, i64, ctypes.POINTER(i32)]
@@ -623,6 +624,21 @@ def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_erro
         _vector(device_error, i32, 1, dev, "device_error")), out
 
 
+def _workspace(fn: str, cache, workspace, stream, *args):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one as large as fn says."""
+    if workspace is None:
+        n = ctypes.c_int64()
+        rc = _entry(fn)(cache._c, *args, ctypes.byref(n))
+        if rc != MOE_OK:
+            raise MoeError(fn, rc)
+        if n.value == 0:
+            return 0, 0, None
+        workspace = _empty_on(n.value, torch.uint8, cache.device, stream)
+        return workspace.data_ptr(), n.value, workspace
+    n = workspace.numel()
+    return _vector(workspace, torch.uint8, n, cache._dev, "workspace"), n, workspace
+
+
 def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tree_mask=None,
                    scale: float | None = None, out=None, device_error=None, workspace=None,
                    stream=None):
@@ -638,21 +654,17 @@ def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tre
         if tree_mask.dtype not in (torch.int64, torch.uint64):
             raise ValueError("tree_mask: 64-bit integers are wanted")
         mask = _vector(tree_mask, tree_mask.dtype, q.shape[0], dev, "tree_mask")
-    if workspace is None:
-        n = ctypes.c_int64()
-        check("moe_tree_attention_workspace", _entry("moe_tree_attention_workspace")(
-            cache._c, args, max_q, ctypes.byref(n)))
-        workspace = _empty_on((n.value,), torch.uint8, cache.device, stream)
-    _call("moe_tree_attention", dev, stream, cache._c, args, mask, max_q,
-          _vector(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
+    ws = _workspace("moe_tree_attention_workspace", cache, workspace, stream, args, max_q)
+    _call("moe_tree_attention", dev, stream, cache._c, args, mask, max_q, *ws[:2])
     return out
 
 
 def prompt_attention(cache: KvCache, q, cu_q, ctx_len, page_table, scale: float | None = None,
-                     out=None, device_error=None, stream=None):
+                     out=None, device_error=None, workspace=None, stream=None):
     """moe_prompt_attention: causal attention of packed prompts, or of chunks behind ctx_len cached
     positions; arguments as for tree_attention, without a limit on the rows of a sequence."""
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
-    _call("moe_prompt_attention", cache._dev, stream, cache._c, args)
+    ws = _workspace("moe_prompt_attention_workspace", cache, workspace, stream, args)
+    _call("moe_prompt_attention", cache._dev, stream, cache._c, args, *ws[:2])
     return out

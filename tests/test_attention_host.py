@@ -77,9 +77,10 @@ def test_caches(L, kw, rc):
     c, n = cache(**kw), ctypes.c_int64(7)
     ref = ctypes.byref
     assert L.moe_qk_norm_rope(ref(c), ref(rope()), None) == rc
-    assert L.moe_prompt_attention(ref(c), ref(attention()), None) == rc
+    assert L.moe_prompt_attention(ref(c), ref(attention()), None, 0, None) == rc
     assert L.moe_tree_attention(ref(c), ref(attention()), None, 1, None, 0, None) == rc
     assert L.moe_tree_attention_workspace(ref(c), ref(attention()), 1, ref(n)) == rc
+    assert L.moe_prompt_attention_workspace(ref(c), ref(attention()), ref(n)) == rc
     assert n.value == 7
 
 
@@ -111,15 +112,17 @@ def test_norm_rope(L, kw, rc):
 def test_attention(L, kw, rc):
     c, a, n = cache(), attention(**kw), ctypes.c_int64()
     ref = ctypes.byref
-    assert L.moe_prompt_attention(ref(c), ref(a), None) == rc
+    assert L.moe_prompt_attention(ref(c), ref(a), None, 0, None) == rc
     assert L.moe_tree_attention(ref(c), ref(a), None, 1, None, 0, None) == rc
     assert L.moe_tree_attention_workspace(ref(c), ref(a), 1, ref(n)) == rc
+    assert L.moe_prompt_attention_workspace(ref(c), ref(a), ref(n)) == rc
 
 
 @pytest.mark.parametrize("page", [8, 24, 48, 2048])
 def test_page_sizes_of_attention(L, page):
     c = cache(page_size=page)
-    assert L.moe_prompt_attention(ctypes.byref(c), ctypes.byref(attention()), None) == UNS
+    assert L.moe_prompt_attention(ctypes.byref(c), ctypes.byref(attention()), None, 0,
+                                  None) == UNS
     assert L.moe_tree_attention(ctypes.byref(c), ctypes.byref(attention()), None, 1, None, 0,
                                 None) == UNS
 
@@ -131,6 +134,9 @@ def test_tree_arguments(L):
         assert L.moe_tree_attention(ref(c), ref(a), None, max_q, None, 0, None) == rc
         assert L.moe_tree_attention_workspace(ref(c), ref(a), max_q, ref(n)) == rc
     assert L.moe_tree_attention_workspace(ref(c), ref(a), 1, None) == INV
+    assert L.moe_prompt_attention_workspace(ref(c), ref(a), None) == INV
+    assert L.moe_prompt_attention(ref(c), ref(a), 0x1008, 1 << 40, None) == INV
+    assert L.moe_prompt_attention(ref(c), ref(a), None, -1, None) == INV
     assert L.moe_tree_attention(ref(c), ref(a), 0x1004, 1, None, 0, None) == INV   # mask address
     assert L.moe_tree_attention(ref(c), ref(a), None, 1, 0x1008, 1 << 40, None) == INV
     assert L.moe_tree_attention(ref(c), ref(a), None, 1, None, -1, None) == INV
@@ -140,13 +146,13 @@ def test_null_and_empty_calls(L):
     ref = ctypes.byref
     assert L.moe_qk_norm_rope(None, ref(rope()), None) == INV
     assert L.moe_qk_norm_rope(ref(cache()), None, None) == INV
-    assert L.moe_prompt_attention(None, ref(attention()), None) == INV
-    assert L.moe_prompt_attention(ref(cache()), None, None) == INV
+    assert L.moe_prompt_attention(None, ref(attention()), None, 0, None) == INV
+    assert L.moe_prompt_attention(ref(cache()), None, None, 0, None) == INV
     assert L.moe_tree_attention(ref(cache()), None, None, 1, None, 0, None) == INV
     none = dict(q=None, k=None, v=None, q_out=None, slots=None, positions=None)
     assert L.moe_qk_norm_rope(ref(cache()), ref(rope(n_tokens=0, **none)), None) == Bn.MOE_OK
     a = attention(n_rows=0, q=None, out=None)
-    assert L.moe_prompt_attention(ref(cache()), ref(a), None) == Bn.MOE_OK
+    assert L.moe_prompt_attention(ref(cache()), ref(a), None, 0, None) == Bn.MOE_OK
     assert L.moe_tree_attention(ref(cache()), ref(a), None, 1, None, 0, None) == Bn.MOE_OK
 
 
