@@ -202,4 +202,12 @@ inline int check_attention(const moe_kv_cache *c, const moe_attention *a, Params
   return MOE_OK;
 }
 
+// Attention in tiles of 128 rows on the 5th-generation tensor cores: causal, or by p.mask
+// (moe_prompt.cu, moe_prompt_tree.cu).
+int tiles_workspace(const moe_kv_cache *cache, const Params &p, int64_t *bytes);
+int run_tiles(const moe_kv_cache *cache, const Params &p, void *workspace, int64_t workspace_bytes,
+              cudaStream_t stream);
+int run_tree_tiles(const moe_kv_cache *cache, const Params &p, void *workspace,
+                   int64_t workspace_bytes, cudaStream_t stream);
+
 }  // namespace attn

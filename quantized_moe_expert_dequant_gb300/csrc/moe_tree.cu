@@ -411,13 +411,19 @@ struct Plan {
   int64_t part, ml, shared, bytes;  // offsets in the workspace
 };
 
+// More than 32 rows an item are compute on mma.sync tiles, which read K and V once for 64 rows; the
+// tiles of 128 rows on tcgen05 keep up with memory.  Drafts of up to 64 tokens over contexts of up to
+// 9000 (12 query, 2 key/value heads of 128): 46.0 us here, NEWTIME there; 8 tokens behind 131000
+// positions (32 query, 8 key/value heads: 32 rows): 263 us here, at the copy rate.
+static bool many_rows(const Params &p) { return static_cast<int64_t>(p.max_q) * p.group > 32; }
+
 static int make_plan(const moe_kv_cache *c, const Params &p, int max_q, Plan *plan) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MOE_ERR_CUDA;
   const int64_t rows = static_cast<int64_t>(max_q) * p.group;
-  plan->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  plan->rows = rows <= 16 ? 16 : 32;
   // no more CTAs than the largest batch that the arguments allow has work for
   const int64_t len = (static_cast<int64_t>(p.table_width) << p.page_shift) / kTile + 1;
   const int64_t items =
@@ -456,8 +462,7 @@ static cudaError_t launch(const Work &w, int grid, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t launch_rows(const Work &w, const Plan &plan, cudaStream_t stream) {
   if (plan.rows == 16) return launch<T, D, 1>(w, plan.grid, stream);
-  if (plan.rows == 32) return launch<T, D, 2>(w, plan.grid, stream);
-  return launch<T, D, 4>(w, plan.grid, stream);
+  return launch<T, D, 2>(w, plan.grid, stream);
 }
 
 }  // namespace attn
@@ -473,6 +478,8 @@ extern "C" int moe_tree_attention_workspace(const moe_kv_cache *cache, const moe
     *bytes = 0;
     return MOE_OK;
   }
+  p.max_q = max_q;
+  if (attn::many_rows(p)) return attn::tiles_workspace(cache, p, bytes);
   attn::Plan plan;
   rc = attn::make_plan(cache, p, max_q, &plan);
   if (rc == MOE_OK) *bytes = plan.bytes;
@@ -490,12 +497,15 @@ extern "C" int moe_tree_attention(const moe_kv_cache *cache, const moe_attention
     return MOE_ERR_INVALID_ARG;
   if (max_q > MOE_TREE_MAX_Q) return MOE_ERR_UNSUPPORTED;
   if (w.p.n_seqs == 0 || w.p.n_rows == 0) return MOE_OK;
+  w.p.mask = tree_mask;
+  w.p.max_q = max_q;
+  if (attn::many_rows(w.p))
+    return attn::run_tiles(cache, w.p, workspace, workspace_bytes,
+                           static_cast<cudaStream_t>(stream));
   attn::Plan plan;
   rc = attn::make_plan(cache, w.p, max_q, &plan);
   if (rc != MOE_OK) return rc;
   if (!workspace || workspace_bytes < plan.bytes) return MOE_ERR_INVALID_ARG;
-  w.p.mask = tree_mask;
-  w.p.max_q = max_q;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   w.part = reinterpret_cast<float *>(ws + plan.part);
   w.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);

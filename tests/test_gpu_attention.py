@@ -110,6 +110,35 @@ def test_many_short_sequences():
     C.assert_within(run_tree(b, 3, masks), ref, tol)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (16, 2, 64), (9, 3, 128)])
+def test_large_trees_behind_long_contexts(Hq, Hkv, D):
+    """Items whose positions several CTAs share, drafts across a step's border, empty rows."""
+    lens, ctxs = [64, 33, 5, 64, 64], [20010, 5120, 127, 0, 5100]
+    b = C.batch(Hq + D, lens, ctxs, Hq, Hkv, D, 64, F16)
+    masks = tree_masks(D, lens, False)
+    masks[3] = masks[70] = 0
+    ref, tol = b.reference(D ** -0.5, masks)
+    C.assert_within(run_tree(b, 64, masks), ref, tol)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (6, 1, 128)])
+def test_prompts_that_many_ctas_share(Hq, Hkv, D):
+    lens, ctxs = [700, 1, 3, 130, 0, 2100], [9000, 12345, 0, 1023, 8000, 0]
+    b = C.batch(Hq * D, lens, ctxs, Hq, Hkv, D, 128, BF16)
+    ref, tol = b.reference(D ** -0.5)
+    C.assert_within(run_prompt(b), ref, tol)
+
+
+def test_many_prompts():
+    gen = torch.Generator().manual_seed(9)
+    n = 900
+    lens = torch.randint(0, 40, (n,), generator=gen).tolist()
+    ctxs = [0 if i % 3 else 200 for i in range(n)]
+    b = C.batch(6, lens, ctxs, 4, 2, 64, 16, BF16)
+    ref, tol = b.reference(0.125)
+    C.assert_within(run_prompt(b), ref, tol)
+
+
 def test_rows_that_see_nothing_are_zeros():
     lens = [4, 1, 2]
     b = C.batch(11, lens, [0, 0, 40], 6, 2, 64, 16, BF16)
