@@ -322,7 +322,7 @@ typedef struct moe_kv_cache {
  *   for i < rot_dim / 2 and (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved;
  * fp32 throughout (angles reduced in fp64), rounded once.  Queries go to q_out; keys, and values
  * only rounded, go to slots[t] = page * page_size + position in the page.  A token whose slot is
- * negative is padding: nothing of it is read or written. Two tokens with one slot leave either. */
+ * negative is padding: nothing of it is written. Two tokens with one slot leave either's elements. */
 typedef struct moe_norm_rope {
   const void *q;           /* [n_tokens][n_q_heads][head_dim] by strides, in_dtype, 16-byte aligned */
   const void *k;           /* [n_tokens][n_kv_heads][head_dim] */

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "moe_decode.h"
@@ -201,6 +202,22 @@ inline int check_attention(const moe_kv_cache *c, const moe_attention *a, Params
   p->scale_log2 = a->scale * 1.4426950408889634f;
   return MOE_OK;
 }
+
+// Raises a kernel's limit of dynamic shared memory, once per device (a call of the runtime takes about
+// a microsecond).
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};
+  cudaError_t set(const void *kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // Attention in tiles of 128 rows on the 5th-generation tensor cores: causal, or by p.mask
 // (moe_prompt.cu, moe_prompt_tree.cu).

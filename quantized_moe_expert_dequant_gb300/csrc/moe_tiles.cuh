@@ -823,42 +823,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and ends in a later one: a thread takes
-// eight columns of a row.  The parts are added in the order of the positions.
+// eight columns of a row.  The parts are added in the order of the positions.  The list of parts
+// is found first, 32 CTAs at a time, so that the loads of one part do not wait for another's.
+constexpr int kMaxCtas = 512;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int tokens,
                                                           const float *part, const float2 *part_ml,
                                                           const Share *share, int ctas) {
+  __shared__ int s_slot[kMaxCtas], s_count;
   pdl_wait();
   const Share sh = share[blockIdx.x];
   if (!sh.tail) return;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int n = 1;
+    if (lane == 0) s_slot[0] = 2 * blockIdx.x + 1;
+    for (int c0 = blockIdx.x + 1; c0 < ctas; c0 += 32) {
+      const int c = c0 + lane;
+      int head = 0, ends = 0;
+      if (c < ctas) head = share[c].head, ends = head && share[c].head_ends;
+      const uint32_t stop = __ballot_sync(0xffffffffu, ends);
+      uint32_t parts = __ballot_sync(0xffffffffu, head);  // without: a CTA that had no work
+      if (stop) parts &= 0xffffffffu >> (32 - __ffs(stop));
+      if (parts >> lane & 1) s_slot[n + __popc(parts & ((1u << lane) - 1))] = 2 * c;
+      n += __popc(parts);
+      if (stop) break;
+    }
+    if (lane == 0) s_count = n;
+  }
+  __syncthreads();
+  const int n = s_count;
   const int i = threadIdx.x >> 7, r = threadIdx.x & 127;
   const int r_tok = r / p.group, tok = sh.tok0 + i * tokens + r_tok;
   if (r >= tokens * p.group || tok >= sh.nq) return;
-  const float4 *src = reinterpret_cast<const float4 *>(part);
-  float m = kNegInf, l = 0.f, o[8] = {};
-  for (int c = blockIdx.x; c < ctas; ++c) {
-    const bool first = c == static_cast<int>(blockIdx.x);
-    int ends = 0;
-    if (!first) {
-      const Share other = share[c];
-      if (!other.head) continue;  // a CTA without work
-      ends = other.head_ends;
+  const float2 *ml = part_ml + threadIdx.x;
+  float m = kNegInf;
+#pragma unroll 4
+  for (int c = 0; c < n; ++c) m = fmaxf(m, ml[s_slot[c] * 256].x);
+  const float4 *src = reinterpret_cast<const float4 *>(part) + (i * (D / 4) + 2 * blockIdx.y) * 128 + r;
+  float l = 0.f, o[8] = {};
+#pragma unroll 4
+  for (int c = 0; c < n; ++c) {
+    const float2 v = ml[s_slot[c] * 256];
+    const float4 *q = src + static_cast<int64_t>(s_slot[c]) * 2 * (D / 4) * 128;
+    const float4 a = q[0], b = q[128];
+    if (v.y > 0.f) {  // a part without weight may not have been written
+      const float g = exp2_approx((v.x - m) * p.scale_log2);
+      l = fmaf(v.y, g, l);
+      o[0] = fmaf(a.x, g, o[0]), o[1] = fmaf(a.y, g, o[1]);
+      o[2] = fmaf(a.z, g, o[2]), o[3] = fmaf(a.w, g, o[3]);
+      o[4] = fmaf(b.x, g, o[4]), o[5] = fmaf(b.y, g, o[5]);
+      o[6] = fmaf(b.z, g, o[6]), o[7] = fmaf(b.w, g, o[7]);
     }
-    const int64_t slot = 2 * static_cast<int64_t>(c) + (first ? 1 : 0);
-    const float2 ml = part_ml[slot * 256 + threadIdx.x];
-    if (ml.y > 0.f) {
-      const float top = fmaxf(m, ml.x);
-      const float f = exp2_approx((m - top) * p.scale_log2);
-      const float g = exp2_approx((ml.x - top) * p.scale_log2);
-      m = top;
-      l = l * f + ml.y * g;
-      const float4 *q = src + ((slot * 2 + i) * (D / 4) + 2 * blockIdx.y) * 128 + r;
-      const float4 u = q[0], v = q[128];
-      const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = o[e] * f + x[e] * g;
-    }
-    if (ends) break;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint4 v;
@@ -881,7 +898,7 @@ static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MOE_ERR_CUDA;
-  plan->grid = sms;
+  plan->grid = sms < kMaxCtas ? sms : kMaxCtas;
   plan->ml = plan->share = plan->bytes = 0;
   const int64_t len = static_cast<int64_t>(p.table_width) << p.page_shift;  // of a sequence at most
   // the line's length times the CTAs stays inside 64 bits
@@ -916,8 +933,8 @@ static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan
       !tc::make_map(&w.v, bf16, p.v, 4, dims, str, box))
     return MOE_ERR_UNSUPPORTED;
   const auto kern = prompt_kernel<T, D, TREE>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Prompt<D>::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Prompt<D>::kSmem);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   kern<<<plan.grid, kPromptThreads, Prompt<D>::kSmem, stream>>>(w);
   if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;

@@ -440,8 +440,8 @@ static int make_plan(const moe_kv_cache *c, const Params &p, int max_q, Plan *pl
 template <typename T, int D, int WR>
 static cudaError_t launch(const Work &w, int grid, cudaStream_t stream) {
   const auto kern = tree_kernel<T, D, WR>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tree<D>::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
   e = cudaGetLastError();
