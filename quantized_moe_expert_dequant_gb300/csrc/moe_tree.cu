@@ -6,40 +6,50 @@
 //   sum; what was summed before a larger maximum is scaled down to it.
 //
 // Bound by the bytes of K and V, so what matters is that every SM streams all the time, whatever
-// the lengths are.  An item is one sequence, one key/value head and one tile of rows (row R is query
-// R / group, head R % group); its positions are cut into tiles of 64.  All tiles of all items, in
-// order, form one line that the CTAs share evenly: CTA c takes the tiles [c W / G, (c + 1) W / G).
-// The lengths are read on the device, so a captured graph balances whatever it is replayed on.  An
-// item that ends up in one CTA is written by it; one that several CTAs share leaves its partial
-// maxima, sums and outputs in the workspace, and join_kernel adds them in order.
+// the lengths are.  An item is one sequence and one key/value head, with the queries of all heads
+// that share it as rows (row R is query R / group, head R % group; more than 32 rows go to the tiles
+// of moe_tiles.cuh); its positions are cut into tiles of 64.  All tiles of all items, in order, form one
+// line that the CTAs share evenly: CTA c takes the tiles [c W / G, (c + 1) W / G).  The lengths are
+// read on the device, so a captured graph balances whatever it is replayed on.  An item that ends up in
+// one CTA is written by it; one that several CTAs share leaves its partial maxima, sums and outputs
+// in the workspace, and join_kernel adds them in order.
 //
 // A CTA is four warps over 16 WR rows: WR warps split the rows, 4 / WR warps the positions of a
-// tile, so a single decoded token (group <= 16 rows) still uses all four.
+// tile, so a single decoded token (group <= 16 rows) still uses all four.  Copies run two or three
+// tiles ahead and across items, so that one item's end does not empty the pipeline of the next:
+// 32 tokens over contexts of 1 to 15991 positions (741 MB) 132 us with a pipeline per item, 125 us
+// so (5.9 TB/s); 8 drafts behind 65536 to 131064 positions (1.75 GB) 264 us (6.6 TB/s).
 #include <algorithm>
 
 #include "moe_attention.cuh"
 
 namespace attn {
 
-constexpr int kTile = 64;  // positions of a tile
 constexpr int kThreads = 128;
+constexpr int kSlice = 40;  // 32 output columns of a row on their way between warps, padded
+
+// positions of a tile: 32 KB of K and V each way; with 64 for heads of 64 too, what a tile costs besides
+// its copies showed (64 sequences, 16 heads of 64: 148 us, 136 with 128)
+constexpr int tile_of(int dim) { return dim == 64 ? 128 : 64; }
 
 template <int D>
 struct Tree {
-  // 16 or 32 KB a stage; with two CTAs an SM there are 96 to 128 KB in flight, more than the 35 KB
-  // that latency times bandwidth asks for
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kTile = tile_of(D);
+  // 32 KB a stage; with two CTAs an SM there are 128 KB in flight, more than the 35 KB that latency
+  // times bandwidth asks for
+  static constexpr int kStages = 3;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kSmem = kStages * 2 * kTileBytes;
+  static constexpr int kRing = kStages * 2 * kTileBytes;
+  static constexpr int kSmem = kRing + 4 * 16 * kSlice * 4;
 };
 constexpr int kCtasPerSm = 2;
-constexpr int kMinTiles = 4;  // tiles that a CTA takes at least: below it joining costs more
+constexpr int kMinPositions = 128, kMaxLeast = 256;  // bounds of the positions that a CTA takes at least
 
 // What one CTA leaves for join_kernel: the item that begins in it and goes on in the next ones.
 struct Shared {
   int pieces;  // CTAs that hold a part; 0: nothing to join
   int row0;    // the sequence's first row
-  int kvh, R0, rows;
+  int kvh, rows;
   int slot;    // 0 or 1: which of its CTA's parts is its first
 };
 
@@ -51,31 +61,32 @@ struct Work {
 };
 
 template <int D>
-__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {  // byte offset in a [64][D] tile
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {  // byte offset in a [rows][D] tile
   return static_cast<uint32_t>(row * D * 2 + ((chunk ^ (row & 7)) << 4));
 }
 
-// The pages of a tile's four quarters (a page has at least 16 positions); -1: nothing there.
+// The pages of each 16 positions of a tile (a page has at least 16); -1: nothing there.
+template <int TILE>
 __device__ __forceinline__ void load_pages(const Params &p, const int32_t *pages, int len, int tile,
-                                           int (&pg)[4]) {
+                                           int (&pg)[TILE / 16]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int pos = tile * kTile + 16 * e;
+  for (int e = 0; e < TILE / 16; ++e) {
+    const int pos = tile * TILE + 16 * e;
     pg[e] = pos < len ? pages[pos >> p.page_shift] : -1;
   }
 }
 
-// Copies positions [64 t, 64 t + 64) of K and V into shared memory; rows past the sequence and on
+// Copies the positions of tile t of K and V into shared memory; rows past the sequence and on
 // a page outside the cache are zeros (what stale pages hold, NaN included, is never multiplied).
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(const Params &p, int len, const int (&pg)[4],
+template <typename T, int D, int TILE>
+__device__ __forceinline__ void load_tile(const Params &p, int len, const int (&pg)[TILE / 16],
                                           int64_t head_off, int tile, uint32_t k_smem,
                                           uint32_t v_smem) {
   constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
 #pragma unroll
-  for (int i = 0; i < kTile / kStep; ++i) {
-    const int r = r0 + i * kStep, pos = tile * kTile + r;
+  for (int i = 0; i < TILE / kStep; ++i) {
+    const int r = r0 + i * kStep, pos = tile * TILE + r;
     const int page = pg[i * kStep / 16];
     const bool valid = pos < len && static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
     const int64_t off = valid ? page * p.page_stride + head_off +
@@ -85,13 +96,11 @@ __device__ __forceinline__ void load_tile(const Params &p, int len, const int (&
     cp_async16(k_smem + d, static_cast<const T *>(p.k) + off, valid);
     cp_async16(v_smem + d, static_cast<const T *>(p.v) + off, valid);
   }
-  if (threadIdx.x < 4) {  // a used page outside the cache is reported
-    const int page = threadIdx.x == 0 ? pg[0] : threadIdx.x == 1 ? pg[1] : threadIdx.x == 2 ? pg[2]
-                                                                                            : pg[3];
-    if (tile * kTile + 16 * static_cast<int>(threadIdx.x) < len &&
-        static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages) && p.err)
+#pragma unroll
+  for (int e = 0; e < TILE / 16; ++e)  // a used page outside the cache is reported
+    if (threadIdx.x == e && tile * TILE + 16 * e < len &&
+        static_cast<unsigned>(pg[e]) >= static_cast<unsigned>(p.n_pages) && p.err)
       atomicOr(p.err, kDevErrBadId);
-  }
 }
 
 // Sums v over the block (every thread gets the sum) and gives each thread the sum before it.
@@ -118,6 +127,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w) {
+  constexpr int kTile = Tree<D>::kTile;
   constexpr int ROWS = 16 * WR, WT = 4 / WR, TW = kTile / WT;  // TW positions of a warp per tile
   constexpr int kStages = Tree<D>::kStages, kTileBytes = Tree<D>::kTileBytes;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -131,8 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
   pdl_launch();
   // all tiles, and the sequence in which this CTA's part of them begins
   const auto weight = [&](const Seq &s) {
-    const int64_t rt = (static_cast<int64_t>(s.nq) * p.group + ROWS - 1) / ROWS;
-    return rt * p.hkv * ((s.len + kTile - 1) / kTile);
+    return s.nq ? static_cast<int64_t>(p.hkv) * ((s.len + kTile - 1) / kTile) : 0;
   };
   const bool first_cta = blockIdx.x == 0;
   int64_t total = 0, before, mine = 0;
@@ -141,7 +150,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     mine = i < p.n_seqs ? weight(load_seq(p, i, first_cta)) : 0;
     total += block_scan(mine, s_warp, &before);
   }
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
+  // A CTA's time grows with its tiles, that of join_kernel with an item's parts: with n tiles an item the
+  // shortest is near sqrt(n) / 2 tiles a CTA.  (One token, positions: us with 2, 4, 8 tiles of 64 at
+  // least.  500: 7.8, 9.6, 12.9; 4000: 16.2, 14.4, 15.2; 16384: 21.6, 21.5, 22.9.)
+  const float per_item = static_cast<float>(total) / (static_cast<float>(p.n_seqs) * p.hkv);
+  const int least = min(kMaxLeast / kTile, max(kMinPositions / kTile,
+                                               static_cast<int>(0.5f * sqrtf(per_item) + 0.5f)));
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least);
   if (threadIdx.x == 0) w.shared[blockIdx.x].pieces = 0;
   if (blockIdx.x >= ctas) return;
   int64_t at = blockIdx.x * total / ctas;
@@ -160,31 +175,65 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     }
   }
   __syncthreads();
-  int seq = s_seq;
-  int64_t seq_at = s_before;  // tiles before the sequence
   const int64_t begin = at;
-
   const uint32_t base = smem_u32(smem);
-  Seq s = load_seq(p, seq, false);
-  while (at < end) {
-    while (at >= seq_at + weight(s)) {
-      seq_at += weight(s);
-      if (++seq >= p.n_seqs) return;  // never, unless the lengths change under the kernel
-      s = load_seq(p, seq, false);
-    }
-    const int nt = (s.len + kTile - 1) / kTile;
-    const int item = static_cast<int>((at - seq_at) / nt);  // (head, row tile)
-    const int rts = (s.nq * p.group + ROWS - 1) / ROWS;
-    const int kvh = item / rts, R0 = (item - kvh * rts) * ROWS, rows = s.nq * p.group;
-    const int64_t item_at = seq_at + static_cast<int64_t>(item) * nt;
-    const int t0 = static_cast<int>(at - item_at);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(nt), end - item_at));
-    const int32_t *pages = p.table + seq * p.table_stride;
-    const int64_t head_off = kvh * p.head_stride;
 
-    int pg[kStages][4];
+  // What is copied next: tile `t` of head `kvh` of sequence `seq`; the tile that is computed is
+  // kStages - 1 behind.  Tile number k of the CTA waits in stage k % kStages; its pages are read one
+  // tile ahead, and a sequence's description one sequence ahead.
+  struct Ahead {
+    const int32_t *pages;
+    int64_t head_off;
+    int left, seq, kvh, t, nt, len, stage, pg[kTile / 16];
+    Seq next;
+  } ld;
+  {
+    const int64_t in_seq = at - s_before;
+    const Seq q = load_seq(p, s_seq, false);
+    ld.left = static_cast<int>(end - at);
+    ld.seq = s_seq, ld.len = q.len, ld.nt = (q.len + kTile - 1) / kTile;
+    ld.kvh = static_cast<int>(in_seq / ld.nt), ld.t = static_cast<int>(in_seq - static_cast<int64_t>(ld.kvh) * ld.nt);
+    ld.stage = 0;
+    ld.pages = p.table + ld.seq * p.table_stride;
+    ld.head_off = ld.kvh * p.head_stride;
+    load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
+    ld.next = load_seq(p, min(ld.seq + 1, p.n_seqs - 1), false);
+  }
+  const auto next_item = [&]() {
+    ld.t = 0;
+    ld.head_off += p.head_stride;
+    if (++ld.kvh < p.hkv) return;
+    ld.kvh = 0;
+    ld.head_off = 0;
+    bool empty = true;  // sequences without rows have no tiles
+    while (empty && ++ld.seq < p.n_seqs) {
+      ld.len = ld.next.len, ld.nt = (ld.len + kTile - 1) / kTile;
+      empty = ld.next.nq == 0;
+      ld.next = load_seq(p, min(ld.seq + 1, p.n_seqs - 1), false);
+    }
+    if (empty) ld.left = 0;
+    ld.pages = p.table + ld.seq * p.table_stride;
+  };
+  const auto copy_next = [&]() {
+    if (ld.left > 0) {
+      const uint32_t st = base + ld.stage * 2 * kTileBytes;
+      load_tile<T, D, kTile>(p, ld.len, ld.pg, ld.head_off, ld.t, st, st + kTileBytes);
+      if (++ld.stage == kStages) ld.stage = 0;
+      --ld.left;
+      if (++ld.t == ld.nt) next_item();
+      if (ld.left > 0) load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
+    }
+    cp_async_commit();
+  };
+
+  int seq = ld.seq, kvh = ld.kvh, t0 = ld.t, stage = 0;
+  Seq s = load_seq(p, seq, false);
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) load_pages(p, pages, s.len, t0 + i, pg[i]);
+  for (int i = 0; i < kStages - 1; ++i) copy_next();
+  while (at < end) {
+    const int nt = (s.len + kTile - 1) / kTile, rows = s.nq * p.group;
+    const int64_t item_at = at - t0;
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(nt), t0 + (end - at)));
     // this lane's two rows: queries, heads, masks
     int row_q[2];
     uint64_t row_mask[2];
@@ -192,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     const uint32_t *qp[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int R = R0 + wr * 16 + g + 8 * h;
+      const int R = wr * 16 + g + 8 * h;
       row_ok[h] = R < rows;
       row_q[h] = row_ok[h] ? R / p.group : 0;
       const int head = kvh * p.group + (row_ok[h] ? R - row_q[h] * p.group : 0);
@@ -214,23 +263,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-    // tile t waits in stage (t - t0) % kStages; the pages of a tile are read one tile ahead
-    const auto issue = [&](int t, const int (&page)[4]) {
-      if (t < t1) {
-        const uint32_t st = base + ((t - t0) % kStages) * 2 * kTileBytes;
-        load_tile<T, D>(p, s.len, page, head_off, t, st, st + kTileBytes);
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(t0 + i, pg[i]);
-    int (&next)[4] = pg[kStages - 1];
     for (int t = t0; t < t1; ++t) {
       cp_async_wait<kStages - 2>();
-      __syncthreads();  // tile t is there, and every warp is done with tile t - 1
-      issue(t + kStages - 1, next);
-      load_pages(p, pages, s.len, t + kStages, next);
-      const uint32_t ks = base + ((t - t0) % kStages) * 2 * kTileBytes, vs = ks + kTileBytes;
+      __syncthreads();  // tile t is there, and every warp is done with the tile before
+      const uint32_t ks = base + stage * 2 * kTileBytes, vs = ks + kTileBytes;
+      if (++stage == kStages) stage = 0;
 
       float sc[TW / 8][4];
 #pragma unroll
@@ -246,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
           Half<T>::mma(sc[2 * j], qa[kk], b[0], b[1]);
           Half<T>::mma(sc[2 * j + 1], qa[kk], b[2], b[3]);
         }
+      copy_next();
       if ((t + 1) * kTile > s.ctx) {  // drafted positions, and those behind the sequence
         const int pos0 = t * kTile + wt * TW + 2 * q4;
 #pragma unroll
@@ -306,65 +344,77 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       }
     }
 
-    // join the warps that split the positions, and the rows' sums over their four lanes
-    cp_async_wait<0>();
-    __syncthreads();
-    float *s_o = reinterpret_cast<float *>(smem);  // [4][16][D]
+    // join the warps that split the positions, 32 columns at a time, and the rows' sums over their
+    // four lanes
+    float *s_o = reinterpret_cast<float *>(smem + Tree<D>::kRing);  // [4][16][kSlice]
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int r = g + 8 * h;
-      if (q4 == 0) s_m[warp][r] = m[h], s_l[warp][r] = l[h];
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<float2 *>(s_o + (warp * 16 + r) * D + 8 * j + 2 * q4) =
-            make_float2(o[j][2 * h], o[j][2 * h + 1]);
+      if (q4 == 0) s_m[warp][g + 8 * h] = m[h], s_l[warp][g + 8 * h] = l[h];
     }
-    __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (at == begin ? 0 : 1);
     if (threadIdx.x == 0 && t0 == 0 && t1 < nt) {
       Shared &r = w.shared[blockIdx.x];
       r.pieces = static_cast<int>(((item_at + nt) * ctas - 1) / total) - blockIdx.x + 1;
-      r.row0 = s.row0, r.kvh = kvh, r.R0 = R0, r.rows = rows, r.slot = at == begin ? 0 : 1;
+      r.row0 = s.row0, r.kvh = kvh, r.rows = rows, r.slot = at == begin ? 0 : 1;
     }
-    for (int i = threadIdx.x; i < ROWS * D / 8; i += kThreads) {
-      const int r = i / (D / 8), c = i % (D / 8), R = R0 + r;
-      if (R >= rows) break;
-      float top = kNegInf;
+    const int r = threadIdx.x / 4, c8 = threadIdx.x % 4;  // eight columns of a row, ROWS * 4 threads
 #pragma unroll
-      for (int v = 0; v < WT; ++v) top = fmaxf(top, s_m[v * WR + r / 16][r % 16]);
-      const float ref = top == kNegInf ? 0.f : top;
-      float total_l = 0.f, x[8] = {};
+    for (int slice = 0; slice < D / 32; ++slice) {
+      if (slice > 0) __syncthreads();  // the last slice has been read
 #pragma unroll
-      for (int v = 0; v < WT; ++v) {
-        const int ww = v * WR + r / 16;
-        const float f = exp2_approx((s_m[ww][r % 16] - ref) * p.scale_log2);
-        total_l += f * s_l[ww][r % 16];
-        const float *src = s_o + (ww * 16 + r % 16) * D + 8 * c;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf(f, src[e], x[e]);
-      }
-      if (whole) {
-        const float inv = total_l > 0.f ? 1.f / total_l : 0.f;  // a row that sees nothing is zeros
-        const int tok = R / p.group, head = kvh * p.group + R - tok * p.group;
-        uint4 v;
-        v.x = Half<T>::pack(x[0] * inv, x[1] * inv);
-        v.y = Half<T>::pack(x[2] * inv, x[3] * inv);
-        v.z = Half<T>::pack(x[4] * inv, x[5] * inv);
-        v.w = Half<T>::pack(x[6] * inv, x[7] * inv);
-        *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (s.row0 + tok) * p.o_row +
-                                   head * p.o_head + 8 * c) = v;
-      } else {
-        float4 *dst = reinterpret_cast<float4 *>(w.part + (slot * ROWS + r) * D + 8 * c);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (c == 0) w.part_ml[slot * ROWS + r] = make_float2(top, total_l);
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float2 *>(s_o + (warp * 16 + g + 8 * h) * kSlice + 8 * j + 2 * q4) =
+              make_float2(o[4 * slice + j][2 * h], o[4 * slice + j][2 * h + 1]);
+      __syncthreads();
+      if (r < ROWS && r < rows) {
+        float top = kNegInf;
+#pragma unroll
+        for (int v = 0; v < WT; ++v) top = fmaxf(top, s_m[v * WR + r / 16][r % 16]);
+        const float ref = top == kNegInf ? 0.f : top;
+        float total_l = 0.f, x[8] = {};
+#pragma unroll
+        for (int v = 0; v < WT; ++v) {
+          const int ww = v * WR + r / 16;
+          const float f = exp2_approx((s_m[ww][r % 16] - ref) * p.scale_log2);
+          total_l += f * s_l[ww][r % 16];
+          const float *src = s_o + (ww * 16 + r % 16) * kSlice + 8 * c8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(f, src[e], x[e]);
+        }
+        const int col = 32 * slice + 8 * c8;
+        if (whole) {
+          const float inv = total_l > 0.f ? 1.f / total_l : 0.f;  // a row that sees nothing is zeros
+          const int tok = r / p.group, head = kvh * p.group + r - tok * p.group;
+          uint4 v;
+          v.x = Half<T>::pack(x[0] * inv, x[1] * inv);
+          v.y = Half<T>::pack(x[2] * inv, x[3] * inv);
+          v.z = Half<T>::pack(x[4] * inv, x[5] * inv);
+          v.w = Half<T>::pack(x[6] * inv, x[7] * inv);
+          *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (s.row0 + tok) * p.o_row +
+                                     head * p.o_head + col) = v;
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(w.part + (slot * ROWS + r) * D + col);
+          dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+          dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (col == 0) w.part_ml[slot * ROWS + r] = make_float2(top, total_l);
+        }
       }
     }
-    __syncthreads();  // the next item's tiles go where s_o is
+    __syncthreads();  // s_o, s_m and s_l are free again
     at = item_at + t1;
+    t0 = 0;
+    if (t1 == nt && ++kvh == p.hkv) {
+      kvh = 0;
+      do {
+        if (++seq >= p.n_seqs) return;  // the end of the line
+        s = load_seq(p, seq, false);
+      } while (s.nq == 0);
+    }
   }
 }
 
@@ -376,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Work w) {
   pdl_wait();
   const Shared sh = w.shared[blockIdx.x];
   const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int R = sh.R0 + r;
+  const int R = r;
   if (sh.pieces == 0 || R >= sh.rows) return;
   const int64_t c0 = blockIdx.x;
   const int64_t first = 2 * c0 + sh.slot;
@@ -413,7 +463,7 @@ struct Plan {
 
 // More than 32 rows an item are compute on mma.sync tiles, which read K and V once for 64 rows; the
 // tiles of 128 rows on tcgen05 keep up with memory.  Drafts of up to 64 tokens over contexts of up to
-// 9000 (12 query, 2 key/value heads of 128): 46.0 us here, NEWTIME there; 8 tokens behind 131000
+// 9000 (12 query, 2 key/value heads of 128): 46.0 us here, 34.9 there; 8 tokens behind 131000
 // positions (32 query, 8 key/value heads: 32 rows): 263 us here, at the copy rate.
 static bool many_rows(const Params &p) { return static_cast<int64_t>(p.max_q) * p.group > 32; }
 
@@ -425,11 +475,12 @@ static int make_plan(const moe_kv_cache *c, const Params &p, int max_q, Plan *pl
   const int64_t rows = static_cast<int64_t>(max_q) * p.group;
   plan->rows = rows <= 16 ? 16 : 32;
   // no more CTAs than the largest batch that the arguments allow has work for
-  const int64_t len = (static_cast<int64_t>(p.table_width) << p.page_shift) / kTile + 1;
+  const int64_t len = (static_cast<int64_t>(p.table_width) << p.page_shift) / tile_of(c->head_dim) + 1;
   const int64_t items =
       (static_cast<int64_t>(p.n_rows) * p.group / plan->rows + p.n_seqs) * p.hkv;
   const int64_t most = len >= INT32_MAX || items >= INT32_MAX ? INT64_MAX : items * len;
-  plan->grid = static_cast<int>(std::min<int64_t>(sms * kCtasPerSm, most / kMinTiles + 1));
+  if (most / (sms * kCtasPerSm) >= INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  plan->grid = static_cast<int>(std::min<int64_t>(sms * kCtasPerSm, most * tile_of(c->head_dim) / kMinPositions + 1));
   plan->part = 0;
   plan->ml = plan->part + 8ll * plan->grid * plan->rows * c->head_dim;
   plan->shared = plan->ml + 16ll * plan->grid * plan->rows;
