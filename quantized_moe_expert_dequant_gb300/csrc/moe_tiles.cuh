@@ -29,8 +29,8 @@ namespace attn {
 constexpr int kPos = 128;               // positions of a step
 constexpr int kSoftmaxWarps = 8;        // four a tile
 constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // and products, copies, items, an idle warp
-// 168 registers at launch; 2 x 128 x 208 + 128 x 88 = 384 x 168
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// 168 registers at launch; 2 x 128 x 216 + 128 x 72 = 384 x 168
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kItems = 4;               // items between the warp that finds them and the others
 constexpr float kGrowth = 8.f;          // log2 of how far a maximum may grow before O is rescaled
 
@@ -62,8 +62,8 @@ struct PromptParams {
 // sequence, head by head, form one line that the CTAs share evenly, whatever the lengths are; a
 // boundary inside an item becomes a boundary between two of its steps, or moves to the item's edge
 // when fewer than kMinSteps steps would be cut off.
-constexpr int kItemCost = 320;
-constexpr int kMinSteps = 4;
+constexpr int kItemCost = 224;
+constexpr int kMinSteps = 2;
 
 struct Spot {  // the place before a step of an item
   int seq, head, tile, step;
@@ -250,6 +250,11 @@ __device__ __forceinline__ float2 unpair(uint64_t v) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -753,43 +758,54 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (idle) continue;
       tc::fence_after();
       // The next item's first P V overwrites O only after this warp has handed over that P.
+      // Short loops: this code runs once an item, and fetching a long stretch of it took longer than
+      // running it (16 packed prompts of 1024 tokens 88 us unrolled, 76 so).
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (item.a > 0 ? 0 : 1);
       if (!item.whole) {
         float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + i) * (D / 4) * 128 + r;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tc::tmem_load32(o, to + 32 * c);
           tc::wait_load(o);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            if (r < rows) part[(8 * c + e / 4) * 128] =
-                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            if (r < rows)
+              part[(8 * c + e / 4) * 128] =
+                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
         }
       } else {
-        // 64 columns at a time, eight lanes exchange 16-byte chunks so that each then has one chunk
-        // of eight rows, and together they write 128 bytes of a row: a lane writing its own row
-        // touches 32 lines an instruction, 3500 cycles for both tiles.
+        // 32 columns at a time, four lanes exchange 16-byte chunks so that each then has one chunk of
+        // four rows, and together they write 64 bytes of a row: a lane writing its own row touches 32
+        // lines an instruction.
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const uint64_t inv2 = pair(inv, inv);
+        T *dst[4];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t v[8][4];
+        for (int j = 0; j < 4; ++j) {
+          const int rr = 32 * (warp % 4) + (lane & 28) + j, rt = rr * recip >> 16;
+          dst[j] = rr < rows ? static_cast<T *>(p.out) + (item.row0 + tok_first + rt) * p.o_row +
+                                   (item.kvh * p.group + rr - rt * p.group) * p.o_head +
+                                   8 * (lane & 3)
+                             : nullptr;
+        }
+#pragma unroll 2
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32], v[4][4];
+          tc::tmem_load32(o, to + 32 * c);
+          tc::wait_load(o);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[32];
-            tc::tmem_load32(o, to + 64 * c + 32 * h);
-            tc::wait_load(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              v[4 * h + e / 4][e % 4] = Half<T>::pack(__uint_as_float(o[2 * e]) * inv,
-                                                      __uint_as_float(o[2 * e + 1]) * inv);
+          for (int e = 0; e < 16; ++e) {
+            const float2 f = unpair(
+                mul2(pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2));
+            v[e / 4][e % 4] = Half<T>::pack(f.x, f.y);
           }
 #pragma unroll
-          for (int k = 1; k < 8; k <<= 1) {
+          for (int k = 1; k < 4; k <<= 1) {
             const bool upper = (lane & k) != 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
               if (!(j & k))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -799,15 +815,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int rr = 32 * (warp % 4) + (lane & 24) + j, rt = rr * recip >> 16;
-            if (rr < w.tokens * p.group && tok_first + rt < item.nq)
-              *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
-                                         (item.row0 + tok_first + rt) * p.o_row +
-                                         (item.kvh * p.group + rr - rt * p.group) * p.o_head +
-                                         64 * c + 8 * (lane & 7)) =
+          for (int j = 0; j < 4; ++j)
+            if (dst[j])
+              *reinterpret_cast<uint4 *>(dst[j] + 32 * c) =
                   make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
-          }
         }
       }
       if (!item.whole && r < rows) w.part_ml[slot * 256 + i * 128 + r] = make_float2(m, l);
