@@ -30,6 +30,8 @@ struct Params {
   float scale_log2;                              // scale * log2(e)
 };
 
+constexpr int kMaxLen = 1 << 30;  // positions of a sequence: every index of one fits 32 bits
+
 // One sequence's queries and positions, checked against the host's bounds: a description that is
 // out of range sets the error bit and counts as a sequence without queries.
 struct Seq {
@@ -44,7 +46,7 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int s, bool report) {
   const int64_t nq = end - r.row0;
   const int64_t len = nq + r.ctx;
   const bool ok = r.row0 >= 0 && nq >= 0 && end <= p.n_rows && nq <= p.max_q && r.ctx >= 0 &&
-                  len <= (static_cast<int64_t>(p.table_width) << p.page_shift);
+                  len <= (static_cast<int64_t>(p.table_width) << p.page_shift) && len <= kMaxLen;
   if (!ok && report && p.err) atomicOr(p.err, kDevErrBadId);
   r.nq = ok ? static_cast<int>(nq) : 0;
   r.len = ok ? static_cast<int>(len) : 0;

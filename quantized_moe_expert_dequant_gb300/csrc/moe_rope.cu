@@ -15,8 +15,8 @@
 // the tokens; the next token's elements are on their way, and the angles of the next few tokens are
 // formed by all warps at once, while this one is worked on.  8192 tokens of 32 query and 8 key/value
 // heads of 128 in bf16 (201 MB): 53.1 us with a block a token that loads after its angles, 44.5 us
-// resident with a token's angles at a time (two warps form them, the others wait), 38.2 us so
-// (5.3 TB/s); two blocks an SM 42.8, deeper copies through shared memory 46.8.
+// resident with a token's angles at a time (two warps form them, the others wait), 37.5 us so
+// (5.4 TB/s); two blocks an SM 42.8, deeper copies through shared memory 46.8.
 #include <algorithm>
 
 #include "moe_attention.cuh"
@@ -94,9 +94,10 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocksPerSm) norm_rope_kernel(co
   const bool live = t < per;
   const int kind = h < p.hq ? 0 : h < p.hq + p.hkv ? 1 : 2;  // query, key, value
   const int head = h - (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv);
-  const bool turned = kind < 2 && l < p.rot / 16;
+  const int lanes = p.rot / 16;  // of a head that turn something; angle f is the (f % 8)-th of lane f / 8
+  const bool turned = kind < 2 && l < lanes;
   int ca = 2 * l, cb = 2 * l + 1;
-  if (!p.interleaved && l < p.rot / 16) ca = l, cb = l + p.rot / 16;
+  if (!p.interleaved && l < lanes) ca = l, cb = l + lanes;
   const In *in = static_cast<const In *>(p.in[kind]) + head * p.head[kind];
   const T *gamma = kind < 2 ? static_cast<const T *>(p.gamma[kind]) : nullptr;
 
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocksPerSm) norm_rope_kernel(co
       turn -= rint(turn);
       float2 cs;
       sincospif(2.f * static_cast<float>(turn), &cs.y, &cs.x);
-      s_cs[buf][tt][f] = cs;
+      s_cs[buf][tt][f % 8 * lanes + f / 8] = cs;
     }
   };
   Raw<In> ra, rb;
@@ -157,11 +158,11 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocksPerSm) norm_rope_kernel(co
       for (int i = 0; i < 8; ++i) b[i] *= r * w[i];
     }
     if (turned && at >= 0) {
-      const float2 *cs = &s_cs[buf][in_batch * per + t][8 * l];
+      const float2 *cs = &s_cs[buf][in_batch * per + t][l];
       if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = cs[i], w = cs[4 + i];
+          const float2 v = cs[i * lanes], w = cs[(4 + i) * lanes];
           const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], q = b[2 * i + 1];
           a[2 * i] = x * v.x - y * v.y, a[2 * i + 1] = y * v.x + x * v.y;
           b[2 * i] = z * w.x - q * w.y, b[2 * i + 1] = q * w.x + z * w.y;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocksPerSm) norm_rope_kernel(co
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 v = cs[i];
+          const float2 v = cs[i * lanes];
           const float x = a[i], y = b[i];
           a[i] = x * v.x - y * v.y, b[i] = y * v.x + x * v.y;
         }

@@ -49,7 +49,7 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr long long kWaitCycles = 400000000LL;  // about 0.2 s; a kernel's waits take microseconds
+constexpr long long kWaitCycles = 4000000000LL;  // about two seconds; a kernel's waits take microseconds
 
 // Waits for the phase of that parity; false after kWaitCycles, or at once when another thread of the
 // CTA has given up (*gone), so that the kernel ends whatever happens.

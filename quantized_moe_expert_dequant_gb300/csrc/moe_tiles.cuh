@@ -5,18 +5,26 @@
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
 //   that row r sees, in one pass over K and V with a running maximum and sum.
 //
-// Bound by the two products (4 D flops per row and position).  A CTA takes two tiles of up to 128
-// rows of one sequence and one key/value head: row R of a tile is token R / group, query head
-// R % group, so all query heads of a key/value head share the K and V that one CTA loads, and a short
-// prompt still fills the tiles.  Per 128 positions and tile:
+// Bound by the two products (4 D flops per row and position).  An item is two tiles of up to 128 rows of
+// one sequence and one key/value head: row R of a tile is token R / group, query head R % group, so
+// all query heads of a key/value head share the K and V that are loaded once, and a short prompt
+// still fills the tiles.  Per 128 positions and tile:
 //   S = Q K^T    128 x 128 x D, both operands in shared memory, S in TMEM
-//   softmax      four warps, one row a thread: S from TMEM to registers, P back over S in 16 bits
+//   softmax      four warps, one row a thread: S from TMEM to registers, P to TMEM in 16 bits
 //   O += P V     128 x D x 128, P from TMEM, V from shared memory, O in TMEM
 // The two tiles take turns: while four warps are at one tile's softmax, the tensor cores work on
-// the other tile.  One thread issues all products in the order S0 S1 | PV0 S0' | PV1 S1' | ..., they
-// complete in that order, and one commit after S0' therefore also says that PV0 is done.
-// O is only scaled down when a row's maximum has grown by more than 2^8 since O's last scale; the
-// weights then stay below 2^8, which 16-bit floats and the fp32 sums hold without loss.
+// the other tile.  One warp issues all products, in an order in which they also complete, one finds
+// the items, one copies.  O is only scaled down when a row's maximum has grown by more than 2^8 since
+// O's last scale; the weights then stay below 2^8, which 16-bit floats and the fp32 sums hold
+// without loss.
+//
+// One persistent CTA an SM.  Measured (32 query, 8 key/value heads of 128, bf16, 8192 tokens, causal):
+// 2567 us with 64-row tiles on mma.sync, 496 us with one CTA per two tiles, 374 us when the
+// products' loop is uniform in its warp (descriptors in a one-lane branch cost 100 cycles a product),
+// 353 us with the work shared evenly (1.56 PFLOP/s).  A step of 128 positions takes 2650 cycles, the
+// products 2048 of them at the peak rate: with both operands in shared memory S runs at 128 bytes a
+// cycle, the limit, and takes about 90 cycles instead of 64 a product.  Sixteen softmax warps of half
+// a row a thread were slower (403 us to 374), and so was a ring of four tiles (455 us to 356).
 #pragma once
 
 #include "moe_attention.cuh"
@@ -41,8 +49,8 @@ struct Prompt {
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
   static constexpr int kColumns = 512;                        // S0 S1 (128 each) O0 O1 (D each)
   // Heads of 64 leave TMEM room for P beside S: the next S is then computed as soon as the last one
-  // has been read, and only the softmax bounds the step (measured: 16 heads of 64, two chunks behind prefixes: 168 -> 132 us, with the even sharing).  With heads
-  // of 128, P lies over S, and S waits for P V.
+  // has been read, and the softmax bounds the step.  With heads of 128, P lies over S, and S waits
+  // for P V.
   static constexpr bool kBeside = D == 64;
   static constexpr int kParts = kBeside ? 1 : 2;              // in which P goes to the tensor cores
 };
@@ -58,10 +66,11 @@ struct PromptParams {
 
 // ------------------------------------------------------------------ who does what
 // An item is one sequence, one key/value head and two tiles of rows; its cost is the positions that
-// its last row sees (all, with tree masks), and kItemCost for its beginning and end.  The costs of all items, sequence by
-// sequence, head by head, form one line that the CTAs share evenly, whatever the lengths are; a
-// boundary inside an item becomes a boundary between two of its steps, or moves to the item's edge
-// when fewer than kMinSteps steps would be cut off.
+// its last row sees (all, with tree masks), and kItemCost for its beginning and end.  The costs of all
+// items, sequence by sequence, head by head, form one line that the CTAs share evenly, whatever the
+// lengths are; a boundary inside an item becomes a boundary between two of its steps, or moves to
+// the item's edge when fewer than kMinSteps steps would be cut off.  (16 packed prompts of 62 to 1984
+// tokens, cost 160, 224, 320: 96.9, 94.7, 96.3 us; least 2, 4 steps: 93.5, 94.7.)
 constexpr int kItemCost = 224;
 constexpr int kMinSteps = 2;
 

@@ -116,9 +116,11 @@ def test_large_trees_behind_long_contexts(Hq, Hkv, D):
     lens, ctxs = [64, 33, 5, 64, 64], [20010, 5120, 127, 0, 5100]
     b = C.batch(Hq + D, lens, ctxs, Hq, Hkv, D, 64, F16)
     masks = tree_masks(D, lens, False)
-    masks[3] = masks[70] = 0
+    masks[3] = masks[70] = masks[110] = 0   # the last one has no context either
     ref, tol = b.reference(D ** -0.5, masks)
-    C.assert_within(run_tree(b, 64, masks), ref, tol)
+    out = run_tree(b, 64, masks)
+    C.assert_within(out, ref, tol)
+    assert not bool(out[110].any()) and bool(out[70].any())
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (6, 1, 128)])
@@ -353,3 +355,41 @@ def test_two_streams_and_repeats(kind):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind,max_q", [("tree", 2), ("tree", 40), ("prompt", 0)])
+def test_workspaces(kind, max_q):
+    """A caller's workspace, filled with anything, does; one that is too small is refused and nothing is
+    written."""
+    b = C.batch(71, [2, 40 if max_q != 2 else 1], [3000, 900], 8, 2, 128, 16, BF16)
+    cache = Bn.KvCache(b.k, b.v)
+    out = torch.full_like(b.q, 5.0)
+
+    def call(ws):
+        if kind == "tree":
+            return Bn.tree_attention(cache, b.q, b.cu, b.ctx, b.table, max_q, workspace=ws, out=out)
+        return Bn.prompt_attention(cache, b.q, b.cu, b.ctx, b.table, workspace=ws, out=out)
+
+    for n in (0, 4096):
+        with pytest.raises(Bn.MoeError) as e:
+            call(torch.zeros(n, dtype=torch.uint8, device="cuda"))
+        assert e.value.rc == Bn.MOE_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert bool((out == 5).all())
+    ref, tol = b.reference(128 ** -0.5)
+    for fill in (0, 255, 127):
+        ws = torch.full((1 << 27,), fill, dtype=torch.uint8, device="cuda")
+        C.assert_within(call(ws), ref, tol)
+        C.assert_within(call(ws), ref, tol)
+
+
+def test_a_table_longer_than_the_sequences():
+    """The table's width bounds the lengths; entries that no sequence uses are not read."""
+    lens, ctxs = [3, 40], [100, 20]
+    b = C.batch(72, lens, ctxs, 4, 2, 64, 16, BF16)
+    wide = torch.full((2, 4000), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    ref, tol = b.reference(0.125)
+    C.assert_within(run_tree(b, 40), ref, tol)
+    C.assert_within(run_prompt(b), ref, tol)
