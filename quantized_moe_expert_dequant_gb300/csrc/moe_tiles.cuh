@@ -14,8 +14,8 @@
 //   O += P V     128 x D x 128, P from TMEM, V from shared memory, O in TMEM
 // The two tiles take turns: while four warps are at one tile's softmax, the tensor cores work on
 // the other tile.  One warp issues all products, in an order in which they also complete, one finds
-// the items, one copies.  O is only scaled down when a row's maximum has grown by more than 2^8 since
-// O's last scale; the weights then stay below 2^8, which 16-bit floats and the fp32 sums hold
+// the items, one copies.  O is only scaled down when a row's weights, relative to an older
+// maximum, add up to more than 2^13 in a step; up to there 16-bit floats and the fp32 sums hold them
 // without loss.
 //
 // One persistent CTA an SM.  Measured (32 query, 8 key/value heads of 128, bf16, 8192 tokens, causal):
@@ -40,7 +40,7 @@ constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // and products, copie
 // 168 registers at launch; 2 x 128 x 216 + 128 x 72 = 384 x 168
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kItems = 4;               // items between the warp that finds them and the others
-constexpr float kGrowth = 8.f;          // log2 of how far a maximum may grow before O is rescaled
+constexpr float kMostWeight = 8192.f;   // sum of a row's weights in a step from which O is rescaled
 
 template <int D>
 struct Prompt {
@@ -52,7 +52,6 @@ struct Prompt {
   // has been read, and the softmax bounds the step.  With heads of 128, P lies over S, and S waits
   // for P V.
   static constexpr bool kBeside = D == 64;
-  static constexpr int kParts = kBeside ? 1 : 2;              // in which P goes to the tensor cores
 };
 
 struct PromptParams {
@@ -291,13 +290,11 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[4][32]) {
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
-// The weights exp2(scale * x - off) of 32 positions: their pairs in 16 bits in y, added to sum; the
-// maxima of `also` (64 positions) on the side, since the exponentials (4 cycles a warp) leave issue
-// slots free.  Eight positions at a time, the use of each eight one group behind their exponentials.
-template <typename T, bool MAX>
+// The weights exp2(scale * x - off) of 32 positions: their pairs in 16 bits in y, added to sum.  Eight
+// positions at a time, the use of each eight one group behind their exponentials.
+template <typename T>
 __device__ __forceinline__ void weights(const uint32_t (&x)[32], float off, float scale,
-                                        uint64_t (&sum)[2], uint32_t (&y)[16], float (&top)[4],
-                                        const uint32_t (&also0)[32], const uint32_t (&also1)[32]) {
+                                        uint64_t (&sum)[2], uint32_t (&y)[16]) {
   const uint64_t sc = pair(scale, scale), shift = pair(-off, -off);
   float w[2][8];
 #pragma unroll
@@ -309,16 +306,6 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float off, floa
             pair(__uint_as_float(x[8 * g + e]), __uint_as_float(x[8 * g + e + 1])), sc, shift));
         w[g & 1][e] = exp2_approx(a.x);
         w[g & 1][e + 1] = exp2_approx(a.y);
-      }
-      if (MAX) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const int k = 8 * g + e;
-          top[e / 2 % 2] =
-              max3(top[e / 2 % 2], __uint_as_float(also0[k]), __uint_as_float(also0[k + 1]));
-          top[2 + e / 2 % 2] =
-              max3(top[2 + e / 2 % 2], __uint_as_float(also1[k]), __uint_as_float(also1[k + 1]));
-        }
       }
     }
     if (g > 0) {
@@ -334,13 +321,28 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float off, floa
   }
 }
 
+// The weights of a row's 128 positions, stored to TMEM at tp; their sum.
+template <typename T>
+__device__ __forceinline__ float store_weights(const uint32_t (&x)[4][32], float off, float scale,
+                                               uint32_t tp) {
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[16];
+    weights<T>(x[c], off, scale, sum, y);
+    tc::tmem_store16(tp + 16 * c, y);
+  }
+  const float2 total = unpair(add2(sum[0], sum[1]));
+  return total.x + total.y;
+}
+
 template <typename T, int D, bool tree>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams w) {
   using C = Prompt<D>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t s_q[2], s_q_free[2], s_full[C::kStages], s_empty[C::kStages],
-      s_s[2], s_x[2], s_p[2][2], s_o[2], s_end, s_item_full[kItems], s_item_free[kItems];
+      s_s[2], s_x[2], s_p[2], s_o[2], s_end, s_item_full[kItems], s_item_free[kItems];
   __shared__ Item s_item[kItems];
   __shared__ int64_t s_warp[kPromptThreads / 32];
   __shared__ Spot s_spot[2];
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::bar_init(bar(s_q_free[i]), 1);
       tc::bar_init(bar(s_s[i]), 1);
       tc::bar_init(bar(s_x[i]), kSoftmaxWarps / 2);
-      for (int h = 0; h < 2; ++h) tc::bar_init(bar(s_p[i][h]), kSoftmaxWarps / 2);
+      tc::bar_init(bar(s_p[i]), kSoftmaxWarps / 2);
       tc::bar_init(bar(s_o[i]), 1);
     }
     for (int i = 0; i < C::kStages; ++i) {
@@ -574,16 +576,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         const auto add_pv = [&](int i) {
           if (t < u[i]) {
+            wait(bar(s_p[i]), n_p[i] & 1);
+            tc::fence_after();
 #pragma unroll
-            for (int h = 0; h < C::kParts; ++h) {
-              wait(bar(s_p[i][h]), n_p[i] & 1);
-              tc::fence_after();
-              constexpr int kPart = kPos / 16 / C::kParts;
-#pragma unroll
-              for (int kk = kPart * h; kk < kPart * h + kPart; ++kk)
-                tc::mma_tmem(one, tm + 2 * kPos + i * D, tm + p_col(i) + kk * 8, v_lo + kk * 128, hi,
-                             i_o, t > 0 || kk > 0);
-            }
+            for (int kk = 0; kk < kPos / 16; ++kk)
+              tc::mma_tmem(one, tm + 2 * kPos + i * D, tm + p_col(i) + kk * 8, v_lo + kk * 128, hi,
+                           i_o, t > 0 || kk > 0);
             if (C::kBeside || t == u[i] - 1) tc::mma_commit(one, bar(s_o[i]));
           }
         };
@@ -663,7 +661,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           if (lane == 0) {
             if (C::kBeside) tc::bar_arrive(bar(s_x[i]));
-            for (int h = 0; h < C::kParts; ++h) tc::bar_arrive(bar(s_p[i][h]));
+            tc::bar_arrive(bar(s_p[i]));
           }
           continue;
         }
@@ -701,21 +699,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (32 * c + e >= see) x[c][e] = __float_as_uint(kNegInf);
         }
-        // The weights are taken relative to m, a maximum of earlier steps, while this step's maximum is
-        // found; only if some row's has outgrown m is O scaled down and the work done again.  With
-        // P over S, the first half of it goes to the tensor cores while the second is computed.
+        // The weights are taken relative to m, the maximum of the first step: whatever reference they
+        // are taken to divides out.  Only when their sum shows that some row has outgrown m (no
+        // weight is larger than the sum) is a new maximum found, O scaled down, and the work done
+        // again; finding the maximum in every step took 450 of 1250 cycles.
         // A row that has seen nothing yet (a later piece of an item, a tree without context) has no m.
         if (t == 0 || (tree && __any_sync(0xffffffffu, m == kNegInf))) {
           const float top = row_max(x);
           if (m == kNegInf) m = top;
         }
         const float ref = m == kNegInf ? 0.f : m;
-        uint64_t sum[2] = {0ull, 0ull};
-        uint32_t y0[16], y1[16];
-        float tops[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-        float off = ref * p.scale_log2;
-        weights<T, true>(x[0], off, p.scale_log2, sum, y0, tops, x[0], x[1]);
-        weights<T, true>(x[1], off, p.scale_log2, sum, y1, tops, x[2], x[3]);
         if (C::kBeside && t > 0) {  // the last step's product has read P and written O
           ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
           ++n_o;
@@ -723,13 +716,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (!ok) break;
           tc::fence_after();
         }
-        const float up = fmaxf(ref, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-        if (__any_sync(0xffffffffu, (up - ref) * p.scale_log2 > kGrowth)) {
+        float add = store_weights<T>(x, ref * p.scale_log2, p.scale_log2, tp);
+        if (__any_sync(0xffffffffu, add > kMostWeight)) {
+          const float up = fmaxf(ref, row_max(x));
           const float f = exp2_approx((ref - up) * p.scale_log2);
           if (m != kNegInf) m = up;
           l *= f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; t > 0 && c < D / 32; ++c) {
             uint32_t o[32];
             tc::tmem_load32(o, to + 32 * c);
             tc::wait_load(o);
@@ -737,27 +731,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tc::tmem_store32(to + 32 * c, o);
           }
-          sum[0] = sum[1] = 0ull;
-          off = up * p.scale_log2;
-          weights<T, false>(x[0], off, p.scale_log2, sum, y0, tops, x[0], x[1]);
-          weights<T, false>(x[1], off, p.scale_log2, sum, y1, tops, x[2], x[3]);
+          add = store_weights<T>(x, up * p.scale_log2, p.scale_log2, tp);
         }
-        const auto hand_over = [&](int part) {  // what has been stored is for the tensor cores
-          tc::wait_store();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(bar(s_p[i][part]));
-        };
-        tc::tmem_store16(tp, y0);
-        tc::tmem_store16(tp + 16, y1);
-        if (C::kParts == 2) hand_over(0);
-        weights<T, false>(x[2], off, p.scale_log2, sum, y0, tops, x[0], x[1]);
-        weights<T, false>(x[3], off, p.scale_log2, sum, y1, tops, x[0], x[1]);
-        tc::tmem_store16(tp + 32, y0);
-        tc::tmem_store16(tp + 48, y1);
-        hand_over(C::kParts - 1);
-        const float2 total = unpair(add2(sum[0], sum[1]));
-        l += total.x + total.y;
+        l += add;
+        tc::wait_store();  // P is for the tensor cores
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar(s_p[i]));
       }
       if (!ok) break;
       ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);

@@ -13,7 +13,7 @@ kernels.  ``attention`` also returns, per output element, how far a kernel may b
                     shifted (exponents of size x: 2^-23 x) and raised by ex2.approx (2^-22)
   2 n 2^-23 A       sums of n weights and weighted values in fp32
   n 2^-25 max|v|    fp16 only: weights below 2^-14 are subnormal (the divisor is at least about 1);
-                    weights are taken relative to a maximum that may be 2^8 below the largest
+                    weights are taken relative to a maximum that may be 2^13 below the largest
 """
 from __future__ import annotations
 
