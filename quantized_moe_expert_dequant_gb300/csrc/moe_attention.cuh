@@ -205,17 +205,19 @@ inline int check_attention(const moe_kv_cache *c, const moe_attention *a, Params
   return MOE_OK;
 }
 
-// Raises a kernel's limit of dynamic shared memory, once per device (a call of the runtime takes about
+// Raises a kernel's limits of dynamic shared memory and cluster size, once per device (a call of the runtime takes about
 // a microsecond).
 struct SmemLimit {
   std::atomic<uint64_t> done{0};
-  cudaError_t set(const void *kernel, int bytes) {
+  cudaError_t set(const void *kernel, int bytes, bool large_clusters = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && large_clusters)  // more than 8 CTAs
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
   }

@@ -362,6 +362,9 @@ def test_workspaces(kind, max_q):
     """A caller's workspace, filled with anything, does; one that is too small is refused and nothing is
     written."""
     b = C.batch(71, [2, 40 if max_q != 2 else 1], [3000, 900], 8, 2, 128, 16, BF16)
+    wide = torch.zeros((2, 4000), dtype=torch.int32, device="cuda")  # too long for clusters
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
     cache = Bn.KvCache(b.k, b.v)
     out = torch.full_like(b.q, 5.0)
 
@@ -381,6 +384,23 @@ def test_workspaces(kind, max_q):
         ws = torch.full((1 << 27,), fill, dtype=torch.uint8, device="cuda")
         C.assert_within(call(ws), ref, tol)
         C.assert_within(call(ws), ref, tol)
+
+
+@pytest.mark.parametrize("n,Hkv", [(1, 1), (1, 19), (2, 10), (3, 6), (19, 2), (20, 2), (38, 1), (39, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_items(n, Hkv, D):
+    """Around the counts of items from which clusters of 16 and of 8 CTAs give way to the shared line;
+    sequences shorter than a cluster has tiles, without rows, without context."""
+    lens = [1 + i % 3 for i in range(n)]
+    ctxs = [(0, 3, 700, 64, 2500)[i % 5] for i in range(n)]
+    if n > 2:
+        lens[1] = 0
+    b = C.batch(n + D, lens, ctxs, 5 * Hkv, Hkv, D, 32, F16 if n % 2 else BF16)
+    masks = tree_masks(n, lens)
+    ref, tol = b.reference(D ** -0.5, masks)
+    C.assert_within(run_tree(b, 3, masks), ref, tol)
+    one = run_tree(b, 3, masks)
+    assert torch.equal(one.view(torch.int16), run_tree(b, 3, masks).view(torch.int16))
 
 
 def test_a_table_longer_than_the_sequences():
