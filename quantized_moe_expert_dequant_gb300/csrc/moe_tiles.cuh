@@ -72,6 +72,11 @@ struct PromptParams {
 // tokens, cost 160, 224, 320: 96.9, 94.7, 96.3 us; least 2, 4 steps: 93.5, 94.7.)
 constexpr int kItemCost = 224;
 constexpr int kMinSteps = 2;
+// Steps of the longest item that the table allows, from which items are shared at all: below, a boundary
+// moves to the nearer edge of its item, and no parts are joined.  (32 query, 8 key/value heads of 128,
+// us shared and not: one prompt of 700 tokens 21.6, 18.2; of 1000 27.3, 21.1; of 2000 43.7, 46.8; of
+// 4000 105, 121; 16 of 1000 147, 143.)
+constexpr int kShareSteps = 9;
 
 struct Spot {  // the place before a step of an item
   int seq, head, tile, step;
@@ -109,7 +114,8 @@ __device__ __forceinline__ int item_steps(const Seq &s, bool tree, int per, int 
 }
 __device__ __forceinline__ int item_count(const Seq &s, int per) { return (s.nq + per - 1) / per; }
 
-__device__ __forceinline__ Spot spot_at(const Seq &s, bool tree, int seq, int per, int64_t y) {
+__device__ __forceinline__ Spot spot_at(const Seq &s, bool tree, bool shared, int seq, int per,
+                                        int64_t y) {
   const int tiles = item_count(s, per);
   const int64_t whole = head_cost(s, tree, per, tiles, tiles);
   Spot r;
@@ -126,6 +132,7 @@ __device__ __forceinline__ Spot spot_at(const Seq &s, bool tree, int seq, int pe
   const int64_t at = head_cost(s, tree, per, tiles, k), cost = head_cost(s, tree, per, tiles, k + 1) - at;
   const int n = item_steps(s, tree, per, k);
   int step = static_cast<int>((y - at) * n / cost);
+  if (!shared) step = 2 * (y - at) < cost ? 0 : n;  // the nearer edge
   if (step < kMinSteps) step = 0;
   r.tile = k;
   r.step = step;
@@ -156,8 +163,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 }
 
 // The CTA's part of the line: from s_spot[0] to s_spot[1].  False when there is nothing at all.
-__device__ __forceinline__ bool find_part(const Params &p, bool tree, int per, int64_t *s_warp,
-                                          Spot *s_spot) {
+__device__ __forceinline__ bool find_part(const Params &p, bool tree, bool shared, int per,
+                                          int64_t *s_warp, Spot *s_spot) {
   const auto cost = [&](const Seq &s) {
     if (s.nq == 0) return static_cast<int64_t>(0);
     const int tiles = item_count(s, per);
@@ -187,7 +194,7 @@ __device__ __forceinline__ bool find_part(const Params &p, bool tree, int per, i
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (below <= edge[e] && edge[e] < below + mine)
-        s_spot[e] = spot_at(s, tree, i, per, edge[e] - below);
+        s_spot[e] = spot_at(s, tree, shared, i, per, edge[e] - below);
   }
   __syncthreads();
   return true;
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     tc::bar_fence_init();
   }
   pdl_launch();
-  const bool any = find_part(p, tree, 2 * w.tokens, s_warp, s_spot);
+  const bool any = find_part(p, tree, w.share != nullptr, 2 * w.tokens, s_warp, s_spot);
   if (w.share && threadIdx.x == 0) {
     Share sh = {};
     if (any && before(s_spot[0], s_spot[1])) {
@@ -904,7 +911,7 @@ static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan) {
   // the line's length times the CTAs stays inside 64 bits
   const double items = static_cast<double>(p.n_rows) / (2 * (128 / p.group)) + p.n_seqs;
   if (items * (static_cast<double>(len) + kItemCost) * p.hkv * sms > 4e18) return MOE_ERR_UNSUPPORTED;
-  if ((len + kPos - 1) / kPos < 2 * kMinSteps) return MOE_OK;  // no item is ever shared
+  if ((len + kPos - 1) / kPos < kShareSteps) return MOE_OK;
   plan->ml = 4ll * 2 * plan->grid * 256 * c->head_dim;
   plan->share = plan->ml + 8ll * 2 * plan->grid * 256;
   plan->bytes = plan->share + static_cast<int64_t>(sizeof(Share)) * plan->grid;
