@@ -131,6 +131,32 @@ def test_prompts_that_many_ctas_share(Hq, Hkv, D):
     C.assert_within(run_prompt(b), ref, tol)
 
 
+@pytest.mark.parametrize("group", [33, 40, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_query_heads_on_one(group, D):
+    lens, ctxs = [1, 30, 5], [77, 0, 1300]
+    b = C.batch(group + D, lens, ctxs, group, 1, D, 16, BF16)
+    ref, tol = b.reference(D ** -0.5)
+    C.assert_within(run_prompt(b), ref, tol)
+    C.assert_within(run_tree(b, 30), ref, tol)
+    masks = tree_masks(group, lens, False)
+    ref, tol = b.reference(D ** -0.5, masks)
+    C.assert_within(run_tree(b, 30, masks), ref, tol)
+
+
+@pytest.mark.parametrize("kind,max_q", [("tree", 2), ("tree", 30), ("prompt", 0)])
+def test_rows_before_the_first_sequence_stay(kind, max_q):
+    b = C.batch(81, [2, 30 if max_q != 2 else 1], [40, 3], 4, 2, 64, 16, BF16, pad_rows=5)
+    rows = b.q.shape[0] - 5
+    ref, tol = b.reference(0.125)
+    shifted = torch.cat([torch.full_like(b.q[:5], float("nan")), b.q[:rows]])
+    out = torch.full_like(shifted, 5.0)
+    moved = C.Batch(b.k, b.v, shifted, b.cu + 5, b.ctx, b.table, b.lens, b.ctxs)
+    run_tree(moved, max_q, out=out) if kind == "tree" else run_prompt(moved, out=out)
+    C.assert_within(out[5:], ref[:rows], tol[:rows])
+    assert bool((out[:5] == 5).all())
+
+
 def test_many_prompts():
     gen = torch.Generator().manual_seed(9)
     n = 900
