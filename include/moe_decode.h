@@ -357,9 +357,9 @@ int moe_qk_norm_rope(const moe_kv_cache *cache, const moe_norm_rope *args, void 
  * Scores, maxima, sums and the weighted sum are fp32; the weights enter the product with v in the
  * cache's dtype; out is rounded once.  A query that sees nothing gets zeros.  Rows behind
  * cu_q[n_seqs] are neither read nor written.  What pages hold beyond a sequence's positions may be
- * anything; K and V of its positions have to be finite.  More than 32 rows (queries times query heads) a key/value head, and all
- * prompts, are copied by tensor maps: strides that those do not take (0 over more than one head,
- * position or page, or 2^40 bytes) return MOE_ERR_UNSUPPORTED. */
+ * anything; K and V of its positions have to be finite.  More than 32 rows (queries times
+ * query heads) a key/value head, and all prompts, are copied by tensor maps: strides that those do
+ * not take (0 over more than one head, position or page, or 2^40 bytes) return MOE_ERR_UNSUPPORTED. */
 typedef struct moe_attention {
   const void *q;           /* [n_rows][n_q_heads][head_dim], cache dtype, 16-byte aligned */
   void *out;               /* likewise; must not overlap q */

@@ -26,7 +26,8 @@ LIB_TIMELINE = os.path.join(PKG, "libmoe_decode_timeline.so")
 SOURCES = ["moe_kernels_g4.cu", "moe_kernels_g6.cu", "moe_kernels_g8.cu", "moe_grouped_g4.cu",
            "moe_grouped_g6.cu", "moe_grouped_g8.cu", "moe_cols_g4.cu", "moe_cols_g6.cu",
            "moe_cols_g8.cu", "moe_kernels.cu", "moe_mma.cu",
-           "moe_api.cu", "moe_pack.cpp", "synth.cu", "gemv.cu", "moe_rope.cu", "moe_prompt.cu", "moe_prompt_tree.cu",
+           "moe_api.cu", "moe_pack.cpp", "synth.cu", "gemv.cu", "moe_rope.cu",
+           "moe_prompt.cu", "moe_prompt_tree.cu",
            "moe_tree.cu", "moe_tree_cluster.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

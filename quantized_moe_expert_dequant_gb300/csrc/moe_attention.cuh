@@ -205,8 +205,8 @@ inline int check_attention(const moe_kv_cache *c, const moe_attention *a, Params
   return MOE_OK;
 }
 
-// Raises a kernel's limits of dynamic shared memory and cluster size, once per device (a call of the runtime takes about
-// a microsecond).
+// Raises a kernel's limits of dynamic shared memory and cluster size, once per device (a call of the
+// runtime takes about a microsecond).
 struct SmemLimit {
   std::atomic<uint64_t> done{0};
   cudaError_t set(const void *kernel, int bytes, bool large_clusters = false) {

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocksPerSm) norm_rope_kernel(co
   const bool live = t < per;
   const int kind = h < p.hq ? 0 : h < p.hq + p.hkv ? 1 : 2;  // query, key, value
   const int head = h - (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv);
-  const int lanes = p.rot / 16;  // of a head that turn something; angle f is the (f % 8)-th of lane f / 8
+  const int lanes = p.rot / 16;  // of a head that turn something; lane j has angles 8 j .. 8 j + 7
   const bool turned = kind < 2 && l < lanes;
   int ca = 2 * l, cb = 2 * l + 1;
   if (!p.interleaved && l < lanes) ca = l, cb = l + lanes;

@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     const Seq q = load_seq(p, s_seq, false);
     ld.left = static_cast<int>(end - at);
     ld.seq = s_seq, ld.len = q.len, ld.nt = (q.len + kTile - 1) / kTile;
-    ld.kvh = static_cast<int>(in_seq / ld.nt), ld.t = static_cast<int>(in_seq - static_cast<int64_t>(ld.kvh) * ld.nt);
+    ld.kvh = static_cast<int>(in_seq / ld.nt);
+    ld.t = static_cast<int>(in_seq - static_cast<int64_t>(ld.kvh) * ld.nt);
     ld.stage = 0;
     ld.pages = p.table + ld.seq * p.table_stride;
     ld.head_off = ld.kvh * p.head_stride;
