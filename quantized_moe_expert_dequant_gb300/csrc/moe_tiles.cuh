@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (C::kBeside) {
           next_s(0);
           next_s(1);
-          turn_ring();
           add_pv(0);
+          turn_ring();
           add_pv(1);
         } else {
           add_pv(0);
