@@ -572,6 +572,7 @@ class KvCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.device, self.dtype = k.device, k.dtype
         self._dev = k.get_device()
+        self._heads = (self.n_kv_heads, self.head_dim)
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
         self._c = _pack_kv_cache(k.data_ptr(), v.data_ptr(), *st, self.n_pages, self.page_size,
                                  self.n_kv_heads, self.head_dim, _DTYPES[k.dtype])
@@ -584,22 +585,36 @@ def qk_norm_rope(cache: KvCache, q, k, v, positions, slots, inv_freq, q_weight=N
     cache's dtype), writes k and v [T, Hkv, D] to their slots (int32 [T]; negative: padding) in
     the cache and returns q_out [T, Hq, D] in the cache's dtype.  positions int32 [T], inv_freq fp64
     [rot_dim / 2] (None: no rotation), weights [D] in the cache's dtype or None: no norm."""
-    T, Hq, D = q.shape
-    dev, dt, to, kv = cache._dev, q.dtype, cache.dtype, (T, cache.n_kv_heads, cache.head_dim)
+    shape = q.shape
+    T, Hq, D = shape
+    dev, dt, to, kv, i32 = cache._dev, q.dtype, cache.dtype, (T, *cache._heads), torch.int32
     if D != cache.head_dim or dt not in _DTYPES:
         raise ValueError(f"q: fp32 or {to} heads of {cache.head_dim} are wanted")
-    shape = (T, Hq, D)
     if q_out is None:
         q_out = _empty_on(shape, to, cache.device, stream)
-    a, b, c = _rows(q, shape, dt, dev, "q"), _rows(k, kv, dt, dev, "k"), _rows(v, kv, dt, dev, "v")
-    qo = _rows(q_out, shape, to, dev, "q_out")
-    i32 = torch.int32
+    # the checks of _rows and _vector in one expression for the calls that pass them: on small
+    # batches the host is what takes time
+    a, b, c, o = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if (a[2] == b[2] == c[2] == o[2] == 1 and k.shape == kv and v.shape == kv and k.dtype is dt
+            and v.dtype is dt and q_out.dtype is to and q_out.shape == shape
+            and q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == dev
+            and slots.dtype is i32 and slots.numel() >= T and slots.is_contiguous()
+            and slots.get_device() == dev):
+        ptrs = q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), slots.data_ptr()
+    else:
+        ptrs = (*(_rows(t, n, d, dev, name)[0] for t, n, d, name in (
+            (q, shape, dt, "q"), (k, kv, dt, "k"), (v, kv, dt, "v"), (q_out, shape, to, "q_out"))),
+            _vector(slots, i32, T, dev, "slots"))
+    many, heads, kv_heads = T > 1, Hq > 1, kv[1] > 1  # a dimension of extent 1 may have any stride
     args = _pack_norm_rope(
-        a[0], b[0], c[0], a[1], a[2], b[1], b[2], c[1], c[2], *qo,
-        _vector(q_weight, to, D, dev, "q_weight"), _vector(k_weight, to, D, dev, "k_weight"),
-        _vector(inv_freq, torch.float64, 1, dev, "inv_freq"),
-        _vector(positions, i32, T, dev, "positions"), _vector(slots, i32, T, dev, "slots"),
-        _vector(device_error, i32, 1, dev, "device_error"), T, Hq,
+        ptrs[0], ptrs[1], ptrs[2], a[0] if many else 0, a[1] if heads else 0, b[0] if many else 0,
+        b[1] if kv_heads else 0, c[0] if many else 0, c[1] if kv_heads else 0, ptrs[3],
+        o[0] if many else 0, o[1] if heads else 0,
+        0 if q_weight is None else _vector(q_weight, to, D, dev, "q_weight"),
+        0 if k_weight is None else _vector(k_weight, to, D, dev, "k_weight"),
+        0 if inv_freq is None else _vector(inv_freq, torch.float64, 1, dev, "inv_freq"),
+        _vector(positions, i32, T, dev, "positions"), ptrs[4],
+        0 if device_error is None else _vector(device_error, i32, 1, dev, "device_error"), T, Hq,
         0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, _DTYPES[dt], eps)
     _call("moe_qk_norm_rope", dev, stream, cache._c, args)
     return q_out

@@ -118,6 +118,24 @@ def test_bad_slots_are_reported():
     assert torch.equal(flat[[0, 1, 31]], v[[0, 2, 4]]) and bool((flat[2:31] == 3).all())
 
 
+def test_the_binding_refuses_other_tensors():
+    q, k, v, w, f = inputs(9, 5, 4, 2, 64, BF16, BF16, 64)
+    kc = torch.zeros((1, 2, 16, 64), dtype=BF16, device="cuda")
+    cache = Bn.KvCache(kc, kc.clone())
+    n = torch.arange(5, dtype=torch.int32, device="cuda")
+    good = dict(q=q, k=k, v=v, positions=n, slots=n, inv_freq=f)
+    Bn.qk_norm_rope(cache, **good)
+    bad = [dict(k=k[:4]), dict(k=k.half()), dict(v=v.cpu()), dict(v=v[:, :1]), dict(slots=n[:4]),
+           dict(slots=n.long()), dict(slots=n.cpu()), dict(positions=n[:4]), dict(q=q.double()),
+           dict(q=q[..., :32]), dict(inv_freq=f.float()), dict(q_weight=w[0].float()),
+           dict(k_weight=w[1][:32]), dict(q_out=torch.empty_like(q).half()),
+           dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
+           dict(slots=torch.zeros(10, dtype=torch.int32, device="cuda")[::2])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            Bn.qk_norm_rope(cache, **{**good, **kw})
+
+
 def test_no_tokens():
     q, k, v, w, f = inputs(8, 0, 4, 2, 64, BF16, BF16, 64)
     kc = torch.zeros((1, 2, 16, 64), dtype=BF16, device="cuda")
