@@ -3,7 +3,7 @@
 // (moe_prompt_tree.cu).
 //
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
-//   that row r sees, in one pass over K and V with a running maximum and sum.
+//   that row r sees, in one pass over K and V; m_r is a maximum of some of the scores.
 //
 // Bound by the two products (4 D flops per row and position).  An item is two tiles of up to 128 rows of
 // one sequence and one key/value head: row R of a tile is token R / group, query head R % group, so
@@ -21,10 +21,11 @@
 // One persistent CTA an SM.  Measured (32 query, 8 key/value heads of 128, bf16, 8192 tokens, causal):
 // 2567 us with 64-row tiles on mma.sync, 496 us with one CTA per two tiles, 374 us when the
 // products' loop is uniform in its warp (descriptors in a one-lane branch cost 100 cycles a product),
-// 353 us with the work shared evenly (1.56 PFLOP/s).  A step of 128 positions takes 2650 cycles, the
-// products 2048 of them at the peak rate: with both operands in shared memory S runs at 128 bytes a
-// cycle, the limit, and takes about 90 cycles instead of 64 a product.  Sixteen softmax warps of half
-// a row a thread were slower (403 us to 374), and so was a ring of four tiles (455 us to 356).
+// 348 us with the work shared evenly, 341 us without a maximum in every step (1.61 PFLOP/s).  A step of
+// 128 positions takes 2620 cycles, the products 2048 of them at the peak rate: with both operands in
+// shared memory S runs at 128 bytes a cycle, the limit, and takes about 90 cycles instead of 64 a
+// product.  Slower were sixteen softmax warps of half a row a thread (403 us to 374), a ring of four
+// tiles (455 to 356), and handing P over in halves once no maximum is in the way (409 to 342).
 #pragma once
 
 #include "moe_attention.cuh"
