@@ -726,6 +726,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         float add = store_weights<T>(x, ref * p.scale_log2, p.scale_log2, tp);
         if (__any_sync(0xffffffffu, add > kMostWeight)) {
+          tc::wait_store();  // P is written again below, and stores to TMEM have no order of their own
           const float up = fmaxf(ref, row_max(x));
           const float f = exp2_approx((ref - up) * p.scale_log2);
           if (m != kNegInf) m = up;

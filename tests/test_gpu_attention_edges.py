@@ -1,0 +1,42 @@
+"""Attention where its kernels can go wrong: references that the scores outgrow, rows that share a warp
+with others, queries that are not finite, weights far below the largest."""
+import pytest
+import torch
+
+from quantized_moe_expert_dequant_gb300 import binding as Bn
+from tests import attention_cases as C
+from tests.test_gpu_attention import mask_tensor, run_prompt, run_tree, tree_masks
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+bits = lambda t: t.view(torch.int16)
+
+
+def positions(b, i):
+    """(page, place in it) of the positions of sequence i."""
+    at = torch.arange(b.lens[i] + b.ctxs[i], device=b.k.device)
+    page = b.k.shape[2]
+    return b.table[i, at // page].long(), at % page
+
+
+@pytest.mark.parametrize("kind", ["tree", "prompt"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_that_outgrow_their_reference_in_every_step(kind, dtype, D):
+    """Scores rise by about 16 every 128 positions, so each step's weights are formed twice, first
+    relative to a reference that they exceed by a factor of e^16 (infinite in fp16)."""
+    lens, ctxs = [60, 33], [900, 400]
+    b = C.batch(D, lens, ctxs, 8, 2, D, 32, dtype, q_scale=0.2)
+    b.q[..., 0] = 4.0
+    for i in range(2):
+        pages, place = positions(b, i)
+        ramp = torch.arange(len(pages), device="cuda") / 32.0
+        b.k[pages, :, place, 0] = ramp[:, None].to(dtype)
+    masks = tree_masks(D, lens)
+    ref, tol = b.reference(1.0, masks if kind == "tree" else None)
+    run = (lambda: run_tree(b, 60, masks, 1.0)) if kind == "tree" else (lambda: run_prompt(b, 1.0))
+    out = run()
+    C.assert_within(out, ref, tol)
+    for _ in range(5):
+        assert torch.equal(bits(run()), bits(out))
