@@ -65,7 +65,10 @@ struct Work {
   Shared *shared;   // [G]
 };
 
+// All threads of the cluster's CTAs.  The aligned form wants converged warps, and the code before it may have
+// split them (half a warp of a tile's rows, the last of a loop).
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

@@ -40,3 +40,18 @@ def test_scores_that_outgrow_their_reference_in_every_step(kind, dtype, D):
     C.assert_within(out, ref, tol)
     for _ in range(5):
         assert torch.equal(bits(run()), bits(out))
+
+
+@pytest.mark.parametrize("group,max_q", [(1, 1), (3, 5), (7, 1), (16, 1), (5, 4), (11, 2), (16, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_clusters_whose_warps_split(group, max_q, D):
+    """A cluster an item with rows that leave lanes of a warp without work in the join, and CTAs without
+    tiles beside those that have some."""
+    lens, ctxs = [max_q, 1, max_q], [5, 64 * 7, 129]
+    b = C.batch(group * D, lens, ctxs, group, 1, D, 16, BF16)
+    masks = tree_masks(group, lens)
+    ref, tol = b.reference(D ** -0.5, masks)
+    out = run_tree(b, max_q, masks)
+    C.assert_within(out, ref, tol)
+    for _ in range(5):
+        assert torch.equal(bits(run_tree(b, max_q, masks)), bits(out))
