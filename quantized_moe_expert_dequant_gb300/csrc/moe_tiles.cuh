@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (!ok) break;
           tc::fence_after();
         }
+        __syncwarp();  // stores and loads of TMEM want converged warps
         float add = store_weights<T>(x, ref * p.scale_log2, p.scale_log2, tp);
         if (__any_sync(0xffffffffu, add > kMostWeight)) {
           tc::wait_store();  // P is written again below, and stores to TMEM have no order of their own
@@ -764,6 +765,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();
           tc::tmem_load32(o, to + 32 * c);
           tc::wait_load(o);
 #pragma unroll
@@ -791,6 +793,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 2
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32], v[4][4];
+          __syncwarp();
           tc::tmem_load32(o, to + 32 * c);
           tc::wait_load(o);
 #pragma unroll

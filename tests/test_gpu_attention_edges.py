@@ -55,3 +55,21 @@ def test_clusters_whose_warps_split(group, max_q, D):
     C.assert_within(out, ref, tol)
     for _ in range(5):
         assert torch.equal(bits(run_tree(b, max_q, masks)), bits(out))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(3, 1, 64), (10, 2, 128), (6, 1, 128), (14, 2, 64), (11, 1, 128)])
+@pytest.mark.parametrize("ctx", [0, 3000])
+def test_rows_that_do_not_fill_their_warps(Hq, Hkv, D, ctx):
+    """Groups that do not divide a tile's 128 rows, last tiles of a few rows; items that one CTA has whole
+    (short tables) and that several share (long ones)."""
+    lens, ctxs = [45, 64, 1, 23], [ctx, 17, 5, 300]
+    b = C.batch(Hq * D, lens, ctxs, Hq, Hkv, D, 64, BF16)
+    ref, tol = b.reference(D ** -0.5)
+    out = run_prompt(b)
+    C.assert_within(out, ref, tol)
+    assert torch.equal(bits(run_prompt(b)), bits(out))
+    masks = tree_masks(D, lens)
+    ref, tol = b.reference(D ** -0.5, masks)
+    out = run_tree(b, 64, masks)
+    C.assert_within(out, ref, tol)
+    assert torch.equal(bits(run_tree(b, 64, masks)), bits(out))
