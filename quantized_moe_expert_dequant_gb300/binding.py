@@ -44,7 +44,8 @@ EXPORTS = ["moe_decode_create", "moe_decode_forward", "moe_decode_get_error", "m
            "moe_synth_codes", "moe_synth_scales", "moe_synth_biases", "moe_route_invert_device",
            "moe_debug_wait_timeout", "moe_router_topk", "moe_debug_col_pieces",
            "moe_debug_col_plan", "moe_qk_norm_rope", "moe_tree_attention_workspace",
-           "moe_tree_attention", "moe_prompt_attention_workspace", "moe_prompt_attention"]
+           "moe_tree_attention", "moe_prompt_attention_workspace", "moe_prompt_attention",
+           "moe_debug_attention_wait_cycles"]
 
 
 class MoeError(RuntimeError):
@@ -138,6 +139,7 @@ def lib() -> ctypes.CDLL:
                 "moe_tree_attention": [vp, vp, vp, i32, vp, i64, vp],
                 "moe_prompt_attention_workspace": [vp, vp, vp],
                 "moe_prompt_attention": [vp, vp, vp, i64, vp],
+                "moe_debug_attention_wait_cycles": [i64],
             }
             if _timeline:
                 sig["moe_stack_timeline"] = [vp, vp, i64, ctypes.POINTER(i32)]
@@ -446,6 +448,11 @@ def debug_wait_timeout(kind: int, device_error: torch.Tensor, stream=None) -> No
     scratch = torch.zeros(1, dtype=torch.int32, device=device_error.device)
     check("moe_debug_wait_timeout", lib().moe_debug_wait_timeout(kind, _p(scratch), _p(device_error),
                                                                  _stream(stream)))
+
+
+def debug_attention_wait_cycles(cycles: int) -> None:
+    """The limit in cycles of the waits in attention kernels launched from now on (0: the usual)."""
+    check("moe_debug_attention_wait_cycles", lib().moe_debug_attention_wait_cycles(cycles))
 
 
 def router_topk(logits: torch.Tensor, top_k: int, stream=None):

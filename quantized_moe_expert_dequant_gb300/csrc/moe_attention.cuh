@@ -223,6 +223,9 @@ struct SmemLimit {
   }
 };
 
+// Limit of the tiles' waits in cycles; 0: the usual one (moe_debug_attention_wait_cycles).
+inline std::atomic<int64_t> debug_wait_cycles{0};
+
 // Attention in tiles of 128 rows on the 5th-generation tensor cores: causal, or by p.mask
 // (moe_prompt.cu, moe_prompt_tree.cu).
 int tiles_workspace(const moe_kv_cache *cache, const Params &p, int64_t *bytes);

@@ -40,3 +40,9 @@ extern "C" int moe_prompt_attention(const moe_kv_cache *cache, const moe_attenti
   if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
   return attn::run_tiles(cache, p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
+
+extern "C" int moe_debug_attention_wait_cycles(int64_t cycles) {
+  if (cycles < 0) return MOE_ERR_INVALID_ARG;
+  attn::debug_wait_cycles.store(cycles, std::memory_order_relaxed);
+  return MOE_OK;
+}

@@ -23,16 +23,16 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The hardware may suspend the thread, up to the hint of 0.1 ms, until the phase completes: a
+// The hardware may suspend the thread, up to about `ns` nanoseconds, until the phase completes: a
 // warp that waits then takes no issue slots from those that work.
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(100000u)
+      : "r"(bar), "r"(parity), "r"(ns)
       : "memory");
   return ok != 0;
 }
@@ -49,16 +49,20 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr long long kWaitCycles = 4000000000LL;  // about two seconds; a kernel's waits take microseconds
+struct Limit {  // of a wait: about two seconds, where a kernel's waits take microseconds
+  long long cycles = 4000000000LL;
+  uint32_t nap_ns = 100000u;  // what the hardware may suspend a thread for at a time
+};
 
-// Waits for the phase of that parity; false after kWaitCycles, or at once when another thread of the
+// Waits for the phase of that parity; false after the limit, or when another thread of the
 // CTA has given up (*gone), so that the kernel ends whatever happens.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gone) {
-  if (bar_try(bar, parity)) return true;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gone,
+                                         const Limit &limit) {
+  if (bar_try(bar, parity, limit.nap_ns)) return true;
   const long long t0 = clock64();
-  while (!bar_try(bar, parity)) {
+  while (!bar_try(bar, parity, limit.nap_ns)) {
     if (*gone) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > limit.cycles) {
       *gone = 1;
       return false;
     }

@@ -31,6 +31,7 @@
 #include "moe_attention.cuh"
 #include "moe_tcgen05.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace attn {
@@ -62,6 +63,7 @@ struct PromptParams {
   float *part;       // [2 G][2][D / 4][128][4]: parts of outputs, four columns of a tile's rows together
   float2 *part_ml;   // [2 G][2][128] (reference maximum, sum)
   struct Share *share;  // [G], null when no item can be shared
+  tc::Limit limit;      // of a wait
 };
 
 // ------------------------------------------------------------------ who does what
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   int taken = 0;  // items
   const auto take = [&](Item &item) {  // a whole warp; false: no more, or a wait gave up
     const int at = taken % kItems;
-    const bool ok = tc::bar_wait(bar(s_item_full[at]), (taken / kItems) & 1, &s_gone);
+    const bool ok = tc::bar_wait(bar(s_item_full[at]), (taken / kItems) & 1, &s_gone, w.limit);
     if (!__all_sync(0xffffffffu, ok)) return false;
     item = s_item[at];
     __syncwarp();
@@ -427,7 +429,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       Walk walk(p, tree, w.tokens, s_spot);
       for (int it = 0;; ++it) {
         const Item item = walk.next();
-        if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone)) break;
+        if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone, w.limit))
+          break;
         s_item[it % kItems] = item;
         tc::bar_arrive(bar(s_item_full[it % kItems]));
         if (!item.more) break;
@@ -442,6 +445,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int per_half = kPos / box_rows, boxes = per_half * (D / 64);
     const int b_row = (lane % per_half) * box_rows, half = lane / per_half;
     int issued = 0, q_loads[2] = {0, 0};  // tiles into the ring, tiles of Q
+    // The products' warp goes on to the end of its step when a wait of its has given up, and gives stages back
+    // whose copies are still under way: nothing is copied there then.
+    const auto free = [&](uint32_t b, int parity) {
+      return tc::bar_wait(b, parity, &s_gone, w.limit) && !*static_cast<volatile int *>(&s_gone);
+    };
     bool ok = true;
     Item item;
     while (ok && take(item)) {
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int st = issued % C::kStages;
-          ok = ok && tc::bar_wait(bar(s_empty[st]), ((issued / C::kStages) & 1) ^ 1, &s_gone);
+          ok = ok && free(bar(s_empty[st]), ((issued / C::kStages) & 1) ^ 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
           if (lane == 0) tc::bar_expect(bar(s_full[st]), C::kTileBytes);
@@ -476,7 +484,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (item.count[i] == 0) continue;
-            ok = ok && tc::bar_wait(bar(s_q_free[i]), (q_loads[i] & 1) ^ 1, &s_gone);
+            ok = ok && free(bar(s_q_free[i]), (q_loads[i] & 1) ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && lane == 0) {
               tc::bar_expect(bar(s_q[i]), static_cast<uint32_t>(w.tokens * p.group * D * 2));
@@ -490,14 +498,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         page = next_page;
       }
     }
-    if (s_gone) {  // let the copies under way land before the shared memory goes
-      volatile int never = 0;
-      for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
-        tc::bar_wait(bar(s_full[it % C::kStages]), (it / C::kStages) & 1, &never);
+    // The copies under way land before the shared memory goes: those that nobody waits for when some
+    // warp gives up, now or after this one has issued its last.
+    volatile int never = 0;
+    for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
+      tc::bar_wait(bar(s_full[it % C::kStages]), (it / C::kStages) & 1, &never, tc::Limit());
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (q_loads[i] > 0) tc::bar_wait(bar(s_q[i]), (q_loads[i] - 1) & 1, &never);
-    }
+    for (int i = 0; i < 2; ++i)
+      if (q_loads[i] > 0) tc::bar_wait(bar(s_q[i]), (q_loads[i] - 1) & 1, &never, tc::Limit());
   } else if (warp == kSoftmaxWarps) {
     // ---------------------------------------------------------------- products
     // Everything here is the same for all lanes (the shuffles say so to the compiler); `one` issues.
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // reads and writes this CTA's own shared memory and TMEM.  No branch depends on a wait, so that the
     // descriptors stay in uniform registers.
     const auto wait = [&](uint32_t b, int parity) {
-      if (!tc::bar_test(b, parity)) tc::bar_wait(b, parity, &s_gone);
+      if (!tc::bar_test(b, parity)) tc::bar_wait(b, parity, &s_gone, w.limit);
       __syncwarp();
     };
     const auto stage = [&](int i) { return ub + (2 + i) * C::kTileBytes; };
@@ -622,11 +630,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (gone) break;
       }
     }
-    if (s_gone) {  // let the products under way end before TMEM goes
-      volatile int never = 0;
-      tc::mma_commit(one, bar(s_end));
-      tc::bar_wait(bar(s_end), 0, &never);
-    }
+    // The products under way end before TMEM and the shared memory go, whoever gives up and when.
+    volatile int never = 0;
+    tc::mma_commit(one, bar(s_end));
+    tc::bar_wait(bar(s_end), 0, &never, tc::Limit());
+    __syncwarp();
   } else if (warp < kSoftmaxWarps) {
     // ---------------------------------------------------------------- softmax, one row a thread
     tc::regs_up<kSoftmaxRegs>();
@@ -656,13 +664,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (tree && tok < item.nq) row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
       float m = kNegInf, l = 0.f;
       for (int t = 0; t < n; ++t, ++n_s) {
-        ok = tc::bar_wait(bar(s_s[i]), n_s & 1, &s_gone);
+        ok = tc::bar_wait(bar(s_s[i]), n_s & 1, &s_gone, w.limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after();
         if (idle) {
           if (C::kBeside && t > 0) {  // its arrival for P must not count for the step before
-            ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
+            ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
             ++n_o;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -718,7 +726,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float ref = m == kNegInf ? 0.f : m;
         if (C::kBeside && t > 0) {  // the last step's product has read P and written O
-          ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
+          ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
           ++n_o;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -750,7 +758,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (lane == 0) tc::bar_arrive(bar(s_p[i]));
       }
       if (!ok) break;
-      ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
+      ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
       ++n_o;
       ok = __all_sync(0xffffffffu, ok && !s_gone);
       if (!ok) break;
@@ -932,6 +940,10 @@ static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan
   w.part = reinterpret_cast<float *>(ws);
   w.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
   w.share = plan.bytes ? reinterpret_cast<Share *>(ws + plan.share) : nullptr;
+  if (const int64_t cycles = debug_wait_cycles.load(std::memory_order_relaxed)) {
+    w.limit.cycles = cycles;
+    w.limit.nap_ns = static_cast<uint32_t>(std::min<int64_t>(cycles, w.limit.nap_ns));
+  }
   const bool bf16 = c->dtype == MOE_DTYPE_BF16;
   const uint64_t q_dims[3] = {D, static_cast<uint64_t>(p.hq), static_cast<uint64_t>(p.n_rows)};
   const int64_t q_str[2] = {p.q_head, p.q_row};

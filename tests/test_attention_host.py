@@ -173,3 +173,9 @@ def test_packed_bytes_have_the_layout_of_the_struct(pack, S):
     b = pack(*vals)
     s = S.from_buffer_copy(b + bytes(max(0, ctypes.sizeof(S) - len(b))))
     assert [getattr(s, n) for n, _ in S._fields_] == vals
+
+
+def test_wait_limits(L):
+    assert L.moe_debug_attention_wait_cycles(-1) == INV
+    assert L.moe_debug_attention_wait_cycles(1000) == Bn.MOE_OK
+    assert L.moe_debug_attention_wait_cycles(0) == Bn.MOE_OK

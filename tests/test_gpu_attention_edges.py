@@ -73,3 +73,39 @@ def test_rows_that_do_not_fill_their_warps(Hq, Hkv, D, ctx):
     out = run_tree(b, 64, masks)
     C.assert_within(out, ref, tol)
     assert torch.equal(bits(run_tree(b, 64, masks)), bits(out))
+
+
+@pytest.mark.parametrize("kind", ["tree", "prompt"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_that_give_up(kind, D):
+    """A limit shorter than the kernel's ordinary waits: at some of them it gives up, with copies and products
+    under way or without, reports that in the error word and ends; calls with the usual limit are
+    right again.  Nothing is out of order on the device, only out of time."""
+    lens, ctxs = [60, 33], [3000, 5000]
+    b = C.batch(D, lens, ctxs, 8, 2, D, 32, BF16)
+    cache = Bn.KvCache(b.k, b.v)
+    ref, tol = b.reference(D ** -0.5)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        err.zero_()
+        if kind == "tree":
+            out = Bn.tree_attention(cache, b.q, b.cu, b.ctx, b.table, 60, device_error=err)
+        else:
+            out = Bn.prompt_attention(cache, b.q, b.cu, b.ctx, b.table, device_error=err)
+        torch.cuda.synchronize()
+        return out, int(err)
+
+    C.assert_within(call()[0], ref, tol)
+    seen = []
+    try:
+        for cycles in (1, 200, 500, 1000, 1500, 2000, 2500, 3000, 4000, 6000, 10000):
+            Bn.debug_attention_wait_cycles(cycles)
+            for _ in range(4):
+                seen.append(call()[1])
+    finally:
+        Bn.debug_attention_wait_cycles(0)
+    assert set(seen) <= {0, 2} and set(seen[:4]) == {2}, seen
+    out, e = call()
+    assert e == 0
+    C.assert_within(out, ref, tol)
