@@ -548,19 +548,24 @@ def _entry(fn: str):
     return getattr(lib(), fn)
 
 
+def _on(dev: int, fn: str, *args) -> None:
+    """One library call with GPU `dev` current: launches and plans go by the current one."""
+    if torch._C._cuda_getDevice() == dev:
+        rc = _entry(fn)(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = _entry(fn)(*args)
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
+
+
 def _call(fn: str, dev: int, stream, *args) -> None:
     """One library call on `stream` (None: the current one of GPU `dev`) with that GPU current."""
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        rc = _entry(fn)(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = _entry(fn)(*args, stream)
-    if rc != MOE_OK:
-        raise MoeError(fn, rc)
+    _on(dev, fn, *args, stream)
 
 
 class KvCache:
@@ -650,9 +655,7 @@ def _workspace(fn: str, cache, workspace, stream, *args):
     """(address, bytes, tensor) of the caller's workspace, or of a new one as large as fn says."""
     if workspace is None:
         n = ctypes.c_int64()
-        rc = _entry(fn)(cache._c, *args, ctypes.byref(n))
-        if rc != MOE_OK:
-            raise MoeError(fn, rc)
+        _on(cache._dev, fn, cache._c, *args, ctypes.byref(n))
         if n.value == 0:
             return 0, 0, None
         workspace = _empty_on(n.value, torch.uint8, cache.device, stream)

@@ -179,3 +179,48 @@ def test_wait_limits(L):
     assert L.moe_debug_attention_wait_cycles(-1) == INV
     assert L.moe_debug_attention_wait_cycles(1000) == Bn.MOE_OK
     assert L.moe_debug_attention_wait_cycles(0) == Bn.MOE_OK
+
+
+@pytest.mark.parametrize("kind", ["tree", "prompt"])
+def test_every_call_is_made_with_the_caches_gpu_current(monkeypatch, kind):
+    """The workspace's size goes by the current GPU's SMs, as the launch does.  (No GPU here: the library,
+    the current device and the tensors' place are stand-ins.)"""
+    now, calls = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.dev
+
+        def __exit__(self, *e):
+            now[0] = self.before
+
+    class OnGpu1(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def entry(fn):
+        def call(*args):
+            calls.append((fn, now[0]))
+            if fn.endswith("_workspace"):
+                args[-1]._obj.value = 64
+            return Bn.MOE_OK
+        return call
+
+    monkeypatch.setattr(Bn, "_entry", entry)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    t = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype).as_subclass(OnGpu1)
+    c = type("Cache", (), dict(_dev=1, head_dim=64, dtype=torch.bfloat16, _c=b"", device="cpu"))()
+    q = t(1, 8, 64, dtype=torch.bfloat16)
+    args = (c, q, t(2), t(1), t(1, 4))
+    out = t(1, 8, 64, dtype=torch.bfloat16)
+    if kind == "tree":
+        Bn.tree_attention(*args, max_q=1, out=out)
+    else:
+        Bn.prompt_attention(*args, out=out)
+    name = f"moe_{kind}_attention"
+    assert calls == [(name + "_workspace", 1), (name, 1)] and now == [0]
