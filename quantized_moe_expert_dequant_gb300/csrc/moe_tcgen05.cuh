@@ -51,16 +51,20 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
 
 struct Limit {  // of a wait: about two seconds, where a kernel's waits take microseconds
   long long cycles = 4000000000LL;
-  uint32_t nap_ns = 100000u;  // what the hardware may suspend a thread for at a time
+  uint32_t nap_ns = 100000u;  // what the hardware may suspend a thread for at a time; 0: it polls
 };
 
 // Waits for the phase of that parity; false after the limit, or when another thread of the
 // CTA has given up (*gone), so that the kernel ends whatever happens.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gone,
                                          const Limit &limit) {
-  if (bar_try(bar, parity, limit.nap_ns)) return true;
+  // (a suspended thread sleeps longer than the shortest limits, whatever it asks for)
+  const auto done = [&]() {
+    return limit.nap_ns ? bar_try(bar, parity, limit.nap_ns) : bar_test(bar, parity);
+  };
+  if (done()) return true;
   const long long t0 = clock64();
-  while (!bar_try(bar, parity, limit.nap_ns)) {
+  while (!done()) {
     if (*gone) return false;
     if (clock64() - t0 > limit.cycles) {
       *gone = 1;

@@ -31,7 +31,6 @@
 #include "moe_attention.cuh"
 #include "moe_tcgen05.cuh"
 
-#include <algorithm>
 #include <type_traits>
 
 namespace attn {
@@ -940,10 +939,8 @@ static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan
   w.part = reinterpret_cast<float *>(ws);
   w.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
   w.share = plan.bytes ? reinterpret_cast<Share *>(ws + plan.share) : nullptr;
-  if (const int64_t cycles = debug_wait_cycles.load(std::memory_order_relaxed)) {
-    w.limit.cycles = cycles;
-    w.limit.nap_ns = static_cast<uint32_t>(std::min<int64_t>(cycles, w.limit.nap_ns));
-  }
+  if (const int64_t cycles = debug_wait_cycles.load(std::memory_order_relaxed))
+    w.limit.cycles = cycles, w.limit.nap_ns = 0;
   const bool bf16 = c->dtype == MOE_DTYPE_BF16;
   const uint64_t q_dims[3] = {D, static_cast<uint64_t>(p.hq), static_cast<uint64_t>(p.n_rows)};
   const int64_t q_str[2] = {p.q_head, p.q_row};
