@@ -355,9 +355,11 @@ int moe_qk_norm_rope(const moe_kv_cache *cache, const moe_norm_rope *args, void 
  * Query heads h * g .. h * g + g - 1 read key/value head h (g = n_q_heads / n_kv_heads <= 64).
  *   out = softmax over the positions seen (scale * q . k) . v
  * Scores, maxima, sums and the weighted sum are fp32; the weights enter the product with v in the
- * cache's dtype; out is rounded once.  A query that sees nothing gets zeros.  Rows behind
- * cu_q[n_seqs] are neither read nor written.  What pages hold beyond a sequence's positions may be
- * anything; K and V of its positions have to be finite.  More than 32 rows (queries times
+ * cache's dtype; out is rounded once.  A query that sees nothing gets zeros.  Rows of q that belong to
+ * no sequence may hold anything (a tile may read them), and those of out are not written.  What
+ * pages hold beyond a sequence's positions may be anything; K and V of its positions have to be
+ * finite.  Neither these nor other sequences' queries show in a sequence's outputs, beyond the order
+ * in which its positions are added: that goes by how a batch is shared out.  More than 32 rows (queries times
  * query heads) a key/value head, and all prompts, are copied by tensor maps: strides that those do
  * not take (0 over more than one head, position or page, or 2^40 bytes) return MOE_ERR_UNSUPPORTED. */
 typedef struct moe_attention {

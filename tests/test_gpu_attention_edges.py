@@ -113,3 +113,33 @@ def test_waits_that_give_up(kind, D):
     out, e = call()
     assert e == 0
     C.assert_within(out, ref, tol)
+
+
+@pytest.mark.parametrize("group", [5, 6, 7, 4])
+@pytest.mark.parametrize("kind", ["tree", "prompt"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_other_rows_hold_does_not_show(group, kind, D):
+    """The first sequence's bytes do not depend on the queries of the next one, on rows behind the last, on
+    what pages hold behind its positions, or on what an earlier call left in shared memory: all of that
+    is in the tiles beside its rows.  Its scores' maximum moves from step to step, so that a vote of
+    other rows for a new reference would change how its weights are rounded."""
+    lens, ctxs = [20, 3], [1100, 60]
+    masks = tree_masks(3, lens) + [0] * 40
+    want = None
+    for junk in (0.0, 50.0, -50.0, 400.0):
+        b = C.batch(group, lens, ctxs, 2 * group, 2, D, 64, BF16, pad_rows=40, stale=junk)
+        b.q[20:23] *= max(1.0, junk)
+        b.q[23:] = junk
+        fill = C.batch(99, [64, 64], [1500, 10], 2 * group, 2, D, 64, BF16)
+        fill.q.mul_(1 + abs(junk))
+        run_prompt(fill)                     # leaves its queries in shared memory
+        run_tree(fill, 64)
+        if kind == "tree":
+            out = run_tree(b, 20, masks)
+        else:
+            out = run_prompt(b)
+        if want is None:
+            want = out[:20].clone()
+            ref, tol = b.reference(D ** -0.5, masks if kind == "tree" else None)
+            C.assert_within(want, ref[:20], tol[:20])
+        assert differing(out[:20], want) == 0, junk
