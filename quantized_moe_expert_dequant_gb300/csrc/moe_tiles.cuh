@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int to
     const float2 v = ml[s_slot[c] * 256];
     const float4 *q = src + static_cast<int64_t>(s_slot[c]) * 2 * (D / 4) * 128;
     const float4 a = q[0], b = q[128];
-    if (v.y > 0.f) {  // a part without weight may not have been written
+    if (!(v.y == 0.f)) {  // a part without weight may not have been written; a sum that is NaN counts
       const float g = exp2_approx((v.x - m) * p.scale_log2);
       l = fmaf(v.y, g, l);
       o[0] = fmaf(a.x, g, o[0]), o[1] = fmaf(a.y, g, o[1]);

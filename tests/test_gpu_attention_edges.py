@@ -143,3 +143,20 @@ def test_what_other_rows_hold_does_not_show(group, kind, D):
             ref, tol = b.reference(D ** -0.5, masks if kind == "tree" else None)
             C.assert_within(want, ref[:20], tol[:20])
         assert differing(out[:20], want) == 0, junk
+
+
+@pytest.mark.parametrize("kind,lens", [("tree", [2, 1]), ("tree", [60, 33]), ("prompt", [60, 33])])
+@pytest.mark.parametrize("ctxs", [[40, 7], [9000, 4000]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_query_that_is_nan_gives_nan(kind, lens, ctxs, D):
+    """... in its own row and head and nowhere else, whether one CTA has its item or several share it."""
+    b = C.batch(D, lens, ctxs, 8, 2, D, 32, BF16)
+    ref, tol = b.reference(D ** -0.5)
+    rows = [(1, 3), (lens[0], 0), (lens[0], 7)]
+    bad = torch.zeros(ref.shape, dtype=torch.bool, device="cuda")
+    for r, h in rows:
+        b.q[r, h, 5] = float("nan")
+        bad[r, h] = True
+    out = run_prompt(b) if kind == "prompt" else run_tree(b, max(lens))
+    assert bool(out[bad].isnan().all())
+    C.assert_within(out[~bad], ref[~bad], tol[~bad])
