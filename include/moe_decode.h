@@ -459,11 +459,12 @@ int moe_router_topk(const float *logits, int32_t m, int32_t n_experts, int32_t t
  * wait runs forever. */
 int moe_debug_wait_timeout(int32_t kind, int32_t *scratch, int32_t *device_error, void *stream);
 
-/* The limit, in GPU cycles, of every wait in the tensor-core attention kernels that later calls of
- * this process launch (prompts, trees of more than 32 rows); 0 gives back the usual one of about two
- * seconds.  With a limit that waits run into on their ordinary way, the kernels give up, wait for
- * their copies and products under way, OR the time-out bit (2) into device_error and end; their
- * outputs are then unspecified, the context stays usable.  A debug export for a test of that. */
+/* The limit, in GPU cycles, of the waits of copies and products in the tensor-core attention kernels
+ * that later calls of this process launch (prompts, trees of more than 32 rows); 0 gives back the
+ * usual one of about two seconds.  With a limit that these run into on their ordinary way, the
+ * kernels give up, wait for their copies and products under way, OR the time-out bit (2) into
+ * device_error and end; their outputs are then unspecified, the context stays usable.  A debug
+ * export for a test of that. */
 int moe_debug_attention_wait_cycles(int64_t cycles);
 
 /* The column split's cut of a CTA's activation columns [u0, u1) into pieces, exactly as the

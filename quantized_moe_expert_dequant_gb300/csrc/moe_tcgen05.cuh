@@ -57,7 +57,7 @@ struct Limit {  // of a wait: about two seconds, where a kernel's waits take mic
 // Waits for the phase of that parity; false after the limit, or when another thread of the
 // CTA has given up (*gone), so that the kernel ends whatever happens.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gone,
-                                         const Limit &limit) {
+                                         const Limit &limit = Limit()) {
   // (a suspended thread sleeps longer than the shortest limits, whatever it asks for)
   const auto done = [&]() {
     return limit.nap_ns ? bar_try(bar, parity, limit.nap_ns) : bar_test(bar, parity);

@@ -62,7 +62,9 @@ struct PromptParams {
   float *part;       // [2 G][2][D / 4][128][4]: parts of outputs, four columns of a tile's rows together
   float2 *part_ml;   // [2 G][2][128] (reference maximum, sum)
   struct Share *share;  // [G], null when no item can be shared
-  tc::Limit limit;      // of a wait
+  // of a wait of the copies and the products; the other warps' is fixed and they leave with these (a limit in
+  // memory in each wait of the softmax: 124 us for 120 on chunks behind prefixes, heads of 64)
+  tc::Limit limit;
 };
 
 // ------------------------------------------------------------------ who does what
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   int taken = 0;  // items
   const auto take = [&](Item &item) {  // a whole warp; false: no more, or a wait gave up
     const int at = taken % kItems;
-    const bool ok = tc::bar_wait(bar(s_item_full[at]), (taken / kItems) & 1, &s_gone, w.limit);
+    const bool ok = tc::bar_wait(bar(s_item_full[at]), (taken / kItems) & 1, &s_gone);
     if (!__all_sync(0xffffffffu, ok)) return false;
     item = s_item[at];
     __syncwarp();
@@ -428,8 +430,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       Walk walk(p, tree, w.tokens, s_spot);
       for (int it = 0;; ++it) {
         const Item item = walk.next();
-        if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone, w.limit))
-          break;
+        if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone)) break;
         s_item[it % kItems] = item;
         tc::bar_arrive(bar(s_item_full[it % kItems]));
         if (!item.more) break;
@@ -501,10 +502,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // warp gives up, now or after this one has issued its last.
     volatile int never = 0;
     for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
-      tc::bar_wait(bar(s_full[it % C::kStages]), (it / C::kStages) & 1, &never, tc::Limit());
+      tc::bar_wait(bar(s_full[it % C::kStages]), (it / C::kStages) & 1, &never);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (q_loads[i] > 0) tc::bar_wait(bar(s_q[i]), (q_loads[i] - 1) & 1, &never, tc::Limit());
+      if (q_loads[i] > 0) tc::bar_wait(bar(s_q[i]), (q_loads[i] - 1) & 1, &never);
   } else if (warp == kSoftmaxWarps) {
     // ---------------------------------------------------------------- products
     // Everything here is the same for all lanes (the shuffles say so to the compiler); `one` issues.
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // The products under way end before TMEM and the shared memory go, whoever gives up and when.
     volatile int never = 0;
     tc::mma_commit(one, bar(s_end));
-    tc::bar_wait(bar(s_end), 0, &never, tc::Limit());
+    tc::bar_wait(bar(s_end), 0, &never);
     __syncwarp();
   } else if (warp < kSoftmaxWarps) {
     // ---------------------------------------------------------------- softmax, one row a thread
@@ -666,13 +667,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (tree && tok < item.nq) row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
       float m = kNegInf, l = 0.f;
       for (int t = 0; t < n; ++t, ++n_s) {
-        ok = tc::bar_wait(bar(s_s[i]), n_s & 1, &s_gone, w.limit);
+        ok = tc::bar_wait(bar(s_s[i]), n_s & 1, &s_gone);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after();
         if (idle) {
           if (C::kBeside && t > 0) {  // its arrival for P must not count for the step before
-            ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
+            ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
             ++n_o;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float ref = m == kNegInf ? 0.f : m;
         if (C::kBeside && t > 0) {  // the last step's product has read P and written O
-          ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
+          ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
           ++n_o;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (lane == 0) tc::bar_arrive(bar(s_p[i]));
       }
       if (!ok) break;
-      ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone, w.limit);
+      ok = tc::bar_wait(bar(s_o[i]), n_o & 1, &s_gone);
       ++n_o;
       ok = __all_sync(0xffffffffu, ok && !s_gone);
       if (!ok) break;
