@@ -660,9 +660,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // a warp without rows only keeps the barriers going
       const int rows = min(w.tokens, item.nq - tok_first) * p.group;
       const bool idle = 32 * (warp % 4) >= rows;
-      // The other rows of the tile hold what is in memory behind its own queries, or what an earlier kernel left:
-      // they have no say in what the warp decides.
-      const bool live = r < rows;
       uint64_t row_mask = 0;  // drafted positions that the row sees
       if (tree && tok < item.nq) row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
       float m = kNegInf, l = 0.f;
@@ -723,7 +720,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // weight is larger than the sum) is a new maximum found, O scaled down, and the work done
         // again; finding the maximum in every step took 450 of 1250 cycles.
         // A row that has seen nothing yet (a later piece of an item, a tree without context) has no m.
-        if (t == 0 || (tree && __any_sync(0xffffffffu, live && m == kNegInf))) {
+        if (t == 0 || (tree && __any_sync(0xffffffffu, m == kNegInf))) {
           const float top = row_max(x);
           if (m == kNegInf) m = top;
         }
@@ -737,7 +734,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();  // stores and loads of TMEM want converged warps
         float add = store_weights<T>(x, ref * p.scale_log2, p.scale_log2, tp);
-        if (__any_sync(0xffffffffu, live && add > kMostWeight)) {
+        // Rows behind the sequence's hold what is in memory there, or what an earlier kernel left: they have no
+        // say.  (Asked first without them: a flag a row in every step costs 1% with heads of 64.)
+        if (__any_sync(0xffffffffu, add > kMostWeight) &&
+            __any_sync(0xffffffffu, r < rows && add > kMostWeight)) {
           tc::wait_store();  // P is written again below, and stores to TMEM have no order of their own
           const float up = fmaxf(ref, row_max(x));
           const float f = exp2_approx((ref - up) * p.scale_log2);
