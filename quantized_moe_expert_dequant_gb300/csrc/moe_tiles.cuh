@@ -3,7 +3,7 @@
 // (moe_prompt_tree.cu).
 //
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
-//   that row r sees, in one pass over K and V; m_r is a maximum of some of the scores.
+//   that row r sees, in one pass over K and V; m_r goes by some of the scores (reference).
 //
 // Bound by the two products (4 D flops per row and position).  An item is two tiles of up to 128 rows of
 // one sequence and one key/value head: row R of a tile is token R / group, query head R % group, so
@@ -14,9 +14,8 @@
 //   O += P V     128 x D x 128, P from TMEM, V from shared memory, O in TMEM
 // The two tiles take turns: while four warps are at one tile's softmax, the tensor cores work on
 // the other tile.  One warp issues all products, in an order in which they also complete, one finds
-// the items, one copies.  O is only scaled down when a row's weights, relative to an older
-// maximum, add up to more than 2^13 in a step; up to there 16-bit floats and the fp32 sums hold them
-// without loss.
+// the items, one copies.  O is only scaled down when a row's weights have outgrown what the type
+// holds (kMostWeight).
 //
 // One persistent CTA an SM.  Measured (32 query, 8 key/value heads of 128, bf16, 8192 tokens, causal):
 // 2567 us with 64-row tiles on mma.sync, 496 us with one CTA per two tiles, 374 us when the
@@ -41,7 +40,9 @@ constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // and products, copie
 // 168 registers at launch; 2 x 128 x 216 + 128 x 72 = 384 x 168
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kItems = 4;               // items between the warp that finds them and the others
-constexpr float kMostWeight = 8192.f;   // sum of a row's weights in a step from which O is rescaled
+// Sum of a row's weights in a step from which O is rescaled: no weight is larger, so none is infinite in fp16.
+template <typename T>
+constexpr float kMostWeight = std::is_same<T, __half>::value ? 65504.f : 8192.f;
 
 template <int D>
 struct Prompt {
@@ -288,7 +289,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ float row_max(const uint32_t (&x)[4][32]) {
+// The largest score of a row, and the lowest of the maxima of its quarters.
+struct Top {
+  float max, low;
+};
+__device__ __forceinline__ Top row_max(const uint32_t (&x)[4][32]) {
   float top[4];  // four chains: one of 64 dependent maxima took 500 cycles
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -298,7 +303,26 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[4][32]) {
       top[c] = max3(top[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
     top[c] = fmaxf(top[c], __uint_as_float(x[c][31]));
   }
-  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  return {fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
+          fminf(fminf(top[0], top[1]), fminf(top[2], top[3]))};
+}
+
+// What a row's weights are taken relative to from its first step on: the maximum there, in bf16.  fp16
+// holds 2^16 down to 2^-14 in full.  Most rows get scores above those of their first step, so the maximum
+// is at 2^0; but a score that stands out from the lowest quarter's by more than 2^6 is higher by as much, up to
+// 2^8, so that the others keep their bits beside it.  A row that outgrows its reference later has a score that
+// stands out, at 2^8 from then on; the 128 weights of a step then stay below 2^16.
+// (8192 tokens, heads of 128, scores with a standard deviation of 1.5, 3, 4.5, 6: 383, 383, 383, 446 us; 382, 384,
+// 404, 434 us with the maximum and 2^13 as the bound; 375, 453, 490, 489 us with the maximum always at 2^10.)
+template <typename T>
+__device__ __forceinline__ float reference(const Top &t, const Params &p) {
+  if (!std::is_same<T, __half>::value) return t.max;
+  const float up = fminf(fmaxf((t.max - t.low) * p.scale_log2 - 6.f, 0.f), 8.f);
+  return t.max - up * p.octave;  // -inf: no score is seen
+}
+template <typename T>
+__device__ __forceinline__ float outgrown(float top, const Params &p) {
+  return std::is_same<T, __half>::value ? top - 8.f * p.octave : top;
 }
 
 // The weights exp2(scale * x - off) of 32 positions: their pairs in 16 bits in y, added to sum.  Eight
@@ -324,8 +348,7 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float off, floa
       for (int e = 0; e < 8; e += 2) {
         const float pa = w[(g - 1) & 1][e], pb = w[(g - 1) & 1][e + 1];
         sum[e / 2 % 2] = add2(sum[e / 2 % 2], pair(pa, pb));
-        // the weights meet v in the cache's type: half a step of it, as large as the output's own
-        // rounding
+        // the weights meet v in the cache's type
         y[(8 * (g - 1) + e) / 2] = Half<T>::pack(pa, pb);
       }
     }
@@ -715,13 +738,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (32 * c + e >= see) x[c][e] = __float_as_uint(kNegInf);
         }
-        // The weights are taken relative to m, the maximum of the first step: whatever reference they
+        // The weights are taken relative to m, which goes by the first step: whatever reference they
         // are taken to divides out.  Only when their sum shows that some row has outgrown m (no
-        // weight is larger than the sum) is a new maximum found, O scaled down, and the work done
+        // weight is larger than the sum) is a new one found, O scaled down, and the work done
         // again; finding the maximum in every step took 450 of 1250 cycles.
         // A row that has seen nothing yet (a later piece of an item, a tree without context) has no m.
         if (t == 0 || (tree && __any_sync(0xffffffffu, m == kNegInf))) {
-          const float top = row_max(x);
+          const float top = reference<T>(row_max(x), p);
           if (m == kNegInf) m = top;
         }
         const float ref = m == kNegInf ? 0.f : m;
@@ -736,10 +759,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         float add = store_weights<T>(x, ref * p.scale_log2, p.scale_log2, tp);
         // Rows behind the sequence's hold what is in memory there, or what an earlier kernel left: they have no
         // say.  (Asked first without them: a flag a row in every step costs 1% with heads of 64.)
-        if (__any_sync(0xffffffffu, add > kMostWeight) &&
-            __any_sync(0xffffffffu, r < rows && add > kMostWeight)) {
+        if (__any_sync(0xffffffffu, add > kMostWeight<T>) &&
+            __any_sync(0xffffffffu, r < rows && add > kMostWeight<T>)) {
           tc::wait_store();  // P is written again below, and stores to TMEM have no order of their own
-          const float up = fmaxf(ref, row_max(x));
+          const float up = fmaxf(ref, outgrown<T>(row_max(x).max, p));
           const float f = exp2_approx((ref - up) * p.scale_log2);
           if (m != kNegInf) m = up;
           l *= f;

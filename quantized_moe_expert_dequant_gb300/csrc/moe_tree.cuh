@@ -3,7 +3,7 @@
 //
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
 //   that row r sees, m_r their largest score: one pass over K and V with the running maximum and
-//   sum; what was summed before a larger maximum is scaled down to it.
+//   sum; what was summed before a larger maximum is scaled down to it.  (fp16: all p times 2^15.)
 //
 // Bound by the bytes of K and V, so what matters is that every SM streams all the time, whatever
 // the lengths are.  An item is one sequence and one key/value head, with the queries of all heads
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
         const float ref = top == kNegInf ? 0.f : top;  // no position seen so far
         scale[h] = exp2_approx((m[h] - ref) * p.scale_log2);
         m[h] = top;
-        const float off = ref * p.scale_log2;
+        const float off = ref * p.scale_log2 - Half<T>::kRow;
         float add = 0.f;
 #pragma unroll
         for (int j = 0; j < TW / 8; ++j)
@@ -377,8 +377,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       }
 #pragma unroll
       for (int j = 0; j < TW / 16; ++j) {
-        // p enters the product in the cache's type (as v is): half a step of it relative to p, the
-        // size of the output's own rounding
+        // p enters the product in the cache's type (as v is)
         const uint32_t a[4] = {Half<T>::pack(sc[2 * j][0], sc[2 * j][1]),
                                Half<T>::pack(sc[2 * j][2], sc[2 * j][3]),
                                Half<T>::pack(sc[2 * j + 1][0], sc[2 * j + 1][1]),

@@ -13,7 +13,7 @@ kernels.  ``attention`` also returns, per output element, how far a kernel may b
                     shifted (exponents of size x: 2^-23 x) and raised by ex2.approx (2^-22)
   2 n 2^-23 A       sums of n weights and weighted values in fp32
   n 2^-25 max|v|    fp16 only: weights below 2^-14 are subnormal (the divisor is at least about 1);
-                    weights are taken relative to a maximum that may be 2^13 below the largest
+                    2^-25 is `least`, smaller where the kernels form larger weights
 """
 from __future__ import annotations
 
@@ -25,8 +25,9 @@ import torch
 UNIT = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 
 
-def attention(q, k, v, seen, scale, n_sum=None):
-    """q [R, D], k and v [N, D], seen bool [R, N] -> (out, tolerance) fp64 [R, D]."""
+def attention(q, k, v, seen, scale, n_sum=None, least=2.0 ** -25):
+    """q [R, D], k and v [N, D], seen bool [R, N] -> (out, tolerance) fp64 [R, D]; least: half of fp16's
+    least step, relative to a weight that the divisor holds."""
     dt = q.dtype
     u = UNIT[dt]
     qd, kd, vd = q.double(), k.double(), v.double()
@@ -46,7 +47,7 @@ def attention(q, k, v, seen, scale, n_sum=None):
     e = float(size) * (D * 2.0 ** -23 + 4 * 2.0 ** -23) + 2.0 ** -21
     tol = 2 * u * out.abs() + A * (u + 2 * e + 2 * (n + 8) * 2.0 ** -23) + 1e-12
     if dt == torch.float16 and n:
-        tol = tol + n * 2.0 ** -25 * vd.abs().amax() + 2.0 ** -25
+        tol = tol + n * least * vd.abs().amax() + 2.0 ** -25
     return out, tol
 
 
@@ -68,7 +69,7 @@ class Batch:
         D = self.k.shape[3]
         return (self.k[used, h].reshape(-1, D)[:n], self.v[used, h].reshape(-1, D)[:n])
 
-    def reference(self, scale, masks=None):
+    def reference(self, scale, masks=None, **kw):
         """(out, tol) fp64 [rows, Hq, D]; masks: a list of ints per row, or None: causal."""
         rows, Hq, D = self.q.shape[0], self.q.shape[1], self.q.shape[2]
         G = Hq // self.k.shape[1]
@@ -88,7 +89,7 @@ class Batch:
             for h in range(Hq):
                 k, v = self.keys(i, h // G)
                 out[at:at + n, h], tol[at:at + n, h] = attention(
-                    self.q[at:at + n, h], k, v, seen, scale)
+                    self.q[at:at + n, h], k, v, seen, scale, **kw)
             at += n
         return out, tol
 

@@ -160,3 +160,47 @@ def test_a_query_that_is_nan_gives_nan(kind, lens, ctxs, D):
     out = run_prompt(b) if kind == "prompt" else run_tree(b, max(lens))
     assert bool(out[bad].isnan().all())
     C.assert_within(out[~bad], ref[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("kind,max_q,wide", [("tree", 2, False), ("tree", 2, True), ("tree", 60, False),
+                                             ("tree", 60, True), ("prompt", 60, False),
+                                             ("prompt", 60, True)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gap", [12.0, 17.0, 18.0, 22.0])
+@pytest.mark.parametrize("at", [0, 290])
+def test_small_weights_of_fp16_caches_are_kept(kind, max_q, wide, D, gap, at):
+    """One position of each sequence outweighs every other one by about e^gap and has the value zero, so
+    the output is what the small weights bring: they are not lost in the range of fp16.  The kernels form
+    weights times 2^15 (trees of up to 32 rows) or 2^8 (tiles, beside a position that stands out so),
+    a weight of 1 being in the divisor, so that half of fp16's least step is 2^-40 or 2^-33 of it."""
+    lens, ctxs = [max_q, 33 if max_q > 33 else 1], [1000, 300]
+    b = C.batch(D, lens, ctxs, 8, 2, D, 32, F16, q_scale=0.1)
+    b.q[..., 0] = 4.0
+    b.v.copy_(256 + 50 * b.v)
+    for i in range(2):
+        pages, place = positions(b, i)
+        b.k[pages, :, place, 0] = 0.0
+        b.k[pages[at], :, place[at]] = 0.0
+        b.k[pages[at], :, place[at], 0] = gap / 4.0
+        b.v[pages[at], :, place[at]] = 0.0
+    if wide:                                 # several CTAs share an item
+        b.table = torch.cat([b.table, torch.full((2, 4000), -1, dtype=torch.int32, device="cuda")], 1)
+    least = 2.0 ** -40 if max_q == 2 else 2.0 ** -33
+    ref, tol = b.reference(1.0, least=least)
+    out = run_prompt(b, 1.0) if kind == "prompt" else run_tree(b, max_q, None, 1.0)
+    C.assert_within(out, ref, tol)
+
+
+def test_equal_weights_of_fp16_caches():
+    """All scores alike over many steps, so that all weights are the same power of two and none is rounded;
+    and the same with values as large as fp16 holds."""
+    for value in (1.0, 60000.0):
+        b = C.batch(5, [60, 2], [2000, 700], 8, 2, 128, 32, F16)
+        b.q.fill_(0.0)
+        b.v.copy_(value * b.v.clamp(-1, 1))
+        ref, tol = b.reference(1.0, least=0.0)
+        C.assert_within(run_prompt(b, 1.0), ref, tol)
+        C.assert_within(run_tree(b, 60, None, 1.0), ref, tol)
+        two = C.Batch(b.k, b.v, b.q[60:], torch.tensor([0, 2], dtype=torch.int32, device="cuda"),
+                      b.ctx[1:], b.table[1:], [2], [700])
+        C.assert_within(run_tree(two, 2, None, 1.0), ref[60:], tol[60:])
