@@ -204,3 +204,34 @@ def test_equal_weights_of_fp16_caches():
         two = C.Batch(b.k, b.v, b.q[60:], torch.tensor([0, 2], dtype=torch.int32, device="cuda"),
                       b.ctx[1:], b.table[1:], [2], [700])
         C.assert_within(run_tree(two, 2, None, 1.0), ref[60:], tol[60:])
+
+
+@pytest.mark.parametrize("token_major", [False, True])
+def test_a_cache_beyond_32_bits(token_major):
+    """Pages whose elements lie beyond 2^32 of the cache's first: written, and read by both attentions."""
+    Hq, Hkv, D, page = 8, 4, 128, 64
+    n_pages = 2 ** 32 // (Hkv * D * page) + 40
+    shape = (n_pages, page, Hkv, D) if token_major else (n_pages, Hkv, page, D)
+    k, v = (torch.empty(shape, dtype=BF16, device="cuda") for _ in range(2))
+    k[:40], v[:40] = 7.0, 7.0                # where an offset of 32 bits would end up
+    if token_major:
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    cache = Bn.KvCache(k, v)
+    n, gen = 300, torch.Generator().manual_seed(1)
+    order = (torch.randperm(40, generator=gen)[:5] + n_pages - 40).to(torch.int32)
+    at = torch.arange(n)
+    slots = (order[at // page] * page + at % page).to(torch.int32).cuda()
+    x = torch.randn((n, Hq + 2 * Hkv, D), generator=gen).to(BF16).cuda()
+    q = Bn.qk_norm_rope(cache, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], at.int().cuda(), slots,
+                        None)
+    assert torch.equal(k[order.long().cuda()[at.cuda() // page], :, at.cuda() % page],
+                       x[:, Hq:Hq + Hkv])
+    assert bool((k[:40] == 7).all() and (v[:40] == 7).all())
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    table = order.view(1, 5).cuda()
+    b = C.Batch(k, v, q, i32(0, n), i32(0), table, [n], [0])
+    ref, tol = b.reference(D ** -0.5)
+    C.assert_within(run_prompt(b), ref, tol)
+    for last in (2, 40):                     # rows of a tree: both kinds of tiles
+        b = C.Batch(k, v, q[n - last:], i32(0, last), i32(n - last), table, [last], [n - last])
+        C.assert_within(run_tree(b, last), ref[n - last:], tol[n - last:])
