@@ -354,8 +354,9 @@ int moe_qk_norm_rope(const moe_kv_cache *cache, const moe_norm_rope *args, void 
  * ctx_len[s], its positions o = 0 .. ctx_len[s] + rows - 1 lie on page page_table[s][o / page_size].
  * Query heads h * g .. h * g + g - 1 read key/value head h (g = n_q_heads / n_kv_heads <= 64).
  *   out = softmax over the positions seen (scale * q . k) . v
- * Scores, maxima, sums and the weighted sum are fp32; the weights enter the product with v in the
- * cache's dtype; out is rounded once.  A query that sees nothing gets zeros.  Rows of q that belong to
+ * Scores, maxima, sums and the weighted sum are fp32 (scale * q . k stays within its range); the
+ * weights enter the product with v in the cache's dtype; out is rounded once.  A query that sees
+ * nothing, or whose scores are all -infinity, gets zeros; one with a score that is NaN gets NaN.  Rows of q that belong to
  * no sequence may hold anything (a tile may read them), and those of out are not written.  What
  * pages hold beyond a sequence's positions may be anything; K and V of its positions have to be
  * finite.  Neither these nor other sequences' queries show in a sequence's outputs, beyond the order

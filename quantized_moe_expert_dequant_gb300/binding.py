@@ -596,7 +596,9 @@ def qk_norm_rope(cache: KvCache, q, k, v, positions, slots, inv_freq, q_weight=N
     """moe_qk_norm_rope: norms and rotates the heads of q [T, Hq, D] and k [T, Hkv, D] (fp32 or the
     cache's dtype), writes k and v [T, Hkv, D] to their slots (int32 [T]; negative: padding) in
     the cache and returns q_out [T, Hq, D] in the cache's dtype.  positions int32 [T], inv_freq fp64
-    [rot_dim / 2] (None: no rotation), weights [D] in the cache's dtype or None: no norm."""
+    [rot_dim / 2] (None: no rotation), weights [D] in the cache's dtype or None: no norm.  The rows of
+    padding are not written: in a q_out made here they are uninitialised memory.  device_error: int32
+    [1], whose bit 1 a slot outside the cache sets (its key and value are not written)."""
     shape = q.shape
     T, Hq, D = shape
     dev, dt, to, kv, i32 = cache._dev, q.dtype, cache.dtype, (T, *cache._heads), torch.int32
@@ -670,7 +672,12 @@ def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tre
     """moe_tree_attention: decoded tokens (max_q = 1) or trees of up to max_q <= 64 drafted tokens a
     sequence.  q [T, Hq, D]; cu_q int32 [n + 1]; ctx_len int32 [n]; page_table int32 [n, width];
     tree_mask int64 [T], bit j of a row: it sees drafted token j of its sequence (None: causal);
-    scale None: 1 / sqrt(D).  workspace: uint8 tensor to use instead of a new one."""
+    scale None: 1 / sqrt(D).  workspace: uint8 tensor to use instead of a new one.
+
+    A sequence that is not within its bounds (more than max_q rows, more positions than its pages) is
+    skipped on the device: its rows of out, like those that belong to no sequence, are not written, and
+    in an out made here they are uninitialised memory.  device_error (int32 [1], zeroed by the caller)
+    shows that without a wait on this call: bit 1 of it is set, for a page outside the cache too."""
     dev = cache._dev
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
@@ -687,7 +694,8 @@ def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tre
 def prompt_attention(cache: KvCache, q, cu_q, ctx_len, page_table, scale: float | None = None,
                      out=None, device_error=None, workspace=None, stream=None):
     """moe_prompt_attention: causal attention of packed prompts, or of chunks behind ctx_len cached
-    positions; arguments as for tree_attention, without a limit on the rows of a sequence."""
+    positions; arguments and device_error as for tree_attention, without a limit on the rows of a
+    sequence."""
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     ws = _workspace("moe_prompt_attention_workspace", cache, workspace, stream, args)

@@ -20,7 +20,8 @@
 // One persistent CTA an SM.  Measured (32 query, 8 key/value heads of 128, bf16, 8192 tokens, causal):
 // 2567 us with 64-row tiles on mma.sync, 496 us with one CTA per two tiles, 374 us when the
 // products' loop is uniform in its warp (descriptors in a one-lane branch cost 100 cycles a product),
-// 348 us with the work shared evenly, 341 us without a maximum in every step (1.61 PFLOP/s).  A step of
+// 348 us with the work shared evenly, 341 us without a maximum in every step (1.61 PFLOP/s; called again and
+// again, at the power limit and 1910 instead of 2070 MHz, 367 us: 1.50 PFLOP/s).  A step of
 // 128 positions takes 2620 cycles, the products 2048 of them at the peak rate: with both operands in
 // shared memory S runs at 128 bytes a cycle, the limit, and takes about 90 cycles instead of 64 a
 // product.  Slower were sixteen softmax warps of half a row a thread (403 us to 374), a ring of four

@@ -8,7 +8,8 @@
 // Bound by the bytes of K and V, so what matters is that every SM streams all the time, whatever
 // the lengths are.  An item is one sequence and one key/value head, with the queries of all heads
 // that share it as rows (row R is query R / group, head R % group; more than 32 rows go to the tiles
-// of moe_tiles.cuh); its positions are cut into tiles of 64.  All tiles of all items, in order, form one
+// of moe_tiles.cuh); its positions are cut into tiles of 64, of 128 with heads of 64 (tile_of).  All tiles of
+// all items, in order, form one
 // line that the CTAs share evenly: CTA c takes the tiles [c W / G, (c + 1) W / G).  The lengths are
 // read on the device, so a captured graph balances whatever it is replayed on.  An item that ends up in
 // one CTA is written by it; one that several CTAs share leaves its partial maxima, sums and outputs
@@ -18,10 +19,10 @@
 // takes each item and joins in distributed shared memory.
 //
 // A CTA is four warps over 16 WR rows: WR warps split the rows, 4 / WR warps the positions of a
-// tile, so a single decoded token (group <= 16 rows) still uses all four.  Copies run two or three
+// tile, so a single decoded token (group <= 16 rows) still uses all four.  Copies run two
 // tiles ahead and across items, so that one item's end does not empty the pipeline of the next:
 // 32 tokens over contexts of 1 to 15991 positions (741 MB) 132 us with a pipeline per item, 125 us
-// so (5.9 TB/s); 8 drafts behind 65536 to 131064 positions (1.75 GB) 264 us (6.6 TB/s).
+// so (5.8 to 5.9 TB/s); 8 drafts behind 65536 to 131064 positions (1.75 GB) 264 us (6.6 TB/s).
 #pragma once
 
 #include <algorithm>
