@@ -121,11 +121,15 @@ def draw(rng):
         lens = [rng.randint(1, most) for _ in range(n)]
         if n > 2 and rng.random() < 0.3:
             lens[rng.randrange(n)] = 0
-        far = _log_int(rng, 16, 131072)
+        far = _log_int(rng, 16 * page if op == "select" else 16, 131072)
         ctx = [rng.choice([0, far]) if rng.random() < 0.2 else rng.randint(far // 8, far)
                for _ in range(n)]
+        longest = rng.randrange(n)
+        ctx[longest], lens[longest] = far, max(lens[longest], 1)
         select = SINK + RECENT + _log_int(rng, 1, 4096 // page)
         while True:
+            if op == "select":  # (nothing to select from otherwise)
+                select = min(select, max(SINK + RECENT + 1, ctx[longest] // page // 2))
             c = _rows("", op, lens, ctx, heads, kv_heads, dim, page, dtype,
                       0 if op == "bounds" else select)
             w = work(c)
