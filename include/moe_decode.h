@@ -402,6 +402,49 @@ int moe_prompt_attention_workspace(const moe_kv_cache *cache, const moe_attentio
 int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, void *workspace,
                          int64_t workspace_bytes, void *stream);
 
+/* ---- attention that does not read the whole cache for every token -----------------------------
+ * A batch whose sequences share their first pages reads those once (moe_prefix_attention); a token
+ * behind a long context reads the pages that were selected for it (moe_page_bounds,
+ * moe_select_pages, moe_sparse_attention).  No counterpart on the pages this library follows; the
+ * rules of the calls above (streams, capture, errors on the device, workspaces) hold here too. */
+
+/* The bounds of the keys on pages: for each page that holds one of the batch's new positions (ctx_len[s]
+ * .. ctx_len[s] + rows - 1 of sequence s), each key/value head and dimension the least and the largest
+ * key over the positions 0 .. ctx_len[s] + rows - 1 on it.  To be called when their keys are in the cache.
+ *   bounds  [n_pages][n_kv_heads][2][head_dim] device, cache dtype, 16-byte aligned: least, largest.
+ *           Other pages' bounds are left as they are.
+ * Of args, q, out, their strides, n_q_heads and scale are not used; n_rows bounds the rows. */
+int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *args, void *bounds, void *stream);
+
+/* The pages that each row of q reads, by their bounds.  A row that sees the positions 0 .. t (causal, as
+ * in moe_prompt_attention) has the pages 0 .. t / page_size of its sequence.  With at most n_select of
+ * them, all; else the first `sink`, the last `recent`, and of the others those with the largest
+ *   score = sum over the query heads of the key/value head of sum_d max(q_d least_d, q_d largest_d),
+ * an upper bound of the sum of q . k over those heads for each key on the page; of equal scores the
+ * lower page's first.  The comparison is that of exact scores (fp64).
+ *   pages   int32 [n_rows][n_kv_heads][n_select] device: places in the sequence's page table,
+ *           ascending, -1 behind the last; rows of no sequence are not written
+ * 0 <= sink, 1 <= recent, sink + recent <= n_select; at most 65536 pages a sequence (MOE_ERR_UNSUPPORTED
+ * beyond).  A page outside the cache has the lowest score.  Of args, out, its strides and scale are not
+ * used.  workspace as for moe_tree_attention, of moe_select_pages_workspace bytes. */
+int moe_select_pages_workspace(const moe_kv_cache *cache, const moe_attention *args, int64_t *bytes);
+int moe_select_pages(const moe_kv_cache *cache, const moe_attention *args, const void *bounds,
+                     int32_t n_select, int32_t sink, int32_t recent, int32_t *pages, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/* Attention of each row over listed pages: out as in moe_attention, over those positions that the row
+ * sees (causal) and that lie on the pages listed for it and the key/value head.
+ *   pages   int32 [n_rows][n_kv_heads][n_select] device, as moe_select_pages gives them: places in the
+ *           sequence's page table in any order.  Entries that are negative or behind the row's last page
+ *           list nothing; a page listed twice counts twice.  A row that sees u pages reads its
+ *           first min(u, n_select) entries.
+ * At most 32 query heads a key/value head (MOE_ERR_UNSUPPORTED beyond).  workspace as for
+ * moe_tree_attention, of moe_sparse_attention_workspace bytes. */
+int moe_sparse_attention_workspace(const moe_kv_cache *cache, const moe_attention *args,
+                                   int32_t n_select, int64_t *bytes);
+int moe_sparse_attention(const moe_kv_cache *cache, const moe_attention *args, const int32_t *pages,
+                         int32_t n_select, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* ---- canonical packing (host) ---------------------------------------------------------------
  * codes: uint8 [rows][cols], one code per byte, each < 2^bits; packed: [rows][cols*bits/8].
  * cols must be a multiple of 64.  Returns MOE_ERR_INVALID_ARG on a code out of range. */

@@ -45,6 +45,8 @@ EXPORTS = ["moe_decode_create", "moe_decode_forward", "moe_decode_get_error", "m
            "moe_debug_wait_timeout", "moe_router_topk", "moe_debug_col_pieces",
            "moe_debug_col_plan", "moe_qk_norm_rope", "moe_tree_attention_workspace",
            "moe_tree_attention", "moe_prompt_attention_workspace", "moe_prompt_attention",
+           "moe_page_bounds", "moe_select_pages_workspace", "moe_select_pages",
+           "moe_sparse_attention_workspace", "moe_sparse_attention",
            "moe_debug_attention_wait_cycles"]
 
 
@@ -137,6 +139,11 @@ def lib() -> ctypes.CDLL:
                 "moe_qk_norm_rope": [vp, vp, vp],
                 "moe_tree_attention_workspace": [vp, vp, i32, vp],
                 "moe_tree_attention": [vp, vp, vp, i32, vp, i64, vp],
+                "moe_page_bounds": [vp, vp, vp, vp],
+                "moe_select_pages_workspace": [vp, vp, vp],
+                "moe_select_pages": [vp, vp, vp, i32, i32, i32, vp, vp, i64, vp],
+                "moe_sparse_attention_workspace": [vp, vp, i32, vp],
+                "moe_sparse_attention": [vp, vp, vp, i32, vp, i64, vp],
                 "moe_prompt_attention_workspace": [vp, vp, vp],
                 "moe_prompt_attention": [vp, vp, vp, i64, vp],
                 "moe_debug_attention_wait_cycles": [i64],
@@ -634,23 +641,32 @@ def qk_norm_rope(cache: KvCache, q, k, v, positions, slots, inv_freq, q_weight=N
     return q_out
 
 
-def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream):
-    dev, D, dt, i32 = cache._dev, cache.head_dim, cache.dtype, torch.int32
-    T, Hq, _ = shape = q.shape
+_NONE = (0, 0, 0)  # for a tensor that a call does not use
+
+
+def _batch_args(cache, a, b, T, Hq, scale, cu_q, ctx_len, page_table, device_error):
+    """moe_attention of q and out as _rows gives them; T rows of Hq query heads."""
+    dev, i32 = cache._dev, torch.int32
     n, width = page_table.shape
+    st = page_table.stride()
+    if page_table.dtype != i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
+        raise ValueError(f"page_table: int32 [n_seqs, width] on cuda:{dev} is wanted")
+    return _pack_attention(
+        a[0], b[0], a[1], a[2], b[1], b[2], _vector(cu_q, i32, n + 1, dev, "cu_q"),
+        _vector(ctx_len, i32, n, dev, "ctx_len"), page_table.data_ptr(), st[0] if n > 1 else width,
+        width, n, T, Hq, scale, _vector(device_error, i32, 1, dev, "device_error"))
+
+
+def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream):
+    dev, D, dt = cache._dev, cache.head_dim, cache.dtype
+    T, Hq, _ = shape = q.shape
     if shape[2] != D:
         raise ValueError(f"q: heads of {D} are wanted")
     if out is None:
         out = _empty_on(shape, dt, cache.device, stream)
-    st = page_table.stride()
-    if page_table.dtype != i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
-        raise ValueError(f"page_table: int32 [n_seqs, width] on cuda:{dev} is wanted")
-    a, b = _rows(q, shape, dt, dev, "q"), _rows(out, shape, dt, dev, "out")
-    return _pack_attention(
-        a[0], b[0], a[1], a[2], b[1], b[2], _vector(cu_q, i32, n + 1, dev, "cu_q"),
-        _vector(ctx_len, i32, n, dev, "ctx_len"), page_table.data_ptr(), st[0] if n > 1 else width,
-        width, n, T, Hq, D ** -0.5 if scale is None else scale,
-        _vector(device_error, i32, 1, dev, "device_error")), out
+    return _batch_args(cache, _rows(q, shape, dt, dev, "q"), _rows(out, shape, dt, dev, "out"), T, Hq,
+                       D ** -0.5 if scale is None else scale, cu_q, ctx_len, page_table,
+                       device_error), out
 
 
 def _workspace(fn: str, cache, workspace, stream, *args):
@@ -700,4 +716,64 @@ def prompt_attention(cache: KvCache, q, cu_q, ctx_len, page_table, scale: float 
                                 stream)
     ws = _workspace("moe_prompt_attention_workspace", cache, workspace, stream, args)
     _call("moe_prompt_attention", cache._dev, stream, cache._c, args, *ws[:2])
+    return out
+
+
+# ---------------------------------------------------------------- without reading the whole cache
+
+def _bounds(cache, bounds) -> int:
+    shape = (cache.n_pages, cache.n_kv_heads, 2, cache.head_dim)
+    if bounds.shape != shape:
+        raise ValueError(f"bounds: {shape} is wanted, not {tuple(bounds.shape)}")
+    return _vector(bounds, cache.dtype, bounds.numel(), cache._dev, "bounds")
+
+
+def page_bounds(cache: KvCache, bounds, cu_q, ctx_len, page_table, n_rows: int, device_error=None,
+                stream=None):
+    """moe_page_bounds: writes the least and the largest key of every page that holds one of the batch's
+    new positions to bounds [n_pages, Hkv, 2, D] (the cache's dtype) and returns it.  Called when the
+    new keys are in the cache; n_rows: the batch's rows, as of q; the other arguments as for
+    tree_attention."""
+    args = _batch_args(cache, _NONE, _NONE, n_rows, 0, 0.0, cu_q, ctx_len, page_table, device_error)
+    _call("moe_page_bounds", cache._dev, stream, cache._c, args, _bounds(cache, bounds))
+    return bounds
+
+
+def select_pages(cache: KvCache, bounds, q, cu_q, ctx_len, page_table, n_select: int, sink: int = 1,
+                 recent: int = 1, out=None, device_error=None, workspace=None, stream=None):
+    """moe_select_pages: for each row of q [T, Hq, D] and key/value head the n_select pages to read, int32
+    [T, Hkv, n_select]: places in the row of page_table, ascending, -1 behind the last.  All that the row
+    sees when they are no more; else the first `sink`, the last `recent` and those whose bounds
+    (page_bounds) allow the largest scores.  Rows of no sequence are not written."""
+    dev = cache._dev
+    T, Hq, D = shape = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q: heads of {cache.head_dim} are wanted")
+    pages = (T, cache.n_kv_heads, n_select)
+    if out is None:
+        out = _empty_on(pages, torch.int32, cache.device, stream)
+    elif out.shape != pages:
+        raise ValueError(f"out: {pages} is wanted, not {tuple(out.shape)}")
+    args = _batch_args(cache, _rows(q, shape, cache.dtype, dev, "q"), _NONE, T, Hq, 0.0, cu_q,
+                       ctx_len, page_table, device_error)
+    ws = _workspace("moe_select_pages_workspace", cache, workspace, stream, args)
+    _call("moe_select_pages", dev, stream, cache._c, args, _bounds(cache, bounds), n_select, sink,
+          recent, _vector(out, torch.int32, out.numel(), dev, "out"), *ws[:2])
+    return out
+
+
+def sparse_attention(cache: KvCache, q, cu_q, ctx_len, page_table, pages,
+                     scale: float | None = None, out=None, device_error=None, workspace=None,
+                     stream=None):
+    """moe_sparse_attention: causal attention of each row of q over the pages listed for it, pages int32
+    [T, Hkv, n_select] as select_pages gives them; the other arguments as for prompt_attention."""
+    if pages.dim() != 3 or pages.shape[:2] != (q.shape[0], cache.n_kv_heads):
+        raise ValueError(f"pages: [{q.shape[0]}, {cache.n_kv_heads}, n_select] is wanted, not "
+                         f"{tuple(pages.shape)}")
+    args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
+                                stream)
+    n = pages.shape[2]
+    ws = _workspace("moe_sparse_attention_workspace", cache, workspace, stream, args, n)
+    _call("moe_sparse_attention", cache._dev, stream, cache._c, args,
+          _vector(pages, torch.int32, pages.numel(), cache._dev, "pages"), n, *ws[:2])
     return out

@@ -55,6 +55,35 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int s, bool report) {
   return r;
 }
 
+// One row of q by itself, for the calls that go by pages of each row: its sequence, how many positions it
+// sees (ctx; causal), and nq = 1, or 0 for a row of no sequence; with n_list pages listed for it at most,
+// it has len positions on them.  load_seq is what reports a sequence that is out of range.
+struct Row : Seq {
+  int seq;
+};
+
+__device__ __forceinline__ Row load_row(const Params &p, int r, int n_list) {
+  Row row = {};
+  row.row0 = r;
+  int s = r;
+  if (p.n_seqs != p.n_rows || p.cu[s] != r || p.cu[s + 1] != r + 1) {  // not a token a sequence
+    int hi = p.n_seqs;  // the last sequence that begins at r or before
+    s = 0;
+    if (r < p.cu[0] || r >= p.cu[hi]) return row;
+    while (hi - s > 1) {
+      const int mid = (s + hi) / 2;
+      if (p.cu[mid] <= r) s = mid; else hi = mid;
+    }
+  }
+  const Seq q = load_seq(p, s, false);
+  if (r < q.row0 || r >= q.row0 + q.nq) return row;
+  row.seq = s;
+  row.nq = 1;
+  row.ctx = q.ctx + r - q.row0 + 1;
+  row.len = min(n_list, ((row.ctx - 1) >> p.page_shift) + 1) << p.page_shift;
+  return row;
+}
+
 __device__ __forceinline__ void pdl_launch() {  // the next kernel may be set up
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -169,10 +198,18 @@ inline int check_cache(const moe_kv_cache *c) {
 }
 
 // Checks an attention call's arguments and fills the kernels' parameters.
-inline int check_attention(const moe_kv_cache *c, const moe_attention *a, Params *p) {
+enum { kUsesQ = 1, kUsesOut = 2 };  // what of them a call uses: without q, n_q_heads neither
+
+inline int check_attention(const moe_kv_cache *c, const moe_attention *args, Params *p,
+                           int uses = kUsesQ | kUsesOut) {
   const int rc = check_cache(c);
   if (rc != MOE_OK) return rc;
-  if (!a || a->n_seqs < 0 || a->n_rows < 0 || a->n_q_heads < 1 || a->n_q_heads % c->n_kv_heads)
+  if (!args) return MOE_ERR_INVALID_ARG;
+  moe_attention used = *args;  // with neutral values for what the call does not use
+  if (!(uses & kUsesQ)) used.n_q_heads = c->n_kv_heads, used.q = c->k, used.q_row_stride = used.q_head_stride = 0;
+  if (!(uses & kUsesOut)) used.out = c->k, used.out_row_stride = used.out_head_stride = 0, used.scale = 1.f;
+  const moe_attention *a = &used;
+  if (a->n_seqs < 0 || a->n_rows < 0 || a->n_q_heads < 1 || a->n_q_heads % c->n_kv_heads)
     return MOE_ERR_INVALID_ARG;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
     return MOE_ERR_UNSUPPORTED;

@@ -1,0 +1,647 @@
+// moe_pages.cu -- which pages of a cache a token reads: the bounds of a page's keys (moe_page_bounds) and the
+// selection by them (moe_select_pages).
+//
+//   lo_jd = min, hi_jd = max of k_d over the positions on page j
+//   score_j = sum over the query heads of a key/value head of sum_d max(q_d lo_jd, q_d hi_jd)
+//           = sum_d Q+_d hi_jd + Q-_d lo_jd,   Q+ (Q-): sum over the heads of the positive (negative) q
+// No key of the page has a larger q . k summed over the heads.
+//
+// Both read their input once and do little with it: bytes and, with few rows, latency bound them.
+#include "moe_attention.cuh"
+
+namespace attn {
+
+constexpr int kBlock = 256;
+constexpr int kWarps = kBlock / 32;
+
+__device__ __forceinline__ uint4 load16(const void *p) { return *static_cast<const uint4 *>(p); }
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static constexpr uint32_t kMost = 0x7f807f80u, kLeast = 0xff80ff80u;  // +inf, -inf
+};
+template <>
+struct Pair<__half> {
+  using V = __half2;
+  static constexpr uint32_t kMost = 0x7c007c00u, kLeast = 0xfc00fc00u;
+};
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  using V = typename Pair<T>::V;
+  const V r = __hmin2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  using V = typename Pair<T>::V;
+  const V r = __hmax2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// ------------------------------------------------------------------ bounds of a page's keys
+// Pages of a sequence that hold its new positions.
+__device__ __forceinline__ int touched(const Params &p, const Seq &s) {
+  return s.nq ? ((s.len - 1) >> p.page_shift) - (s.ctx >> p.page_shift) + 1 : 0;
+}
+
+// One block a touched page (blockIdx.x, counted over all sequences) and key/value head: D / 8 threads side
+// by side read a position, so that a page of 64 is four loads a thread, all under way at once.
+template <typename T, int D>
+__global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bounds) {
+  constexpr int kChunks = D / 8, kRows = kBlock / kChunks;
+  __shared__ int s_sum[kWarps], s_seq, s_page;
+  __shared__ uint4 s_lo[kWarps][kChunks], s_hi[kWarps][kChunks];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the sequence that the page belongs to
+  if (threadIdx.x == 0) s_seq = -1;
+  int64_t below = 0;
+  for (int b = 0; b < p.n_seqs; b += kBlock) {
+    const int i = b + threadIdx.x;
+    int mine = 0, first = 0;
+    if (i < p.n_seqs) {
+      const Seq s = load_seq(p, i, blockIdx.x == 0 && blockIdx.y == 0);
+      mine = touched(p, s), first = s.ctx >> p.page_shift;
+    }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int64_t before = below + x - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      below += s_sum[w];
+    }
+    if (before <= blockIdx.x && blockIdx.x < before + mine)
+      s_seq = i, s_page = first + static_cast<int>(blockIdx.x - before);
+    if (below > blockIdx.x && blockIdx.x > 0) break;  // (block 0 checks all sequences)
+  }
+  __syncthreads();
+  if (s_seq < 0) return;
+  const int at = s_page;
+  const Seq s = load_seq(p, s_seq, false);
+  const int page = p.table[s_seq * p.table_stride + at];
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, kDevErrBadId);
+    return;
+  }
+  const int held = min(1 << p.page_shift, s.len - (at << p.page_shift));
+  const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+  const T *k = static_cast<const T *>(p.k) + page * p.page_stride + blockIdx.y * p.head_stride + 8 * c;
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lo[e] = Pair<T>::kMost, hi[e] = Pair<T>::kLeast;
+#pragma unroll 4
+  for (int r = r0; r < held; r += kRows) {
+    const uint4 x = load16(k + r * p.tok_stride);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lo[e] = min2<T>(lo[e], y[e]), hi[e] = max2<T>(hi[e], y[e]);
+  }
+#pragma unroll
+  for (int o = kChunks; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = min2<T>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+      hi[e] = max2<T>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+    }
+  if (lane < kChunks) {
+    s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    s_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+  __syncthreads();
+  if (threadIdx.x >= 2 * kChunks) return;
+  const bool top = threadIdx.x >= kChunks;
+  uint4 v = top ? s_hi[0][c] : s_lo[0][c];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const uint4 x = top ? s_hi[w][c] : s_lo[w][c];
+    v.x = top ? max2<T>(v.x, x.x) : min2<T>(v.x, x.x);
+    v.y = top ? max2<T>(v.y, x.y) : min2<T>(v.y, x.y);
+    v.z = top ? max2<T>(v.z, x.z) : min2<T>(v.z, x.z);
+    v.w = top ? max2<T>(v.w, x.w) : min2<T>(v.w, x.w);
+  }
+  T *dst = bounds + ((static_cast<int64_t>(page) * p.hkv + blockIdx.y) * 2 + top) * D + 8 * c;
+  *reinterpret_cast<uint4 *>(dst) = v;
+}
+
+// ------------------------------------------------------------------ selection
+// The order of two pages may hang on the last bit of their scores, so it is decided in two steps: fp32 scores
+// with a bound on their error tell which pages are certainly among the k best and which are certainly
+// not; what lies between is compared by scores in fp64 (exact but for bounds and queries that differ by more
+// than 2^30).  A score is the fp32 sum of terms t_i, each of a product that is rounded once and a Q that is:
+// with at most 15 additions one after the other, it is off by less than 18 * 2^-24 sum |t_i| < kError sum |t_i|.
+constexpr float kError = 2e-6f;
+constexpr int kPagesABlock = 64;     // of a block that scores
+constexpr int kMaxPages = 65536;     // of a sequence: a bit each in shared memory
+constexpr int kKeys = 8192;          // scores that are kept in shared memory
+constexpr int kBins = 1024;
+constexpr int kFew = 64;             // pages compared in fp64 one against the other
+
+struct Select {
+  Params p;
+  const void *bounds;  // [n_pages][hkv][2][D]
+  float2 *score;       // [rows of this launch][hkv][width]: score, sum of the terms' sizes
+  int32_t *out;        // [n_rows][hkv][n_select]
+  int row0, rows, width, n_select, sink, recent;
+};
+
+__device__ __forceinline__ bool better(double a, int i, double b, int j) {
+  return a > b || (a == b && i < j);
+}
+
+// Q- and Q+ of a row and key/value head, side by side as the bounds are: in fp64, where the sum of up to 64
+// values of 16 bits is exact but for values that differ by more than 2^40.
+template <typename T, int D, typename V>
+__device__ __forceinline__ void sum_heads(const Params &p, int row, int kvh, V *s_q) {
+  const T *q = static_cast<const T *>(p.q) + row * p.q_row +
+               static_cast<int64_t>(kvh) * p.group * p.q_head;
+  for (int d = threadIdx.x; d < D; d += kBlock) {
+    double down = 0., up = 0.;
+    for (int h = 0; h < p.group; ++h) {
+      const double x = static_cast<float>(q[h * p.q_head + d]);
+      if (x < 0.) down += x; else up += x;  // (a NaN goes up)
+    }
+    s_q[d] = static_cast<V>(down), s_q[D + d] = static_cast<V>(up);
+  }
+}
+
+// Scores of kPagesABlock pages for R rows, one after the other; eight lanes take a page, so that what they
+// read is 128 bytes in a row, and three exchanges add their parts.  Rows of one sequence share its bounds.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
+  constexpr int kParts = 2 * D / 64;  // 16-byte parts of a page's bounds that a lane takes
+  constexpr int kTurns = kPagesABlock / (kBlock / 8);
+  __shared__ __align__(16) float s_q[R][2 * D];
+  const Params &p = w.p;
+  pdl_launch();
+  const int first = w.row0 + blockIdx.x * R, kvh = blockIdx.y;
+  const int page0 = blockIdx.z * kPagesABlock + (threadIdx.x >> 3), part = threadIdx.x & 7;
+  const int n = min(R, w.row0 + w.rows - first);
+  Row row[R];
+  int most = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    row[r] = {};
+    if (r < n) row[r] = load_row(p, first + r, 1);
+    // pages between the first and the last that are selected anyway
+    row[r].len = row[r].nq ? ((row[r].ctx - 1) >> p.page_shift) + 1 : 0;
+    row[r].len = row[r].len > w.n_select ? row[r].len - w.recent : 0;
+    most = max(most, row[r].len);
+  }
+  if (blockIdx.z * kPagesABlock >= most || blockIdx.z * kPagesABlock + kPagesABlock <= w.sink) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (row[r].len > 0) sum_heads<T, D>(p, first + r, kvh, s_q[r]);
+  __syncthreads();
+  const auto fetch = [&](int seq, int count, uint4 (&x)[kTurns][kParts], bool (&there)[kTurns]) {
+    int at[kTurns];
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int j = page0 + t * (kBlock / 8);
+      at[t] = j < count ? p.table[seq * p.table_stride + j] : -1;
+      there[t] = static_cast<unsigned>(at[t]) < static_cast<unsigned>(p.n_pages);
+      if (!there[t] && j < count && j >= w.sink && part == 0 && p.err) atomicOr(p.err, kDevErrBadId);
+    }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const T *src = static_cast<const T *>(w.bounds) +
+                     (static_cast<int64_t>(there[t] ? at[t] : 0) * p.hkv + kvh) * 2 * D + 8 * part;
+#pragma unroll
+      for (int e = 0; e < kParts; ++e) x[t][e] = load16(src + 64 * e);
+    }
+  };
+  uint4 x[kTurns][kParts];
+  bool there[kTurns];
+  int held = -1, held_count = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (row[r].len == 0) continue;
+    if (row[r].seq != held || row[r].len > held_count) {
+      held = row[r].seq, held_count = row[r].len;
+#pragma unroll
+      for (int z = r + 1; z < R; ++z)  // what the later rows of the sequence want too
+        if (row[z].seq == held) held_count = max(held_count, row[z].len);
+      fetch(held, held_count, x, there);
+    }
+    float4 q[kParts][2];
+#pragma unroll
+    for (int e = 0; e < kParts; ++e) {
+      const float4 *src = reinterpret_cast<const float4 *>(s_q[r] + 64 * e + 8 * part);
+      q[e][0] = src[0], q[e][1] = src[1];
+    }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      float s[kParts], a[kParts];
+#pragma unroll
+      for (int e = 0; e < kParts; ++e) {  // sums of eight terms
+        const float2 b0 = Half<T>::unpack(x[t][e].x), b1 = Half<T>::unpack(x[t][e].y),
+                     b2 = Half<T>::unpack(x[t][e].z), b3 = Half<T>::unpack(x[t][e].w);
+        const float b[8] = {b0.x, b0.y, b1.x, b1.y, b2.x, b2.y, b3.x, b3.y};
+        const float y[8] = {q[e][0].x, q[e][0].y, q[e][0].z, q[e][0].w,
+                            q[e][1].x, q[e][1].y, q[e][1].z, q[e][1].w};
+        s[e] = a[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[e] = fmaf(y[i], b[i], s[e]);
+          a[e] = fmaf(fabsf(y[i]), fabsf(b[i]), a[e]);
+        }
+      }
+#pragma unroll
+      for (int o = kParts / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < o; ++e) s[e] += s[e + o], a[e] += a[e + o];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+        a[0] += __shfl_xor_sync(0xffffffffu, a[0], o);
+      }
+      const int j = page0 + t * (kBlock / 8);
+      if (part == 0 && j < row[r].len)
+        w.score[(static_cast<int64_t>(blockIdx.x * R + r) * p.hkv + kvh) * w.width + j] =
+            there[t] ? make_float2(s[0], a[0]) : make_float2(kNegInf, 0.f);
+    }
+  }
+}
+
+// Larger scores have larger keys; NaN has -infinity's.
+__device__ __forceinline__ uint32_t key_of(float s) {
+  if (!(s == s)) s = kNegInf;
+  const uint32_t b = __float_as_uint(s);
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+}
+__device__ __forceinline__ uint64_t key_of(double s) {
+  if (!(s == s)) s = -__builtin_huge_val();
+  const uint64_t b = __double_as_longlong(s);
+  return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+
+// Sum over the block, for every thread.
+__device__ __forceinline__ int block_sum(int v, int *s_sum) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += s_sum[w];
+  return all;
+}
+// Sum over the threads before this one.
+__device__ __forceinline__ int block_below(int v, int *s_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) base += s_sum[w];
+  return base + x - v;
+}
+
+// One block a row and key/value head.
+template <typename T, int D>
+__global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
+  extern __shared__ uint32_t s_dyn[];
+  __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_at[kFew];
+  __shared__ uint32_t s_lo, s_hi;
+  __shared__ float s_size;
+  __shared__ double s_q[2 * D], s_exact[kFew];
+  const Params &p = w.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row_i = w.row0 + blockIdx.x, kvh = blockIdx.y;
+  if (row_i == 0 && kvh == 0)
+    for (int i = threadIdx.x; i < p.n_seqs; i += kBlock) load_seq(p, i, true);
+  const Row row = load_row(p, row_i, 1);
+  const int pages = row.nq ? ((row.ctx - 1) >> p.page_shift) + 1 : 0;
+  int32_t *out = w.out + (static_cast<int64_t>(row_i) * p.hkv + kvh) * w.n_select;
+  if (pages <= w.n_select) {
+    pdl_wait();
+    if (row.nq)
+      for (int i = threadIdx.x; i < w.n_select; i += kBlock) out[i] = i < pages ? i : -1;
+    return;
+  }
+  const int words = (pages + 31) / 32, j0 = w.sink, j1 = pages - w.recent, n = j1 - j0;
+  const int want = w.n_select - w.sink - w.recent;
+  uint32_t *s_sel = s_dyn, *s_mid = s_sel + words, *s_bins = s_mid + words, *s_keys = s_bins + kBins;
+  for (int i = threadIdx.x; i < words; i += kBlock) {
+    uint32_t m = 0;
+    for (int b = 0; b < 32; ++b) {
+      const int j = 32 * i + b;
+      if (j < pages && (j < j0 || j >= j1)) m |= 1u << b;
+    }
+    s_sel[i] = m, s_mid[i] = 0u;
+  }
+  if (threadIdx.x == 0) s_lo = ~0u, s_hi = 0u, s_size = 0.f, s_count = 0;
+  __syncthreads();
+  pdl_wait();
+  float2 *score = w.score + (static_cast<int64_t>(blockIdx.x) * p.hkv + kvh) * w.width;
+  const bool kept = n <= kKeys;
+  const auto key_at = [&](int i) { return kept ? s_keys[i] : key_of(score[j0 + i].x); };
+  if (want > 0) {
+    uint32_t lo = ~0u, hi = 0u;
+    float size = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kBlock) {
+      const float2 s = score[j0 + i];
+      const uint32_t key = key_of(s.x);
+      if (kept) s_keys[i] = key;
+      lo = min(lo, key), hi = max(hi, key);
+      size = s.y <= size ? size : s.y;  // (a NaN stays)
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+    // sizes are positive or NaN: their order is that of their bits
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+    if (lane == 0) {
+      atomicMin(&s_lo, lo), atomicMax(&s_hi, hi);
+      atomicMax(reinterpret_cast<uint32_t *>(&s_size), most);
+    }
+    __syncthreads();
+    // [lo, hi]: keys among which the want-th largest is; `above` keys are larger than those
+    lo = s_lo, hi = s_hi;
+    size = s_size;
+    if (!(size <= 3e38f)) size = -kNegInf;
+    const float error = 2.f * kError * size + 1e-40f;  // (products below fp32's range)
+    int above = 0, inside = n;
+    while (lo < hi && inside > 1) {
+      const int shift = max(0, 32 - __clz(hi - lo) - 10);
+      for (int i = threadIdx.x; i < kBins; i += kBlock) s_bins[i] = 0u;
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kBlock) {
+        const uint32_t key = key_at(i);
+        if (lo <= key && key <= hi) atomicAdd(&s_bins[(key - lo) >> shift], 1u);
+      }
+      __syncthreads();
+      // bins from the largest keys down, four a thread
+      uint32_t c[4];
+      int sum = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = s_bins[kBins - 1 - 4 * threadIdx.x - e], sum += c[e];
+      int before = above + block_below(sum, s_sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (before < want && want <= before + static_cast<int>(c[e]))
+          s_bin = kBins - 1 - 4 * threadIdx.x - e, s_above = before, s_in_bin = c[e];
+        before += c[e];
+      }
+      __syncthreads();
+      const uint32_t from = lo + (static_cast<uint32_t>(s_bin) << shift);
+      lo = from;
+      hi = min(hi, from + ((1u << shift) - 1));
+      above = s_above, inside = s_in_bin;
+    }
+    // certainly in, and those that only fp64 can tell
+    const float t_hi = score_of(hi) + error, t_lo = score_of(lo) - error;
+    int in = 0, mid = 0;
+    const int whole = (n + 31) / 32 * 32;
+    for (int i = threadIdx.x; i < whole; i += kBlock) {
+      bool is_in = false, is_mid = false;
+      if (i < n) {
+        const float s = score_of(key_at(i));
+        is_in = s > t_hi;
+        is_mid = !is_in && !(s < t_lo);
+      }
+      in += is_in, mid += is_mid;
+      const int j = j0 + i;
+      if (is_in) atomicOr(&s_sel[j >> 5], 1u << (j & 31));
+      if (is_mid) {
+        atomicOr(&s_mid[j >> 5], 1u << (j & 31));
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kFew) s_at[at] = j;
+      }
+    }
+    in = block_sum(in, s_sum);
+    mid = block_sum(mid, s_sum);
+    const int need = want - in;  // of the mid ones: 1 .. mid
+    if (need >= mid) {
+      for (int i = threadIdx.x; i < words; i += kBlock) s_sel[i] |= s_mid[i];
+    } else {
+      sum_heads<T, D>(p, row_i, kvh, s_q);
+      __syncthreads();
+      bool any = false;
+      for (int d = threadIdx.x; d < 2 * D; d += kBlock) any |= s_q[d] != 0.;
+      any = __syncthreads_or(any);  // without (a row of padding), all scores are 0
+      const auto exact = [&](int j) {  // a whole warp
+        const int page = p.table[row.seq * p.table_stride + j];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages))
+          return -__builtin_huge_val();
+        const T *src =
+            static_cast<const T *>(w.bounds) + (static_cast<int64_t>(page) * p.hkv + kvh) * 2 * D;
+        double x = 0.;
+        for (int d = lane; d < 2 * D; d += 32)
+          x = fma(s_q[d], static_cast<double>(static_cast<float>(src[d])), x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x == x ? x : -__builtin_huge_val();
+      };
+      if (any && mid <= kFew) {
+        for (int i = warp; i < mid; i += kWarps) {
+          const double x = exact(s_at[i]);
+          if (lane == 0) s_exact[i] = x;
+        }
+        __syncthreads();
+        if (threadIdx.x < mid) {
+          const double x = s_exact[threadIdx.x];
+          const int j = s_at[threadIdx.x];
+          int ahead = 0;
+          for (int i = 0; i < mid; ++i) ahead += better(s_exact[i], s_at[i], x, j);
+          if (ahead < need) atomicOr(&s_sel[j >> 5], 1u << (j & 31));
+        }
+      } else {
+        // Many pages with the same score but for rounding.  Their fp64 keys take the scores' place, and
+        // the need-th largest is found bit by bit.
+        uint64_t *key = reinterpret_cast<uint64_t *>(score);
+        for (int i = warp; any && i < words; i += kWarps)
+          for (uint32_t m = s_mid[i]; m; m &= m - 1) {
+            const int j = 32 * i + __ffs(m) - 1;
+            const double x = exact(j);
+            if (lane == 0) key[j] = key_of(x);
+          }
+        __syncthreads();
+        const auto count = [&](uint64_t least) {
+          int c = 0;
+          for (int i = threadIdx.x; i < words; i += kBlock)
+            for (uint32_t m = s_mid[i]; m; m &= m - 1) c += key[32 * i + __ffs(m) - 1] >= least;
+          return block_sum(c, s_sum);
+        };
+        uint64_t last = 0;
+        for (int b = 63; any && b >= 0; --b)
+          if (count(last | 1ull << b) >= need) last |= 1ull << b;
+        const int ties = any ? need - count(last + 1) : need;  // the lower pages
+        const int each = (words + kBlock - 1) / kBlock;
+        const int i0 = min(words, static_cast<int>(threadIdx.x) * each), i1 = min(words, i0 + each);
+        int mine = 0;
+        for (int i = i0; i < i1; ++i)
+          for (uint32_t m = s_mid[i]; m; m &= m - 1) mine += !any || key[32 * i + __ffs(m) - 1] == last;
+        int before = block_below(mine, s_sum);
+        for (int i = i0; i < i1; ++i)
+          for (uint32_t m = s_mid[i]; m; m &= m - 1) {
+            const uint64_t x = any ? key[32 * i + __ffs(m) - 1] : last;
+            if (x > last || (x == last && before++ < ties)) s_sel[i] |= m & -m;
+          }
+      }
+    }
+    __syncthreads();
+  }
+  // the pages in order
+  int done = 0;
+  for (int b = 0; b < words; b += kBlock) {
+    const int i = b + threadIdx.x;
+    const uint32_t mine = i < words ? s_sel[i] : 0u;
+    int at = done + block_below(__popc(mine), s_sum);
+    for (uint32_t m = mine; m; m &= m - 1, ++at)
+      if (at < w.n_select) out[at] = 32 * i + __ffs(m) - 1;
+    done += block_sum(__popc(mine), s_sum);
+  }
+}
+
+struct SelectPlan {
+  int rows;       // of one launch
+  int64_t bytes;
+};
+
+// Scores of all rows at once, while they take no more than this.
+constexpr int64_t kMostScores = 1ll << 28;
+
+static int plan_select(const Params &p, SelectPlan *plan) {
+  if (p.table_width > kMaxPages || p.hkv > 65535) return MOE_ERR_UNSUPPORTED;
+  const int64_t row = 8ll * p.hkv * p.table_width;
+  plan->rows = static_cast<int>(std::min<int64_t>(p.n_rows, std::max<int64_t>(1, kMostScores / row)));
+  plan->bytes = row * plan->rows;
+  return MOE_OK;
+}
+
+template <typename T, int D>
+static cudaError_t launch_select(Select &w, const SelectPlan &plan, cudaStream_t stream) {
+  const Params &p = w.p;
+  const int words = (p.table_width + 31) / 32;
+  const int smem = 4 * (2 * words + kBins + std::min(p.table_width, kKeys));
+  const auto pick = pick_kernel<T, D>;
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(pick),
+                            4 * (2 * (kMaxPages / 32) + kBins + kKeys));
+  if (e != cudaSuccess) return e;
+  const unsigned chunks = (p.table_width + kPagesABlock - 1) / kPagesABlock;
+  for (w.row0 = 0; w.row0 < p.n_rows; w.row0 += plan.rows) {
+    w.rows = std::min(plan.rows, p.n_rows - w.row0);
+    const bool scored = p.table_width > w.n_select;
+    // sequences of some rows share what is read
+    if (!scored)
+      ;  // every page of every row is selected
+    else if (p.n_rows >= 4 * static_cast<int64_t>(p.n_seqs))
+      score_kernel<T, D, 4><<<dim3((w.rows + 3) / 4, p.hkv, chunks), kBlock, 0, stream>>>(w);
+    else
+      score_kernel<T, D, 1><<<dim3(w.rows, p.hkv, chunks), kBlock, 0, stream>>>(w);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(w.rows, p.hkv);
+    cfg.blockDim = dim3(kBlock);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = scored ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, pick, w);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace attn
+
+extern "C" int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *a, void *bounds,
+                               void *stream) {
+  attn::Params p;
+  const int rc = attn::check_attention(cache, a, &p, 0);
+  if (rc != MOE_OK) return rc;
+  if (!bounds || !attn::aligned(bounds, 16)) return MOE_ERR_INVALID_ARG;
+  if (p.hkv > 65535) return MOE_ERR_UNSUPPORTED;
+  if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
+  // a sequence of r > 0 rows has new positions on at most min(r, (r - 1) / page + 2) pages
+  const int64_t pages = std::min<int64_t>(p.n_rows, (p.n_rows >> p.page_shift) + 2ll * p.n_seqs);
+  const dim3 grid(static_cast<unsigned>(pages), p.hkv);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cache->dtype == MOE_DTYPE_BF16) {
+    auto *b = static_cast<__nv_bfloat16 *>(bounds);
+    if (cache->head_dim == 64)
+      attn::bounds_kernel<__nv_bfloat16, 64><<<grid, attn::kBlock, 0, st>>>(p, b);
+    else
+      attn::bounds_kernel<__nv_bfloat16, 128><<<grid, attn::kBlock, 0, st>>>(p, b);
+  } else {
+    auto *b = static_cast<__half *>(bounds);
+    if (cache->head_dim == 64)
+      attn::bounds_kernel<__half, 64><<<grid, attn::kBlock, 0, st>>>(p, b);
+    else
+      attn::bounds_kernel<__half, 128><<<grid, attn::kBlock, 0, st>>>(p, b);
+  }
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" int moe_select_pages_workspace(const moe_kv_cache *cache, const moe_attention *a,
+                                          int64_t *bytes) {
+  attn::Params p;
+  int rc = attn::check_attention(cache, a, &p, attn::kUsesQ);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
+  attn::SelectPlan plan;
+  rc = attn::plan_select(p, &plan);
+  if (rc == MOE_OK) *bytes = plan.bytes;
+  return rc;
+}
+
+extern "C" int moe_select_pages(const moe_kv_cache *cache, const moe_attention *a, const void *bounds,
+                                int32_t n_select, int32_t sink, int32_t recent, int32_t *pages,
+                                void *workspace, int64_t workspace_bytes, void *stream) {
+  attn::Select w;
+  int rc = attn::check_attention(cache, a, &w.p, attn::kUsesQ);
+  if (rc != MOE_OK) return rc;
+  if (sink < 0 || recent < 1 || n_select < static_cast<int64_t>(sink) + recent ||
+      !attn::aligned(bounds, 16) || !attn::aligned(pages, 4) || workspace_bytes < 0 ||
+      !attn::aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (w.p.n_seqs == 0 || w.p.n_rows == 0) return MOE_OK;
+  if (!bounds || !pages) return MOE_ERR_INVALID_ARG;
+  attn::SelectPlan plan;
+  rc = attn::plan_select(w.p, &plan);
+  if (rc != MOE_OK) return rc;
+  if (!workspace || workspace_bytes < plan.bytes) return MOE_ERR_INVALID_ARG;
+  w.bounds = bounds;
+  w.score = static_cast<float2 *>(workspace);
+  w.out = pages;
+  w.width = w.p.table_width;
+  w.n_select = n_select;
+  w.sink = sink;
+  w.recent = recent;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == MOE_DTYPE_BF16)
+    e = cache->head_dim == 64 ? attn::launch_select<__nv_bfloat16, 64>(w, plan, st)
+                              : attn::launch_select<__nv_bfloat16, 128>(w, plan, st);
+  else
+    e = cache->head_dim == 64 ? attn::launch_select<__half, 64>(w, plan, st)
+                              : attn::launch_select<__half, 128>(w, plan, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

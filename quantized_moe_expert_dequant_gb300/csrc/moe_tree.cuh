@@ -26,6 +26,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_attention.cuh"
 
@@ -64,6 +65,8 @@ struct Work {
   float *part;      // [2 G][ROWS][D] partial outputs: slot 2c the CTA's first item, 2c + 1 its last
   float2 *part_ml;  // [2 G][ROWS] (maximum, sum)
   Shared *shared;   // [G]
+  const int32_t *list;  // [n_rows][hkv][n_list] pages of each row, of its table; null: all of them
+  int n_list;
 };
 
 // All threads of the cluster's CTAs.  The aligned form wants converged warps, and the code before it may have
@@ -138,6 +141,52 @@ __device__ __forceinline__ void load_tile(const Params &p, int len, const int (&
       atomicOr(p.err, kDevErrBadId);
 }
 
+// The same for listed pages: see[e] of the 16 positions are seen (the others are not read).
+template <int TILE>
+__device__ __forceinline__ void load_listed(const Params &p, const int32_t *list, int seq, int limit,
+                                            int len, int tile, int (&pg)[TILE / 16],
+                                            int (&see)[TILE / 16]) {
+#pragma unroll
+  for (int e = 0; e < TILE / 16; ++e) {
+    const int pos = tile * TILE + 16 * e;
+    const int at = pos < len ? list[pos >> p.page_shift] : -1;
+    const bool seen = at >= 0 && at <= (limit - 1) >> p.page_shift;
+    pg[e] = seen ? p.table[seq * p.table_stride + at] : -1;
+    const int left = limit - (at << p.page_shift) - (pos & ((1 << p.page_shift) - 1));
+    see[e] = seen ? max(0, min(left, 16)) : 0;
+  }
+}
+
+template <typename T, int D, int TILE>
+__device__ __forceinline__ void load_listed_tile(const Params &p, const int (&pg)[TILE / 16],
+                                                 const int (&see)[TILE / 16], int64_t head_off,
+                                                 int tile, uint32_t k_smem, uint32_t v_smem,
+                                                 int *s_see) {
+  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
+  const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+#pragma unroll
+  for (int i = 0; i < TILE / kStep; ++i) {
+    const int r = r0 + i * kStep, pos = tile * TILE + r;
+    const int page = pg[i * kStep / 16];
+    const bool valid = (r & 15) < see[i * kStep / 16] &&
+                       static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+    const int64_t off = valid ? page * p.page_stride + head_off +
+                                    (pos & ((1 << p.page_shift) - 1)) * p.tok_stride + 8 * c
+                              : 0;
+    const uint32_t d = swizzled<D>(r, c);
+    cp_async16(k_smem + d, static_cast<const T *>(p.k) + off, valid);
+    cp_async16(v_smem + d, static_cast<const T *>(p.v) + off, valid);
+  }
+#pragma unroll
+  for (int e = 0; e < TILE / 16; ++e)
+    if (threadIdx.x == e) {
+      const bool bad =
+          see[e] > 0 && static_cast<unsigned>(pg[e]) >= static_cast<unsigned>(p.n_pages);
+      if (bad && p.err) atomicOr(p.err, kDevErrBadId);
+      s_see[e] = bad ? 0 : see[e];
+    }
+}
+
 // Sums v over the block (every thread gets the sum) and gives each thread the sum before it.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_t *before) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -161,8 +210,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 }
 
 // CS > 0: a cluster of CS CTAs takes an item, each an even part of its tiles, and joins the parts in
-// distributed shared memory.
-template <typename T, int D, int WR, int CS>
+// distributed shared memory.  SPARSE: items are rows and their lists of pages (w.list).
+template <typename T, int D, int WR, int CS, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w) {
   constexpr int kTile = Tree<D>::kTile;
   constexpr int ROWS = 16 * WR, WT = 4 / WR, TW = kTile / WT;  // TW positions of a warp per tile
@@ -172,7 +221,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
   __shared__ int64_t s_warp[4], s_before;
   __shared__ int s_seq;
   __shared__ float2 s_part_ml[ROWS];
+  __shared__ int s_see[SPARSE ? kStages : 1][kTile / 16];
+  using Item = std::conditional_t<SPARSE, Row, Seq>;
   const Params &p = w.p;
+  const int n_items = SPARSE ? p.n_rows : p.n_seqs;  // a key/value head
+  const auto load = [&](int i, bool report) -> Item {
+    if constexpr (SPARSE)
+      return load_row(p, i, w.n_list);
+    else
+      return load_seq(p, i, report);
+  };
+  if constexpr (SPARSE) {
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < p.n_seqs; i += kThreads) load_seq(p, i, true);
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
   const int wr = warp % WR, wt = warp / WR;
 
@@ -180,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
   if constexpr (CS > 0) {
     const int item = blockIdx.x / CS, rank = blockIdx.x % CS;
     const int sq = item / p.hkv, head = item - sq * p.hkv;
-    const Seq q = load_seq(p, sq, rank == 0 && head == 0 && threadIdx.x == 0);
+    const Item q = load(sq, rank == 0 && head == 0 && threadIdx.x == 0);
     if (q.nq == 0) return;  // the whole cluster
     const int nt = (q.len + kTile - 1) / kTile;
     // tiles count from the beginning of the sequence's line, as below
@@ -190,20 +252,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
   } else {
     pdl_launch();
     // all tiles, and the sequence in which this CTA's part of them begins
-    const auto weight = [&](const Seq &s) {
+    const auto weight = [&](const Item &s) {
       return s.nq ? static_cast<int64_t>(p.hkv) * ((s.len + kTile - 1) / kTile) : 0;
     };
     const bool first_cta = blockIdx.x == 0;
     int64_t before, mine = 0;
-    for (int b = 0; b < p.n_seqs; b += kThreads) {
+    for (int b = 0; b < n_items; b += kThreads) {
       const int i = b + threadIdx.x;
-      mine = i < p.n_seqs ? weight(load_seq(p, i, first_cta)) : 0;
+      mine = i < n_items ? weight(load(i, first_cta)) : 0;
       total += block_scan(mine, s_warp, &before);
     }
     // A CTA's time grows with its tiles, that of join_kernel with an item's parts: with n tiles an item the
     // shortest is near sqrt(n) / 2 tiles a CTA.  (One token, positions: us with 2, 4, 8 tiles of 64 at
     // least.  500: 7.8, 9.6, 12.9; 4000: 16.2, 14.4, 15.2; 16384: 21.6, 21.5, 22.9.)
-    const float per_item = static_cast<float>(total) / (static_cast<float>(p.n_seqs) * p.hkv);
+    const float per_item = static_cast<float>(total) / (static_cast<float>(n_items) * p.hkv);
     const int least = min(kMaxLeast / kTile, max(kMinPositions / kTile,
                                                  static_cast<int>(0.5f * sqrtf(per_item) + 0.5f)));
     ctas = min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least);
@@ -211,13 +273,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     if (blockIdx.x >= ctas) return;
     at = blockIdx.x * total / ctas;
     end = (blockIdx.x + 1) * total / ctas;
-    if (p.n_seqs <= kThreads) {
+    if (n_items <= kThreads) {
       if (before <= at && at < before + mine) s_seq = threadIdx.x, s_before = before;
     } else {
       int64_t sum = 0;
       for (int b = 0; sum <= at; b += kThreads) {
         const int i = b + threadIdx.x;
-        mine = i < p.n_seqs ? weight(load_seq(p, i, false)) : 0;
+        mine = i < n_items ? weight(load(i, false)) : 0;
         const int64_t all = block_scan(mine, s_warp, &before);
         before += sum;
         if (before <= at && at < before + mine) s_seq = i, s_before = before;
@@ -236,50 +298,71 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     const int32_t *pages;
     int64_t head_off;
     int left, seq, kvh, t, nt, len, stage, pg[kTile / 16];
-    Seq next;
+    Item next;
+    int limit, table, see[kTile / 16];  // listed pages: pages is the list, of pages of sequence `table`
   } ld;
+  const auto look_up = [&]() {
+    if constexpr (SPARSE)
+      load_listed<kTile>(p, ld.pages, ld.table, ld.limit, ld.len, ld.t, ld.pg, ld.see);
+    else
+      load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
+  };
   {
     const int64_t in_seq = at - s_before;
-    const Seq q = load_seq(p, s_seq, false);
+    const Item q = load(s_seq, false);
     ld.left = static_cast<int>(end - at);
     ld.seq = s_seq, ld.len = q.len, ld.nt = (q.len + kTile - 1) / kTile;
     ld.kvh = static_cast<int>(in_seq / ld.nt);
     ld.t = static_cast<int>(in_seq - static_cast<int64_t>(ld.kvh) * ld.nt);
     ld.stage = 0;
-    ld.pages = p.table + ld.seq * p.table_stride;
+    if constexpr (SPARSE) {
+      ld.pages = w.list + (static_cast<int64_t>(ld.seq) * p.hkv + ld.kvh) * w.n_list;
+      ld.limit = q.ctx, ld.table = q.seq;
+    } else {
+      ld.pages = p.table + ld.seq * p.table_stride;
+    }
     ld.head_off = ld.kvh * p.head_stride;
-    load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
-    ld.next = load_seq(p, min(ld.seq + 1, p.n_seqs - 1), false);
+    look_up();
+    ld.next = load(min(ld.seq + 1, n_items - 1), false);
   }
   const auto next_item = [&]() {
     ld.t = 0;
     ld.head_off += p.head_stride;
+    if (SPARSE) ld.pages += w.n_list;
     if (++ld.kvh < p.hkv) return;
     ld.kvh = 0;
     ld.head_off = 0;
     bool empty = true;  // sequences without rows have no tiles
-    while (empty && ++ld.seq < p.n_seqs) {
+    while (empty && ++ld.seq < n_items) {
       ld.len = ld.next.len, ld.nt = (ld.len + kTile - 1) / kTile;
       empty = ld.next.nq == 0;
-      ld.next = load_seq(p, min(ld.seq + 1, p.n_seqs - 1), false);
+      if constexpr (SPARSE) ld.limit = ld.next.ctx, ld.table = ld.next.seq;
+      ld.next = load(min(ld.seq + 1, n_items - 1), false);
     }
     if (empty) ld.left = 0;
-    ld.pages = p.table + ld.seq * p.table_stride;
+    if constexpr (SPARSE)
+      ld.pages = w.list + static_cast<int64_t>(ld.seq) * p.hkv * w.n_list;
+    else
+      ld.pages = p.table + ld.seq * p.table_stride;
   };
   const auto copy_next = [&]() {
     if (ld.left > 0) {
       const uint32_t st = base + ld.stage * 2 * kTileBytes;
-      load_tile<T, D, kTile>(p, ld.len, ld.pg, ld.head_off, ld.t, st, st + kTileBytes);
+      if constexpr (SPARSE)
+        load_listed_tile<T, D, kTile>(p, ld.pg, ld.see, ld.head_off, ld.t, st, st + kTileBytes,
+                                      s_see[ld.stage]);
+      else
+        load_tile<T, D, kTile>(p, ld.len, ld.pg, ld.head_off, ld.t, st, st + kTileBytes);
       if (++ld.stage == kStages) ld.stage = 0;
       --ld.left;
       if (++ld.t == ld.nt) next_item();
-      if (ld.left > 0) load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
+      if (ld.left > 0) look_up();
     }
     cp_async_commit();
   };
 
   int seq = ld.seq, kvh = ld.kvh, t0 = ld.t, stage = 0;
-  Seq s = load_seq(p, seq, false);
+  Item s = load(seq, false);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy_next();
   while (at < end) {
@@ -300,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       qp[h] = reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) +
                                                  (s.row0 + row_q[h]) * p.q_row + head * p.q_head);
       // without masks: bits 0 .. query
+      if (SPARSE) continue;
       row_mask[h] = p.mask ? p.mask[s.row0 + row_q[h]] : ~0ull >> (63 - row_q[h]);
     }
     uint32_t qa[D / 16][4];
@@ -319,6 +403,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       cp_async_wait<kStages - 2>();
       __syncthreads();  // tile t is there, and every warp is done with the tile before
       const uint32_t ks = base + stage * 2 * kTileBytes, vs = ks + kTileBytes;
+      int see[TW / 16];
+      if constexpr (SPARSE) {
+#pragma unroll
+        for (int j = 0; j < TW / 16; ++j) see[j] = s_see[stage][wt * (TW / 16) + j];
+      }
       if (++stage == kStages) stage = 0;
 
       float sc[TW / 8][4];
@@ -336,7 +425,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
           Half<T>::mma(sc[2 * j + 1], qa[kk], b[2], b[3]);
         }
       copy_next();
-      if ((t + 1) * kTile > s.ctx) {  // drafted positions, and those behind the sequence
+      if constexpr (SPARSE) {
+#pragma unroll
+        for (int j = 0; j < TW / 8; ++j)
+          if (see[j / 2] < 16)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (8 * (j & 1) + 2 * q4 + (e & 1) >= see[j / 2]) sc[j][e] = kNegInf;
+      } else if ((t + 1) * kTile > s.ctx) {  // drafted positions, and those behind the sequence
         const int pos0 = t * kTile + wt * TW + 2 * q4;
 #pragma unroll
         for (int j = 0; j < TW / 8; ++j)
@@ -469,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       kvh = 0;
       do {
         if (CS > 0) break;
-        if (++seq >= p.n_seqs) return;  // the end of the line
-        s = load_seq(p, seq, false);
+        if (++seq >= n_items) return;  // the end of the line
+        s = load(seq, false);
       } while (s.nq == 0);
     }
   }
@@ -555,6 +651,99 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Work w) {
                                                head * p.o_head + V * lane);
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) dst[e] = Half<T>::pack(x[2 * e] * inv, x[2 * e + 1] * inv);
+}
+
+struct Plan {
+  int grid, rows;  // CTAs, rows of a tile
+  int cluster;     // CTAs of an item's cluster; 0: all CTAs share all items
+  int64_t part, ml, shared, bytes;  // offsets in the workspace
+};
+
+constexpr int64_t kClusterPositions = 16384;  // up to which a cluster takes an item
+
+// Of n items a key/value head with up to `rows` rows and `positions` positions each; `most_items` of them
+// at most can have any.
+inline int make_plan(const moe_kv_cache *c, const Params &p, int64_t n, int64_t most_items,
+                     int64_t rows, int64_t positions, Plan *plan) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  plan->rows = rows <= 16 ? 16 : 32;
+  // With few items a cluster takes each, when the 16 or 8 CTAs of every one can be resident at once: one
+  // kernel instead of two.  (32 query, 8 key/value heads of 128, one token, shared line against clusters
+  // of 16: 500 positions 8.5, 6.8 us; 4000 15.1, 10.8; 8000 18.2, 14.8; 16000 21.8, 22.6; 32000 34.7,
+  // 39.2.  16 items of 4000: 15.2, clusters of 16 17.2, of 8 12.4; 32 items of 2000: 13.8, of 8 10.1.)
+  plan->cluster = 0;
+  plan->part = plan->ml = plan->shared = plan->bytes = 0;
+  const int64_t clusters = n * p.hkv;
+  if (positions <= kClusterPositions)
+    plan->cluster = clusters * 16 <= sms ? 16 : clusters * 8 <= sms * kCtasPerSm ? 8 : 0;
+  plan->grid = static_cast<int>(clusters) * plan->cluster;
+  if (plan->cluster) return MOE_OK;
+  // no more CTAs than the largest batch that the arguments allow has work for
+  const int64_t len = positions / tile_of(c->head_dim) + 1;
+  const int64_t items = most_items * p.hkv;
+  const int64_t most = len >= INT32_MAX || items >= INT32_MAX ? INT64_MAX : items * len;
+  if (most / (sms * kCtasPerSm) >= INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  plan->grid = static_cast<int>(
+      std::min<int64_t>(sms * kCtasPerSm, most * tile_of(c->head_dim) / kMinPositions + 1));
+  plan->part = 0;
+  plan->ml = plan->part + 8ll * plan->grid * plan->rows * c->head_dim;
+  plan->shared = plan->ml + 16ll * plan->grid * plan->rows;
+  plan->bytes = plan->shared + static_cast<int64_t>(sizeof(Shared)) * plan->grid;
+  return MOE_OK;
+}
+
+inline void use_workspace(const Plan &plan, void *workspace, Work *w) {
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  w->part = reinterpret_cast<float *>(ws + plan.part);
+  w->part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
+  w->shared = reinterpret_cast<Shared *>(ws + plan.shared);
+}
+
+// All CTAs share all items.
+template <typename T, int D, int WR, bool SPARSE>
+static cudaError_t launch_line(const Work &w, int grid, cudaStream_t stream) {
+  const auto kern = tree_kernel<T, D, WR, 0, SPARSE>;
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the joining blocks are set up while the kernel runs and wait for its end
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 16 * WR / (kThreads / 32));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, 16 * WR>, w);
+}
+
+// A cluster of CS CTAs takes each of `items` items.
+template <typename T, int D, int WR, int CS, bool SPARSE>
+static cudaError_t launch_cluster(const Work &w, int items, cudaStream_t stream) {
+  const auto kern = tree_kernel<T, D, WR, CS, SPARSE>;
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem, CS > 8);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items * CS);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Tree<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, w);
 }
 
 // A few items: each by a cluster of cs (8 or 16) CTAs.
