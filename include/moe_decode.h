@@ -408,6 +408,21 @@ int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, v
  * moe_select_pages, moe_sparse_attention).  No counterpart on the pages this library follows; the
  * rules of the calls above (streams, capture, errors on the device, workspaces) hold here too. */
 
+/* moe_tree_attention of a batch in which groups of sequences share their first positions: sequences
+ * cu_group[g] .. cu_group[g + 1] - 1 (int32 [n_groups + 1] device, ascending from >= 0 to <= n_seqs; sequences
+ * outside share nothing) hold the same keys and values at the positions 0 .. prefix_len[g] - 1 (int32 [n_groups]
+ * device).  Those are read once for the group, from the pages that its first sequence's row of the page table
+ * names; the others' rows are not read there.  Whole pages are shared: positions on the page that a
+ * prefix ends in are each sequence's own.  A sequence with fewer than prefix_len[g] positions before its
+ * queries is computed by itself.  out as by moe_tree_attention up to rounding.  workspace as for
+ * moe_tree_attention, of moe_prefix_attention_workspace bytes. */
+int moe_prefix_attention_workspace(const moe_kv_cache *cache, const moe_attention *args,
+                                   int32_t n_groups, int32_t max_q, int64_t *bytes);
+int moe_prefix_attention(const moe_kv_cache *cache, const moe_attention *args,
+                         const int32_t *cu_group, const int32_t *prefix_len, int32_t n_groups,
+                         const uint64_t *tree_mask, int32_t max_q, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
 /* The bounds of the keys on pages: for each page that holds one of the batch's new positions (ctx_len[s]
  * .. ctx_len[s] + rows - 1 of sequence s), each key/value head and dimension the least and the largest
  * key over the positions 0 .. ctx_len[s] + rows - 1 on it.  To be called when their keys are in the cache.

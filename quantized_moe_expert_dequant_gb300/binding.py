@@ -45,7 +45,8 @@ EXPORTS = ["moe_decode_create", "moe_decode_forward", "moe_decode_get_error", "m
            "moe_debug_wait_timeout", "moe_router_topk", "moe_debug_col_pieces",
            "moe_debug_col_plan", "moe_qk_norm_rope", "moe_tree_attention_workspace",
            "moe_tree_attention", "moe_prompt_attention_workspace", "moe_prompt_attention",
-           "moe_page_bounds", "moe_select_pages_workspace", "moe_select_pages",
+           "moe_prefix_attention_workspace", "moe_prefix_attention", "moe_page_bounds",
+           "moe_select_pages_workspace", "moe_select_pages",
            "moe_sparse_attention_workspace", "moe_sparse_attention",
            "moe_debug_attention_wait_cycles"]
 
@@ -139,6 +140,8 @@ def lib() -> ctypes.CDLL:
                 "moe_qk_norm_rope": [vp, vp, vp],
                 "moe_tree_attention_workspace": [vp, vp, i32, vp],
                 "moe_tree_attention": [vp, vp, vp, i32, vp, i64, vp],
+                "moe_prefix_attention_workspace": [vp, vp, i32, i32, vp],
+                "moe_prefix_attention": [vp, vp, vp, vp, i32, vp, i32, vp, i64, vp],
                 "moe_page_bounds": [vp, vp, vp, vp],
                 "moe_select_pages_workspace": [vp, vp, vp],
                 "moe_select_pages": [vp, vp, vp, i32, i32, i32, vp, vp, i64, vp],
@@ -682,6 +685,14 @@ def _workspace(fn: str, cache, workspace, stream, *args):
     return _vector(workspace, torch.uint8, n, cache._dev, "workspace"), n, workspace
 
 
+def _tree_mask(tree_mask, rows, dev) -> int:
+    if tree_mask is None:
+        return 0
+    if tree_mask.dtype not in (torch.int64, torch.uint64):
+        raise ValueError("tree_mask: 64-bit integers are wanted")
+    return _vector(tree_mask, tree_mask.dtype, rows, dev, "tree_mask")
+
+
 def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tree_mask=None,
                    scale: float | None = None, out=None, device_error=None, workspace=None,
                    stream=None):
@@ -697,11 +708,7 @@ def tree_attention(cache: KvCache, q, cu_q, ctx_len, page_table, max_q: int, tre
     dev = cache._dev
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
-    mask = 0
-    if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int64, torch.uint64):
-            raise ValueError("tree_mask: 64-bit integers are wanted")
-        mask = _vector(tree_mask, tree_mask.dtype, q.shape[0], dev, "tree_mask")
+    mask = _tree_mask(tree_mask, q.shape[0], dev)
     ws = _workspace("moe_tree_attention_workspace", cache, workspace, stream, args, max_q)
     _call("moe_tree_attention", dev, stream, cache._c, args, mask, max_q, *ws[:2])
     return out
@@ -720,6 +727,24 @@ def prompt_attention(cache: KvCache, q, cu_q, ctx_len, page_table, scale: float 
 
 
 # ---------------------------------------------------------------- without reading the whole cache
+
+def prefix_attention(cache: KvCache, q, cu_q, ctx_len, page_table, cu_group, prefix_len, max_q: int,
+                     tree_mask=None, scale: float | None = None, out=None, device_error=None,
+                     workspace=None, stream=None):
+    """moe_prefix_attention: tree_attention of sequences that share their first positions, group by group:
+    sequences cu_group[g] .. cu_group[g + 1] - 1 (int32 [n_groups + 1]) the first prefix_len[g] (int32
+    [n_groups]), which are read once for the group, by its first sequence's row of page_table.  The other
+    arguments, and what happens to sequences out of range, as for tree_attention."""
+    dev, groups = cache._dev, prefix_len.numel()
+    args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
+                                stream)
+    mask = _tree_mask(tree_mask, q.shape[0], dev)
+    ws = _workspace("moe_prefix_attention_workspace", cache, workspace, stream, args, groups, max_q)
+    _call("moe_prefix_attention", dev, stream, cache._c, args,
+          _vector(cu_group, torch.int32, groups + 1, dev, "cu_group"),
+          _vector(prefix_len, torch.int32, groups, dev, "prefix_len"), groups, mask, max_q, *ws[:2])
+    return out
+
 
 def _bounds(cache, bounds) -> int:
     shape = (cache.n_pages, cache.n_kv_heads, 2, cache.head_dim)

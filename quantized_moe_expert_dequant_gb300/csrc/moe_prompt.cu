@@ -13,7 +13,7 @@ int tiles_workspace(const moe_kv_cache *cache, const Params &p, int64_t *bytes) 
 int run_tiles(const moe_kv_cache *cache, const Params &p, void *workspace, int64_t workspace_bytes,
               cudaStream_t stream) {
   return p.mask ? run_tree_tiles(cache, p, workspace, workspace_bytes, stream)
-                : run<false>(cache, p, workspace, workspace_bytes, stream);
+                : run<kCausal>(cache, p, workspace, workspace_bytes, stream);
 }
 
 }  // namespace attn

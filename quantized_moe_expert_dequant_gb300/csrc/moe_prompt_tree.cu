@@ -6,7 +6,7 @@ namespace attn {
 
 int run_tree_tiles(const moe_kv_cache *cache, const Params &p, void *workspace,
                    int64_t workspace_bytes, cudaStream_t stream) {
-  return run<true>(cache, p, workspace, workspace_bytes, stream);
+  return run<kTree>(cache, p, workspace, workspace_bytes, stream);
 }
 
 }  // namespace attn

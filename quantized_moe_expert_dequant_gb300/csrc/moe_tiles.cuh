@@ -1,6 +1,6 @@
 // moe_tiles.cuh -- attention in tiles of 128 rows over the pages of a cache, on the 5th-generation tensor
 // cores: causal for packed prompts (moe_prompt.cu), by masks for large trees of drafted tokens
-// (moe_prompt_tree.cu).
+// (moe_prompt_tree.cu), and for batches that share a prefix (moe_prompt_shared.cu).
 //
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
 //   that row r sees, in one pass over K and V; m_r goes by some of the scores (reference).
@@ -57,13 +57,33 @@ struct Prompt {
   static constexpr bool kBeside = D == 64;
 };
 
+// kShared: sequences whose first pages are the same (moe_prefix_attention).  The rows of all sequences of a
+// group are one tall sequence over the shared positions, read once for all; each sequence's other
+// positions are items of their own, and combine_kernel joins the two.
+enum Mode { kCausal, kTree, kShared };
+
+struct Prefixes {
+  const int32_t *cu;   // [n_groups + 1] sequences of the groups
+  const int32_t *len;  // [n_groups] positions that a group shares
+  int n_groups;
+  // what whole items leave, for the prefix and for the rest: rows' outputs [2][n_rows][hq][D], their (maximum,
+  // sum) [2][n_rows][hq], and where a row's parts begin, [2][n_rows][hkv]: kInRows, or the CTA in which its item
+  // begins
+  float *out;
+  float2 *ml;
+  int32_t *begin;
+};
+constexpr int kInRows = -1;
+
 struct PromptParams {
   Params p;
+  Prefixes g;
   CUtensorMap q, k, v;
   int tokens;        // of a tile: 128 / group
   float *part;       // [2 G][2][D / 4][128][4]: parts of outputs, four columns of a tile's rows together
   float2 *part_ml;   // [2 G][2][128] (reference maximum, sum)
   struct Share *share;  // [G], null when no item can be shared
+  bool split;           // whether items are shared
   // of a wait of the copies and the products; the other warps' is fixed and they leave with these (a limit in
   // memory in each wait of the softmax: 124 us for 120 on chunks behind prefixes, heads of 64)
   tc::Limit limit;
@@ -83,6 +103,77 @@ constexpr int kMinSteps = 2;
 // us shared and not: one prompt of 700 tokens 21.6, 18.2; of 1000 27.3, 21.1; of 2000 43.7, 46.8; of
 // 4000 105, 121; 16 of 1000 147, 143.)
 constexpr int kShareSteps = 9;
+
+// A sequence as items are made of it: row `seq` of the page table, from page0 on.
+struct Part : Seq {
+  int seq, page0, rest;  // rest: 0 for a group's prefix
+};
+
+// The positions that a group shares, whole pages only (the page that a prefix ends in is each sequence's
+// own); -1 when its description is out of range.
+__device__ __forceinline__ int prefix_of(const Params &p, const Prefixes &g, int i) {
+  const int a = g.cu[i], b = g.cu[i + 1], len = g.len[i];
+  // (beside a group whose end is before its beginning, the bounds mean nothing either)
+  const bool ok = a >= 0 && a <= b && b <= p.n_seqs && len >= 0 && (i == 0 || g.cu[i - 1] <= a) &&
+                  (i + 1 == g.n_groups || b <= g.cu[i + 2]) &&
+                  len <= (static_cast<int64_t>(p.table_width) << p.page_shift) && len <= kMaxLen;
+  return ok ? len >> p.page_shift << p.page_shift : -1;
+}
+
+// The group of a sequence and the positions that it shares: 0 without a group, and when the prefix is longer
+// than what the sequence has before its queries.
+__device__ __forceinline__ int shared_by(const Params &p, const Prefixes &g, int s, int ctx, int *group) {
+  int lo = 0, hi = g.n_groups;  // the last group that begins at s or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (g.cu[mid] <= s) lo = mid; else hi = mid;
+  }
+  *group = lo;
+  if (g.n_groups == 0 || s < g.cu[lo] || s >= g.cu[lo + 1]) return 0;
+  const int len = prefix_of(p, g, lo);
+  return len > 0 && len <= ctx ? len : 0;
+}
+
+// A group's rows over its prefix.
+__device__ __forceinline__ Seq load_group(const Params &p, const Prefixes &g, int i, bool report) {
+  Seq r = {};
+  const int len = prefix_of(p, g, i);
+  bool ok = len >= 0;
+  if (len > 0 && g.cu[i] < g.cu[i + 1]) {
+    r.row0 = p.cu[g.cu[i]];
+    const int64_t end = p.cu[g.cu[i + 1]];
+    ok = r.row0 >= 0 && end >= r.row0 && end <= p.n_rows;
+    if (ok) r.nq = static_cast<int>(end - r.row0), r.ctx = r.len = len;
+  }
+  if (!ok && report && p.err) atomicOr(p.err, kDevErrBadId);
+  return r;
+}
+
+template <int MODE>
+__device__ __forceinline__ int part_count(const PromptParams &w) {
+  return MODE == kShared ? w.g.n_groups + w.p.n_seqs : w.p.n_seqs;
+}
+
+template <int MODE>
+__device__ __forceinline__ Part load_part(const PromptParams &w, int i, bool report) {
+  Part r;
+  r.seq = i, r.page0 = 0, r.rest = 1;
+  if (MODE == kShared && i < w.g.n_groups) {
+    static_cast<Seq &>(r) = load_group(w.p, w.g, i, report);
+    r.seq = r.nq ? w.g.cu[i] : 0;
+    r.rest = 0;
+    return r;
+  }
+  if (MODE == kShared) r.seq = i -= w.g.n_groups;
+  static_cast<Seq &>(r) = load_seq(w.p, i, report);
+  if (MODE == kShared && r.nq) {
+    int group;
+    const int base = shared_by(w.p, w.g, i, r.ctx, &group);
+    r.ctx -= base, r.len -= base;
+    r.page0 = base >> w.p.page_shift;
+  }
+  return r;
+}
 
 struct Spot {  // the place before a step of an item
   int seq, head, tile, step;
@@ -169,8 +260,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 }
 
 // The CTA's part of the line: from s_spot[0] to s_spot[1].  False when there is nothing at all.
-__device__ __forceinline__ bool find_part(const Params &p, bool tree, bool shared, int per,
-                                          int64_t *s_warp, Spot *s_spot) {
+template <int MODE>
+__device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_t *s_warp,
+                                          Spot *s_spot) {
+  const Params &p = w.p;
+  constexpr bool tree = MODE != kCausal;
+  const bool shared = w.split;
+  const int parts = part_count<MODE>(w);
   const auto cost = [&](const Seq &s) {
     if (s.nq == 0) return static_cast<int64_t>(0);
     const int tiles = item_count(s, per);
@@ -178,21 +274,21 @@ __device__ __forceinline__ bool find_part(const Params &p, bool tree, bool share
   };
   int64_t total = 0, below = 0, mine = 0;
   Seq s = {0, 0, 0, 0};
-  for (int b = 0; b < p.n_seqs; b += kPromptThreads) {
+  for (int b = 0; b < parts; b += kPromptThreads) {
     const int i = b + threadIdx.x;
     mine = 0;
-    if (i < p.n_seqs) s = load_seq(p, i, blockIdx.x == 0), mine = cost(s);
+    if (i < parts) s = load_part<MODE>(w, i, blockIdx.x == 0), mine = cost(s);
     total += block_scan(mine, s_warp, &below);
   }
   if (total == 0) return false;
   const int64_t edge[2] = {blockIdx.x * total / gridDim.x, (blockIdx.x + 1) * total / gridDim.x};
-  if (threadIdx.x == 0 && edge[1] == total) s_spot[1] = {p.n_seqs, 0, 0, 0};
+  if (threadIdx.x == 0 && edge[1] == total) s_spot[1] = {parts, 0, 0, 0};
   int64_t sum = 0;
-  for (int b = 0; b < p.n_seqs; b += kPromptThreads) {
+  for (int b = 0; b < parts; b += kPromptThreads) {
     const int i = b + threadIdx.x;
-    if (p.n_seqs > kPromptThreads) {
+    if (parts > kPromptThreads) {
       mine = 0;
-      if (i < p.n_seqs) s = load_seq(p, i, false), mine = cost(s);
+      if (i < parts) s = load_part<MODE>(w, i, false), mine = cost(s);
       const int64_t all = block_scan(mine, s_warp, &below);
       below += sum;
       sum += all;
@@ -209,39 +305,41 @@ __device__ __forceinline__ bool find_part(const Params &p, bool tree, bool share
 // An item as the warps work on it: the sequence, its first token here, the steps from `a` on that are
 // this CTA's, and how many of them each tile has.  more = 0: the CTA's part of the line is done.
 struct alignas(16) Item {
-  int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, pad[3];
+  int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, page0, rest, pad;
 };
 static_assert(sizeof(Item) == 64, "read as four 16-byte words");
 
 // Walks a CTA's part of the line, item by item.
+template <int MODE>
 struct Walk {
-  const Params &p;
-  const bool tree;
-  const int tokens, per;
+  static constexpr bool tree = MODE != kCausal;
+  const PromptParams &w;
+  const int tokens, per, parts;
   Spot at, end;
-  Seq s;
+  Part s;
   int tiles;
 
-  __device__ __forceinline__ Walk(const Params &p, bool tree, int tokens, const Spot *spot)
-      : p(p), tree(tree), tokens(tokens), per(2 * tokens), at(spot[0]), end(spot[1]) {
-    s = load_seq(p, min(at.seq, p.n_seqs - 1), false);
+  __device__ __forceinline__ Walk(const PromptParams &w, const Spot *spot)
+      : w(w), tokens(w.tokens), per(2 * tokens), parts(part_count<MODE>(w)), at(spot[0]), end(spot[1]) {
+    s = load_part<MODE>(w, min(at.seq, parts - 1), false);
     tiles = item_count(s, per);
   }
   __device__ __forceinline__ Item next() {
     Item r = {};
     for (;;) {
-      if (!before(at, end) || at.seq >= p.n_seqs) return r;
+      if (!before(at, end) || at.seq >= parts) return r;
       if (at.tile < tiles) break;
       at.tile = 0;
-      if (s.nq == 0 || ++at.head >= p.hkv) {
+      if (s.nq == 0 || ++at.head >= w.p.hkv) {
         at.head = 0;
-        if (++at.seq >= p.n_seqs) return r;
-        s = load_seq(p, at.seq, false);
+        if (++at.seq >= parts) return r;
+        s = load_part<MODE>(w, at.seq, false);
         tiles = item_count(s, per);
       }
     }
     r.more = 1;
-    r.seq = at.seq, r.kvh = at.head;
+    r.seq = s.seq, r.kvh = at.head;
+    r.page0 = s.page0, r.rest = s.rest;
     r.row0 = s.row0, r.ctx = s.ctx, r.nq = s.nq, r.len = s.len;
     r.tok0 = at.tile * per;
     r.a = at.step;
@@ -371,10 +469,11 @@ __device__ __forceinline__ float store_weights(const uint32_t (&x)[4][32], float
   return total.x + total.y;
 }
 
-template <typename T, int D, bool tree>
+template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams w) {
   using C = Prompt<D>;
+  constexpr bool tree = MODE != kCausal;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t s_q[2], s_q_free[2], s_full[C::kStages], s_empty[C::kStages],
       s_s[2], s_x[2], s_p[2], s_o[2], s_end, s_item_full[kItems], s_item_free[kItems];
@@ -409,7 +508,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     tc::bar_fence_init();
   }
   pdl_launch();
-  const bool any = find_part(p, tree, w.share != nullptr, 2 * w.tokens, s_warp, s_spot);
+  const bool any = find_part<MODE>(w, 2 * w.tokens, s_warp, s_spot);
   if (w.share && threadIdx.x == 0) {
     Share sh = {};
     if (any && before(s_spot[0], s_spot[1])) {
@@ -418,7 +517,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       sh.head = a.step > 0;
       sh.head_ends = !one;
       sh.tail = b.step > 0 && !(one && a.step > 0);
-      if (sh.tail) {
+      if (MODE != kShared && sh.tail) {
         const Seq q = load_seq(p, b.seq, false);
         sh.row0 = q.row0, sh.nq = q.nq, sh.kvh = b.head, sh.tok0 = b.tile * 2 * w.tokens;
       }
@@ -451,7 +550,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == kSoftmaxWarps + 2) {
     // ---------------------------------------------------------------- items, ahead of the others
     if (lane == 0) {
-      Walk walk(p, tree, w.tokens, s_spot);
+      Walk<MODE> walk(w, s_spot);
       for (int it = 0;; ++it) {
         const Item item = walk.next();
         if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone)) break;
@@ -477,7 +576,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     Item item;
     while (ok && take(item)) {
-      const int32_t *pages = p.table + item.seq * p.table_stride;
+      const int32_t *pages = p.table + item.seq * p.table_stride + (MODE == kShared ? item.page0 : 0);
       const auto page_of = [&](int t) {
         const int pos = t * kPos + b_row;
         return lane < boxes && pos < item.len ? pages[pos >> p.page_shift] : p.n_pages;
@@ -685,7 +784,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int rows = min(w.tokens, item.nq - tok_first) * p.group;
       const bool idle = 32 * (warp % 4) >= rows;
       uint64_t row_mask = 0;  // drafted positions that the row sees
-      if (tree && tok < item.nq) row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
+      if (MODE == kTree && tok < item.nq)
+        row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
+      if (MODE == kShared && item.rest && tok < item.nq) {  // (of a prefix, every position is before ctx)
+        row_mask = ~0ull >> (63 - tok);
+        if (p.mask) row_mask = p.mask[item.row0 + tok] & (~0ull >> (64 - item.nq));
+      }
       float m = kNegInf, l = 0.f;
       for (int t = 0; t < n; ++t, ++n_s) {
         ok = tc::bar_wait(bar(s_s[i]), n_s & 1, &s_gone);
@@ -795,7 +899,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // Short loops: this code runs once an item, and fetching a long stretch of it took longer than
       // running it (16 packed prompts of 1024 tokens 88 us unrolled, 76 so).
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (item.a > 0 ? 0 : 1);
-      if (!item.whole) {
+      if (MODE == kShared && r < rows && item.a == 0) {
+        const int64_t row = static_cast<int64_t>(item.rest) * p.n_rows + item.row0 + tok;
+        const int head = r - r_tok * p.group;
+        if (head == 0) w.g.begin[row * p.hkv + item.kvh] = item.whole ? kInRows : blockIdx.x;
+        if (item.whole) w.g.ml[row * p.hq + item.kvh * p.group + head] = make_float2(m, l);
+      }
+      if (MODE == kShared && item.whole) {
+        float4 *dst = reinterpret_cast<float4 *>(w.g.out) +
+                      ((static_cast<int64_t>(item.rest) * p.n_rows + item.row0 + tok) * p.hq +
+                       item.kvh * p.group + r - r_tok * p.group) * (D / 4);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          tc::tmem_load32(o, to + 32 * c);
+          tc::wait_load(o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            if (r < rows)
+              dst[8 * c + e / 4] =
+                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        }
+      } else if (!item.whole) {
         float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + i) * (D / 4) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -935,12 +1062,104 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int to
                              8 * blockIdx.y) = v;
 }
 
+// kShared: joins what the items over the prefix and over the rest have left of a sequence's rows, one block a
+// sequence and key/value head, eight columns of a row a thread; parts are added in the order of the positions.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) combine_kernel(const Params p, const Prefixes g, int tokens,
+                                                      const float *part, const float2 *part_ml,
+                                                      const Share *share, int ctas) {
+  __shared__ uint32_t s_head[kMaxCtas / 32], s_ends[kMaxCtas / 32];
+  pdl_wait();
+  const int s = blockIdx.x / p.hkv, kvh = blockIdx.x % p.hkv;
+  const Seq q = load_seq(p, s, false);
+  if (q.nq == 0) return;
+  for (int c0 = 0; c0 < kMaxCtas; c0 += 128) {
+    const int c = c0 + threadIdx.x;
+    const bool head = c < ctas && share[c].head;
+    const uint32_t heads = __ballot_sync(0xffffffffu, head);
+    const uint32_t ends = __ballot_sync(0xffffffffu, head && share[c].head_ends);
+    if (threadIdx.x % 32 == 0) s_head[c / 32] = heads, s_ends[c / 32] = ends;
+  }
+  int group;
+  const int base = shared_by(p, g, s, q.ctx, &group);
+  Seq both[2] = {{}, q};  // what the rows are counted in: the group, the sequence
+  if (base > 0) both[0] = load_group(p, g, group, false);
+  // rows outside their group's: offsets of the batch that do not fit together
+  const bool first = base > 0 && q.row0 >= both[0].row0 && q.row0 + q.nq <= both[0].row0 + both[0].nq;
+  if (base > 0 && !first) {
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, kDevErrBadId);
+    return;
+  }
+  __syncthreads();
+  const int c8 = threadIdx.x % (D / 8);
+  for (int R = blockIdx.y * (128 / (D / 8)) + threadIdx.x / (D / 8); R < q.nq * p.group;
+       R += gridDim.y * (128 / (D / 8))) {
+    const int tok = R / p.group, head = R - tok * p.group;
+    const int64_t row = q.row0 + tok;
+    // the parts, one after the other: f(maximum and sum, eight columns)
+    const auto each = [&](auto f) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k == 0 && !first) continue;
+        const int64_t at = k * static_cast<int64_t>(p.n_rows) + row;
+        const int c = g.begin[at * p.hkv + kvh];
+        if (c == kInRows) {
+          const int64_t i = at * p.hq + kvh * p.group + head;
+          f(g.ml + i, reinterpret_cast<const float4 *>(g.out) + i * (D / 4) + 2 * c8, 1);
+          continue;
+        }
+        if (static_cast<unsigned>(c) >= static_cast<unsigned>(ctas)) continue;  // (a wait gave up)
+        const int in_item = (q.row0 - both[k].row0 + tok) % (2 * tokens), i = in_item / tokens;
+        const int r = (in_item - i * tokens) * p.group + head;
+        const auto one = [&](int slot) {
+          f(part_ml + slot * 256 + i * 128 + r,
+            reinterpret_cast<const float4 *>(part) +
+                ((static_cast<int64_t>(slot) * 2 + i) * (D / 4) + 2 * c8) * 128 + r,
+            128);
+        };
+        one(2 * c + 1);
+        for (int n = c + 1; n < ctas; ++n) {
+          if (!(s_head[n / 32] >> (n % 32) & 1)) continue;  // a CTA that had no work
+          one(2 * n);
+          if (s_ends[n / 32] >> (n % 32) & 1) break;
+        }
+      }
+    };
+    float m = kNegInf;
+    each([&](const float2 *ml, const float4 *, int) { m = fmaxf(m, ml->x); });
+    float l = 0.f, o[8] = {};
+    each([&](const float2 *ml, const float4 *x, int apart) {
+      const float2 v = *ml;
+      const float4 a = x[0], b = x[apart];
+      if (!(v.y == 0.f)) {  // a part without weight may not have been written; a sum that is NaN counts
+        const float f = exp2_approx((v.x - m) * p.scale_log2);
+        l = fmaf(v.y, f, l);
+        o[0] = fmaf(a.x, f, o[0]), o[1] = fmaf(a.y, f, o[1]);
+        o[2] = fmaf(a.z, f, o[2]), o[3] = fmaf(a.w, f, o[3]);
+        o[4] = fmaf(b.x, f, o[4]), o[5] = fmaf(b.y, f, o[5]);
+        o[6] = fmaf(b.z, f, o[6]), o[7] = fmaf(b.w, f, o[7]);
+      }
+    });
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint4 v;
+    v.x = Half<T>::pack(o[0] * inv, o[1] * inv);
+    v.y = Half<T>::pack(o[2] * inv, o[3] * inv);
+    v.z = Half<T>::pack(o[4] * inv, o[5] * inv);
+    v.w = Half<T>::pack(o[6] * inv, o[7] * inv);
+    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.o_row + (kvh * p.group + head) * p.o_head +
+                               8 * c8) = v;
+  }
+}
+
 struct PromptPlan {
   int grid;
-  int64_t ml, share, bytes;  // offsets in the workspace
+  bool split;
+  int64_t ml, share, bytes;    // offsets in the workspace
+  int64_t out, row_ml, begin;  // of kShared
 };
 
-static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan) {
+// n_groups: of kShared; -1: another mode.
+static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan, int n_groups = -1) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -949,24 +1168,40 @@ static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan) {
   plan->ml = plan->share = plan->bytes = 0;
   const int64_t len = static_cast<int64_t>(p.table_width) << p.page_shift;  // of a sequence at most
   // the line's length times the CTAs stays inside 64 bits
-  const double items = static_cast<double>(p.n_rows) / (2 * (128 / p.group)) + p.n_seqs;
+  double items = static_cast<double>(p.n_rows) / (2 * (128 / p.group)) + p.n_seqs;
+  if (n_groups >= 0) items = 2 * items + n_groups;
   if (items * (static_cast<double>(len) + kItemCost) * p.hkv * sms > 4e18) return MOE_ERR_UNSUPPORTED;
-  if ((len + kPos - 1) / kPos < kShareSteps) return MOE_OK;
+  plan->split = (len + kPos - 1) / kPos >= kShareSteps;
+  if (!plan->split && n_groups < 0) return MOE_OK;
   plan->ml = 4ll * 2 * plan->grid * 256 * c->head_dim;
   plan->share = plan->ml + 8ll * 2 * plan->grid * 256;
   plan->bytes = plan->share + static_cast<int64_t>(sizeof(Share)) * plan->grid;
+  if (n_groups >= 0) {
+    const int64_t heads = 2ll * p.n_rows * p.hq;
+    plan->out = (plan->bytes + 15) / 16 * 16;
+    plan->row_ml = plan->out + 4 * heads * c->head_dim;
+    plan->begin = plan->row_ml + 8 * heads;
+    plan->bytes = plan->begin + 4 * 2ll * p.n_rows * p.hkv;
+  }
   return MOE_OK;
 }
 
-template <typename T, int D, bool TREE>
-static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan, uint8_t *ws,
-                  cudaStream_t stream) {
+template <typename T, int D, int MODE>
+static int launch(const moe_kv_cache *c, const Params &p, const Prefixes &g, const PromptPlan &plan,
+                  uint8_t *ws, cudaStream_t stream) {
   PromptParams w;
   w.p = p;
   w.tokens = 128 / p.group;
   w.part = reinterpret_cast<float *>(ws);
   w.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
   w.share = plan.bytes ? reinterpret_cast<Share *>(ws + plan.share) : nullptr;
+  w.split = plan.split;
+  w.g = g;
+  if (MODE == kShared) {
+    w.g.out = reinterpret_cast<float *>(ws + plan.out);
+    w.g.ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
+    w.g.begin = reinterpret_cast<int32_t *>(ws + plan.begin);
+  }
   if (const int64_t cycles = debug_wait_cycles.load(std::memory_order_relaxed))
     w.limit.cycles = cycles, w.limit.nap_ns = 0;
   const bool bf16 = c->dtype == MOE_DTYPE_BF16;
@@ -981,7 +1216,7 @@ static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan
       !tc::make_map(&w.k, bf16, p.k, 4, dims, str, box) ||
       !tc::make_map(&w.v, bf16, p.v, 4, dims, str, box))
     return MOE_ERR_UNSUPPORTED;
-  const auto kern = prompt_kernel<T, D, TREE>;
+  const auto kern = prompt_kernel<T, D, MODE>;
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Prompt<D>::kSmem);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -998,27 +1233,44 @@ static int launch(const moe_kv_cache *c, const Params &p, const PromptPlan &plan
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prompt_join_kernel<T, D>, p, w.tokens,
-                         static_cast<const float *>(w.part),
-                         static_cast<const float2 *>(w.part_ml),
-                         static_cast<const Share *>(w.share), plan.grid);
+  if constexpr (MODE == kShared) {
+    const int rows = 128 / (D / 8);  // of a block at a time
+    cfg.gridDim = dim3(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + rows - 1) / rows));
+    cfg.blockDim = dim3(128);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<T, D>, p, w.g, w.tokens,
+                           static_cast<const float *>(w.part),
+                           static_cast<const float2 *>(w.part_ml),
+                           static_cast<const Share *>(w.share), plan.grid);
+  } else {
+    e = cudaLaunchKernelEx(&cfg, prompt_join_kernel<T, D>, p, w.tokens,
+                           static_cast<const float *>(w.part),
+                           static_cast<const float2 *>(w.part_ml),
+                           static_cast<const Share *>(w.share), plan.grid);
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// The kernel for causal (TREE false) or masked (TREE true) attention of one cache type.
-template <bool TREE>
+template <int MODE>
+static int run_planned(const moe_kv_cache *cache, const Params &p, const Prefixes &g,
+                       const PromptPlan &plan, void *workspace, int64_t workspace_bytes,
+                       cudaStream_t stream) {
+  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MOE_ERR_INVALID_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  if (cache->dtype == MOE_DTYPE_BF16)
+    return cache->head_dim == 64 ? launch<__nv_bfloat16, 64, MODE>(cache, p, g, plan, ws, stream)
+                                 : launch<__nv_bfloat16, 128, MODE>(cache, p, g, plan, ws, stream);
+  return cache->head_dim == 64 ? launch<__half, 64, MODE>(cache, p, g, plan, ws, stream)
+                               : launch<__half, 128, MODE>(cache, p, g, plan, ws, stream);
+}
+
+// The kernel for causal or masked attention of one cache type.
+template <int MODE>
 static int run(const moe_kv_cache *cache, const Params &p, void *workspace, int64_t workspace_bytes,
                cudaStream_t stream) {
   PromptPlan plan;
   const int rc = make_plan(cache, p, &plan);
   if (rc != MOE_OK) return rc;
-  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MOE_ERR_INVALID_ARG;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if (cache->dtype == MOE_DTYPE_BF16)
-    return cache->head_dim == 64 ? launch<__nv_bfloat16, 64, TREE>(cache, p, plan, ws, stream)
-                                 : launch<__nv_bfloat16, 128, TREE>(cache, p, plan, ws, stream);
-  return cache->head_dim == 64 ? launch<__half, 64, TREE>(cache, p, plan, ws, stream)
-                               : launch<__half, 128, TREE>(cache, p, plan, ws, stream);
+  return run_planned<MODE>(cache, p, Prefixes{}, plan, workspace, workspace_bytes, stream);
 }
 
 }  // namespace attn
