@@ -596,6 +596,7 @@ class KvCache:
         self._dev = k.get_device()
         self._heads = (self.n_kv_heads, self.head_dim)
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self._shape = (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, _DTYPES[k.dtype])
         self._c = _pack_kv_cache(k.data_ptr(), v.data_ptr(), *st, self.n_pages, self.page_size,
                                  self.n_kv_heads, self.head_dim, _DTYPES[k.dtype])
 
@@ -654,22 +655,58 @@ def _batch_args(cache, a, b, T, Hq, scale, cu_q, ctx_len, page_table, device_err
     st = page_table.stride()
     if page_table.dtype != i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
         raise ValueError(f"page_table: int32 [n_seqs, width] on cuda:{dev} is wanted")
+    # the checks of _vector in one expression for the calls that pass them: on small batches the host is
+    # what takes time
+    if (cu_q.dtype is i32 and ctx_len.dtype is i32 and cu_q.get_device() == dev
+            and ctx_len.get_device() == dev and cu_q.numel() > n and ctx_len.numel() >= n
+            and cu_q.is_contiguous() and ctx_len.is_contiguous()):
+        cu, ctx = cu_q.data_ptr(), ctx_len.data_ptr()
+    else:
+        cu = _vector(cu_q, i32, n + 1, dev, "cu_q")
+        ctx = _vector(ctx_len, i32, n, dev, "ctx_len")
     return _pack_attention(
-        a[0], b[0], a[1], a[2], b[1], b[2], _vector(cu_q, i32, n + 1, dev, "cu_q"),
-        _vector(ctx_len, i32, n, dev, "ctx_len"), page_table.data_ptr(), st[0] if n > 1 else width,
-        width, n, T, Hq, scale, _vector(device_error, i32, 1, dev, "device_error"))
+        a[0], b[0], a[1], a[2], b[1], b[2], cu, ctx, page_table.data_ptr(), st[0] if n > 1 else width,
+        width, n, T, Hq, scale,
+        0 if device_error is None else _vector(device_error, i32, 1, dev, "device_error"))
 
 
 def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error, stream):
     dev, D, dt = cache._dev, cache.head_dim, cache.dtype
-    T, Hq, _ = shape = q.shape
-    if shape[2] != D:
+    T, Hq, dim = shape = q.shape
+    if dim != D:
         raise ValueError(f"q: heads of {D} are wanted")
+    a = _rows(q, shape, dt, dev, "q")
     if out is None:
         out = _empty_on(shape, dt, cache.device, stream)
-    return _batch_args(cache, _rows(q, shape, dt, dev, "q"), _rows(out, shape, dt, dev, "out"), T, Hq,
-                       D ** -0.5 if scale is None else scale, cu_q, ctx_len, page_table,
-                       device_error), out
+        b = out.data_ptr(), Hq * D, D
+    else:
+        b = _rows(out, shape, dt, dev, "out")
+    return _batch_args(cache, a, b, T, Hq, D ** -0.5 if scale is None else scale, cu_q, ctx_len,
+                       page_table, device_error), out
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn: str, dev: int, shape, n: int, width: int, T: int, Hq: int, *more) -> int:
+    """What fn answers for a cache of shape (pages, heads, positions of a page, head_dim, dtype) and a batch of
+    n sequences, T rows and Hq query heads: it goes by nothing else, and no address is read."""
+    n_pages, kv_heads, page, dim, dtype = shape
+    c = _pack_kv_cache(16, 16, 0, 0, 0, n_pages, page, kv_heads, dim, dtype)
+    a = _pack_attention(16, 16, 0, 0, 0, 0, 16, 16, 16, width, width, n, T, Hq, 1.0, 0)
+    size = ctypes.c_int64()
+    _on(dev, fn, c, a, *more, ctypes.byref(size))
+    return size.value
+
+
+def _scratch(fn: str, cache, workspace, stream, page_table, shape, *more):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one for a batch of q's shape."""
+    if workspace is None:
+        n = _workspace_bytes(fn, cache._dev, cache._shape, *page_table.shape, shape[0], shape[1], *more)
+        if n == 0:
+            return 0, 0, None
+        workspace = _empty_on(n, torch.uint8, cache.device, stream)
+        return workspace.data_ptr(), n, workspace
+    n = workspace.numel()
+    return _vector(workspace, torch.uint8, n, cache._dev, "workspace"), n, workspace
 
 
 def _workspace(fn: str, cache, workspace, stream, *args):
@@ -739,7 +776,8 @@ def prefix_attention(cache: KvCache, q, cu_q, ctx_len, page_table, cu_group, pre
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     mask = _tree_mask(tree_mask, q.shape[0], dev)
-    ws = _workspace("moe_prefix_attention_workspace", cache, workspace, stream, args, groups, max_q)
+    ws = _scratch("moe_prefix_attention_workspace", cache, workspace, stream, page_table, q.shape, groups,
+                  max_q)
     _call("moe_prefix_attention", dev, stream, cache._c, args,
           _vector(cu_group, torch.int32, groups + 1, dev, "cu_group"),
           _vector(prefix_len, torch.int32, groups, dev, "prefix_len"), groups, mask, max_q, *ws[:2])
@@ -750,7 +788,7 @@ def _bounds(cache, bounds) -> int:
     shape = (cache.n_pages, cache.n_kv_heads, 2, cache.head_dim)
     if bounds.shape != shape:
         raise ValueError(f"bounds: {shape} is wanted, not {tuple(bounds.shape)}")
-    return _vector(bounds, cache.dtype, bounds.numel(), cache._dev, "bounds")
+    return _vector(bounds, cache.dtype, 0, cache._dev, "bounds")
 
 
 def page_bounds(cache: KvCache, bounds, cu_q, ctx_len, page_table, n_rows: int, device_error=None,
@@ -777,13 +815,16 @@ def select_pages(cache: KvCache, bounds, q, cu_q, ctx_len, page_table, n_select:
     pages = (T, cache.n_kv_heads, n_select)
     if out is None:
         out = _empty_on(pages, torch.int32, cache.device, stream)
+        to = out.data_ptr()
     elif out.shape != pages:
         raise ValueError(f"out: {pages} is wanted, not {tuple(out.shape)}")
-    args = _batch_args(cache, _rows(q, shape, cache.dtype, dev, "q"), _NONE, T, Hq, 0.0, cu_q,
-                       ctx_len, page_table, device_error)
-    ws = _workspace("moe_select_pages_workspace", cache, workspace, stream, args)
+    else:
+        to = _vector(out, torch.int32, 0, dev, "out")
+    args = _batch_args(cache, _rows(q, shape, cache.dtype, dev, "q"), _NONE, T, Hq, 0.0, cu_q, ctx_len,
+                       page_table, device_error)
+    ws = _scratch("moe_select_pages_workspace", cache, workspace, stream, page_table, shape)
     _call("moe_select_pages", dev, stream, cache._c, args, _bounds(cache, bounds), n_select, sink,
-          recent, _vector(out, torch.int32, out.numel(), dev, "out"), *ws[:2])
+          recent, to, *ws[:2])
     return out
 
 
@@ -798,7 +839,7 @@ def sparse_attention(cache: KvCache, q, cu_q, ctx_len, page_table, pages,
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     n = pages.shape[2]
-    ws = _workspace("moe_sparse_attention_workspace", cache, workspace, stream, args, n)
+    ws = _scratch("moe_sparse_attention_workspace", cache, workspace, stream, page_table, q.shape, n)
     _call("moe_sparse_attention", cache._dev, stream, cache._c, args,
           _vector(pages, torch.int32, pages.numel(), cache._dev, "pages"), n, *ws[:2])
     return out

@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
   __shared__ int s_sum[kWarps], s_seq, s_page;
   __shared__ uint4 s_lo[kWarps][kChunks], s_hi[kWarps][kChunks];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_launch();
   // the sequence that the page belongs to
   if (threadIdx.x == 0) s_seq = -1;
   int64_t below = 0;
@@ -137,10 +139,10 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
 // The order of two pages may hang on the last bit of their scores, so it is decided in two steps: fp32 scores
 // with a bound on their error tell which pages are certainly among the k best and which are certainly
 // not; what lies between is compared by scores in fp64 (exact but for bounds and queries that differ by more
-// than 2^30).  A score is the fp32 sum of terms t_i, each of a product that is rounded once and a Q that is:
-// with at most 15 additions one after the other, it is off by less than 18 * 2^-24 sum |t_i| < kError sum |t_i|.
-constexpr float kError = 2e-6f;
-constexpr int kPagesABlock = 64;     // of a block that scores
+// than 2^30).  A score is the fp32 sum of terms Q b: Q a sum over the heads of numbers of one sign, the terms
+// added in at most 10 steps one after the other, so it is off by less than (group + 12) 2^-24 times the sum of
+// the terms' sizes, and that is at most max_d |b_d| times sum_d |Q_d|.
+constexpr int kPagesATurn = 64;      // that a block scores at a time: two for each eight lanes
 constexpr int kMaxPages = 65536;     // of a sequence: a bit each in shared memory
 constexpr int kKeys = 8192;          // scores that are kept in shared memory
 constexpr int kBins = 1024;
@@ -149,126 +151,159 @@ constexpr int kFew = 64;             // pages compared in fp64 one against the o
 struct Select {
   Params p;
   const void *bounds;  // [n_pages][hkv][2][D]
-  float2 *score;       // [rows of this launch][hkv][width]: score, sum of the terms' sizes
+  float2 *score;       // [rows of this launch][hkv][width]: score, bound of the sum of its terms' sizes
   int32_t *out;        // [n_rows][hkv][n_select]
   int row0, rows, width, n_select, sink, recent;
+  float error;         // of a score, relative to the sizes' sum
 };
 
 __device__ __forceinline__ bool better(double a, int i, double b, int j) {
   return a > b || (a == b && i < j);
 }
 
-// Q- and Q+ of a row and key/value head, side by side as the bounds are: in fp64, where the sum of up to 64
-// values of 16 bits is exact but for values that differ by more than 2^40.
+// Q- and Q+ of a row and key/value head, side by side as the bounds are; in fp64 the sum of up to 64 values of
+// 16 bits is exact but for values that differ by more than 2^40.  Returns this thread's sum of sizes.
 template <typename T, int D, typename V>
-__device__ __forceinline__ void sum_heads(const Params &p, int row, int kvh, V *s_q) {
+__device__ __forceinline__ V sum_heads(const Params &p, int row, int kvh, V *s_q) {
   const T *q = static_cast<const T *>(p.q) + row * p.q_row +
                static_cast<int64_t>(kvh) * p.group * p.q_head;
+  V size = 0;
   for (int d = threadIdx.x; d < D; d += kBlock) {
-    double down = 0., up = 0.;
+    V down = 0, up = 0;
+#pragma unroll 8
     for (int h = 0; h < p.group; ++h) {
-      const double x = static_cast<float>(q[h * p.q_head + d]);
-      if (x < 0.) down += x; else up += x;  // (a NaN goes up)
+      const V x = static_cast<float>(q[h * p.q_head + d]);
+      if (x < 0) down += x; else up += x;  // (a NaN goes up)
     }
-    s_q[d] = static_cast<V>(down), s_q[D + d] = static_cast<V>(up);
+    s_q[d] = down, s_q[D + d] = up;
+    size += up - down;
   }
+  return size;
 }
 
-// Scores of kPagesABlock pages for R rows, one after the other; eight lanes take a page, so that what they
-// read is 128 bytes in a row, and three exchanges add their parts.  Rows of one sequence share its bounds.
+// Scores of `turns` times kPagesATurn pages for R rows.  Eight lanes take a page, so that what they read is
+// 128 bytes in a row and three exchanges add their parts.  Rows of one sequence share its bounds.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
+__global__ void __launch_bounds__(kBlock) score_kernel(const Select w, int turns) {
   constexpr int kParts = 2 * D / 64;  // 16-byte parts of a page's bounds that a lane takes
-  constexpr int kTurns = kPagesABlock / (kBlock / 8);
+  constexpr int kPages = kPagesATurn / (kBlock / 8);
   __shared__ __align__(16) float s_q[R][2 * D];
+  __shared__ float s_size[R];
   const Params &p = w.p;
+  pdl_wait();
   pdl_launch();
   const int first = w.row0 + blockIdx.x * R, kvh = blockIdx.y;
-  const int page0 = blockIdx.z * kPagesABlock + (threadIdx.x >> 3), part = threadIdx.x & 7;
+  const int begin = blockIdx.z * turns * kPagesATurn, part = threadIdx.x & 7;
   const int n = min(R, w.row0 + w.rows - first);
   Row row[R];
   int most = 0;
+  bool one = true;  // sequence
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     row[r] = {};
     if (r < n) row[r] = load_row(p, first + r, 1);
-    // pages between the first and the last that are selected anyway
+    // pages before those at the end that are selected anyway
     row[r].len = row[r].nq ? ((row[r].ctx - 1) >> p.page_shift) + 1 : 0;
     row[r].len = row[r].len > w.n_select ? row[r].len - w.recent : 0;
+    if (row[r].len > 0) one &= most == 0 || row[r].seq == row[0].seq;
     most = max(most, row[r].len);
   }
-  if (blockIdx.z * kPagesABlock >= most || blockIdx.z * kPagesABlock + kPagesABlock <= w.sink) return;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (row[r].len > 0) sum_heads<T, D>(p, first + r, kvh, s_q[r]);
+  if (begin >= most || begin + turns * kPagesATurn <= w.sink) return;
+  one &= row[0].len > 0;
+  if (threadIdx.x < R) s_size[threadIdx.x] = 0.f;
   __syncthreads();
-  const auto fetch = [&](int seq, int count, uint4 (&x)[kTurns][kParts], bool (&there)[kTurns]) {
-    int at[kTurns];
+
+  uint4 x[kPages][kParts];
+  float top[kPages];  // largest size of a bound; -1: no page
+  const auto fetch = [&](int seq, int count, int page0) {
+    int at[kPages];
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
+    for (int t = 0; t < kPages; ++t) {
       const int j = page0 + t * (kBlock / 8);
       at[t] = j < count ? p.table[seq * p.table_stride + j] : -1;
-      there[t] = static_cast<unsigned>(at[t]) < static_cast<unsigned>(p.n_pages);
-      if (!there[t] && j < count && j >= w.sink && part == 0 && p.err) atomicOr(p.err, kDevErrBadId);
+      top[t] = static_cast<unsigned>(at[t]) < static_cast<unsigned>(p.n_pages) ? 0.f : -1.f;
+      if (top[t] < 0.f && j < count && j >= w.sink && part == 0 && p.err)
+        atomicOr(p.err, kDevErrBadId);
     }
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
+    for (int t = 0; t < kPages; ++t) {
       const T *src = static_cast<const T *>(w.bounds) +
-                     (static_cast<int64_t>(there[t] ? at[t] : 0) * p.hkv + kvh) * 2 * D + 8 * part;
+                     (static_cast<int64_t>(top[t] < 0.f ? 0 : at[t]) * p.hkv + kvh) * 2 * D + 8 * part;
 #pragma unroll
       for (int e = 0; e < kParts; ++e) x[t][e] = load16(src + 64 * e);
     }
   };
-  uint4 x[kTurns][kParts];
-  bool there[kTurns];
-  int held = -1, held_count = 0;
+  const auto sizes = [&]() {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (row[r].len == 0) continue;
-    if (row[r].seq != held || row[r].len > held_count) {
-      held = row[r].seq, held_count = row[r].len;
+    for (int t = 0; t < kPages; ++t) {
+      uint32_t m = 0u;
 #pragma unroll
-      for (int z = r + 1; z < R; ++z)  // what the later rows of the sequence want too
-        if (row[z].seq == held) held_count = max(held_count, row[z].len);
-      fetch(held, held_count, x, there);
+      for (int e = 0; e < kParts; ++e)
+        m = max2<T>(max2<T>(m, x[t][e].x & 0x7fff7fffu),
+                    max2<T>(max2<T>(x[t][e].y & 0x7fff7fffu, x[t][e].z & 0x7fff7fffu),
+                            x[t][e].w & 0x7fff7fffu));
+      const float2 f = Half<T>::unpack(m);
+      float v = fmaxf(f.x, f.y);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if (top[t] >= 0.f) top[t] = v;
     }
-    float4 q[kParts][2];
+  };
+  int page0 = begin + (threadIdx.x >> 3);
+  if (one) fetch(row[0].seq, most, page0);
 #pragma unroll
-    for (int e = 0; e < kParts; ++e) {
-      const float4 *src = reinterpret_cast<const float4 *>(s_q[r] + 64 * e + 8 * part);
-      q[e][0] = src[0], q[e][1] = src[1];
+  for (int r = 0; r < R; ++r)
+    if (row[r].len > 0) {
+      float size = sum_heads<T, D>(p, first + r, kvh, s_q[r]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
+      if ((threadIdx.x & 31) == 0 && threadIdx.x < D) atomicAdd(&s_size[r], size);
     }
+  __syncthreads();
+  for (int turn = 0; turn < turns && begin + turn * kPagesATurn < most; ++turn) {
+    if (one) sizes();
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-      float s[kParts], a[kParts];
+    for (int r = 0; r < R; ++r) {
+      if (row[r].len == 0) continue;
+      if (!one) fetch(row[r].seq, row[r].len, page0), sizes();
+      float s[kPages];
 #pragma unroll
-      for (int e = 0; e < kParts; ++e) {  // sums of eight terms
-        const float2 b0 = Half<T>::unpack(x[t][e].x), b1 = Half<T>::unpack(x[t][e].y),
-                     b2 = Half<T>::unpack(x[t][e].z), b3 = Half<T>::unpack(x[t][e].w);
-        const float b[8] = {b0.x, b0.y, b1.x, b1.y, b2.x, b2.y, b3.x, b3.y};
-        const float y[8] = {q[e][0].x, q[e][0].y, q[e][0].z, q[e][0].w,
-                            q[e][1].x, q[e][1].y, q[e][1].z, q[e][1].w};
-        s[e] = a[e] = 0.f;
+      for (int t = 0; t < kPages; ++t) {
+        uint64_t sum[kParts];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[e] = fmaf(y[i], b[i], s[e]);
-          a[e] = fmaf(fabsf(y[i]), fabsf(b[i]), a[e]);
+        for (int e = 0; e < kParts; ++e) {
+          const float4 *q = reinterpret_cast<const float4 *>(s_q[r] + 64 * e + 8 * part);
+          const float4 a = q[0], b = q[1];
+          const auto both = [](uint32_t v) {
+            const float2 f = Half<T>::unpack(v);
+            return pair(f.x, f.y);
+          };
+          sum[e] = mul2(pair(a.x, a.y), both(x[t][e].x));
+          sum[e] = fma2(pair(a.z, a.w), both(x[t][e].y), sum[e]);
+          sum[e] = fma2(pair(b.x, b.y), both(x[t][e].z), sum[e]);
+          sum[e] = fma2(pair(b.z, b.w), both(x[t][e].w), sum[e]);
         }
+#pragma unroll
+        for (int o = kParts / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int e = 0; e < o; ++e) sum[e] = add2(sum[e], sum[e + o]);
+        const float2 f = unpair(sum[0]);
+        s[t] = f.x + f.y;
       }
 #pragma unroll
-      for (int o = kParts / 2; o > 0; o >>= 1)
+      for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < o; ++e) s[e] += s[e + o], a[e] += a[e + o];
+        for (int t = 0; t < kPages; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
-        a[0] += __shfl_xor_sync(0xffffffffu, a[0], o);
+      for (int t = 0; t < kPages; ++t) {
+        const int j = page0 + t * (kBlock / 8);
+        if (part == 0 && j < row[r].len)
+          w.score[(static_cast<int64_t>(blockIdx.x * R + r) * p.hkv + kvh) * w.width + j] =
+              top[t] >= 0.f ? make_float2(s[t], top[t] * s_size[r]) : make_float2(kNegInf, 0.f);
       }
-      const int j = page0 + t * (kBlock / 8);
-      if (part == 0 && j < row[r].len)
-        w.score[(static_cast<int64_t>(blockIdx.x * R + r) * p.hkv + kvh) * w.width + j] =
-            there[t] ? make_float2(s[0], a[0]) : make_float2(kNegInf, 0.f);
     }
+    page0 += kPagesATurn;
+    if (one && turn + 1 < turns) fetch(row[0].seq, most, page0);
   }
 }
 
@@ -328,6 +363,9 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
   const Params &p = w.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row_i = w.row0 + blockIdx.x, kvh = blockIdx.y;
+  // without scores, this is the call's first kernel (and otherwise the one before has waited for the batch)
+  if (w.width <= w.n_select) pdl_wait();
+  pdl_launch();
   if (row_i == 0 && kvh == 0)
     for (int i = threadIdx.x; i < p.n_seqs; i += kBlock) load_seq(p, i, true);
   const Row row = load_row(p, row_i, 1);
@@ -379,7 +417,7 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     lo = s_lo, hi = s_hi;
     size = s_size;
     if (!(size <= 3e38f)) size = -kNegInf;
-    const float error = 2.f * kError * size + 1e-40f;  // (products below fp32's range)
+    const float error = 2.f * w.error * size + 1e-40f;  // (products below fp32's range)
     int above = 0, inside = n;
     while (lo < hi && inside > 1) {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
@@ -530,7 +568,7 @@ static int plan_select(const Params &p, SelectPlan *plan) {
 }
 
 template <typename T, int D>
-static cudaError_t launch_select(Select &w, const SelectPlan &plan, cudaStream_t stream) {
+static cudaError_t launch_select(Select w, const SelectPlan &plan, cudaStream_t stream) {
   const Params &p = w.p;
   const int words = (p.table_width + 31) / 32;
   const int smem = 4 * (2 * words + kBins + std::min(p.table_width, kKeys));
@@ -539,30 +577,19 @@ static cudaError_t launch_select(Select &w, const SelectPlan &plan, cudaStream_t
   cudaError_t e = limit.set(reinterpret_cast<const void *>(pick),
                             4 * (2 * (kMaxPages / 32) + kBins + kKeys));
   if (e != cudaSuccess) return e;
-  const unsigned chunks = (p.table_width + kPagesABlock - 1) / kPagesABlock;
+  const unsigned turns = (p.table_width + kPagesATurn - 1) / kPagesATurn;
   for (w.row0 = 0; w.row0 < p.n_rows; w.row0 += plan.rows) {
     w.rows = std::min(plan.rows, p.n_rows - w.row0);
-    const bool scored = p.table_width > w.n_select;
-    // sequences of some rows share what is read
-    if (!scored)
-      ;  // every page of every row is selected
-    else if (p.n_rows >= 4 * static_cast<int64_t>(p.n_seqs))
-      score_kernel<T, D, 4><<<dim3((w.rows + 3) / 4, p.hkv, chunks), kBlock, 0, stream>>>(w);
-    else
-      score_kernel<T, D, 1><<<dim3(w.rows, p.hkv, chunks), kBlock, 0, stream>>>(w);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.rows, p.hkv);
-    cfg.blockDim = dim3(kBlock);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = scored ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, pick, w);
+    if (p.table_width > w.n_select) {  // (otherwise every page of every row is selected)
+      // sequences of some rows share what is read
+      if (p.n_rows >= 4 * static_cast<int64_t>(p.n_seqs))
+        e = launch_early(score_kernel<T, D, 4>, dim3((w.rows + 3) / 4, p.hkv, (turns + 3) / 4), kBlock,
+                         0, stream, w, 4);
+      else
+        e = launch_early(score_kernel<T, D, 1>, dim3(w.rows, p.hkv, turns), kBlock, 0, stream, w, 1);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_early(pick, dim3(w.rows, p.hkv), kBlock, smem, stream, w);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -582,20 +609,16 @@ extern "C" int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *a
   const int64_t pages = std::min<int64_t>(p.n_rows, (p.n_rows >> p.page_shift) + 2ll * p.n_seqs);
   const dim3 grid(static_cast<unsigned>(pages), p.hkv);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == MOE_DTYPE_BF16) {
-    auto *b = static_cast<__nv_bfloat16 *>(bounds);
-    if (cache->head_dim == 64)
-      attn::bounds_kernel<__nv_bfloat16, 64><<<grid, attn::kBlock, 0, st>>>(p, b);
-    else
-      attn::bounds_kernel<__nv_bfloat16, 128><<<grid, attn::kBlock, 0, st>>>(p, b);
-  } else {
-    auto *b = static_cast<__half *>(bounds);
-    if (cache->head_dim == 64)
-      attn::bounds_kernel<__half, 64><<<grid, attn::kBlock, 0, st>>>(p, b);
-    else
-      attn::bounds_kernel<__half, 128><<<grid, attn::kBlock, 0, st>>>(p, b);
-  }
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  using B = __nv_bfloat16;
+  using H = __half;
+  cudaError_t e;
+  if (cache->dtype == MOE_DTYPE_BF16)
+    e = attn::launch_early(cache->head_dim == 64 ? attn::bounds_kernel<B, 64> : attn::bounds_kernel<B, 128>,
+                           grid, attn::kBlock, 0, st, p, static_cast<B *>(bounds));
+  else
+    e = attn::launch_early(cache->head_dim == 64 ? attn::bounds_kernel<H, 64> : attn::bounds_kernel<H, 128>,
+                           grid, attn::kBlock, 0, st, p, static_cast<H *>(bounds));
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" int moe_select_pages_workspace(const moe_kv_cache *cache, const moe_attention *a,
@@ -635,6 +658,7 @@ extern "C" int moe_select_pages(const moe_kv_cache *cache, const moe_attention *
   w.n_select = n_select;
   w.sink = sink;
   w.recent = recent;
+  w.error = (w.p.group + 12) * 6e-8f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == MOE_DTYPE_BF16)

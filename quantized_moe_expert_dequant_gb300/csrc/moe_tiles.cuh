@@ -356,32 +356,6 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -507,6 +481,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     s_gone = 0;
     tc::bar_fence_init();
   }
+  if (MODE == kShared) pdl_wait();
   pdl_launch();
   const bool any = find_part<MODE>(w, 2 * w.tokens, s_warp, s_spot);
   if (w.share && threadIdx.x == 0) {
@@ -1070,6 +1045,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p, const Pref
                                                       const Share *share, int ctas) {
   __shared__ uint32_t s_head[kMaxCtas / 32], s_ends[kMaxCtas / 32];
   pdl_wait();
+  pdl_launch();
   const int s = blockIdx.x / p.hkv, kvh = blockIdx.x % p.hkv;
   const Seq q = load_seq(p, s, false);
   if (q.nq == 0) return;
@@ -1220,32 +1196,23 @@ static int launch(const moe_kv_cache *c, const Params &p, const Prefixes &g, con
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Prompt<D>::kSmem);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  kern<<<plan.grid, kPromptThreads, Prompt<D>::kSmem, stream>>>(w);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-  if (!plan.bytes) return MOE_OK;
+  const float *part = w.part;
+  const float2 *part_ml = w.part_ml;
+  const Share *share = w.share;
   // the joining blocks are set up while the kernel runs and wait for its end
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan.grid, D / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   if constexpr (MODE == kShared) {
+    e = launch_early(kern, dim3(plan.grid), kPromptThreads, Prompt<D>::kSmem, stream, w);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     const int rows = 128 / (D / 8);  // of a block at a time
-    cfg.gridDim = dim3(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + rows - 1) / rows));
-    cfg.blockDim = dim3(128);
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<T, D>, p, w.g, w.tokens,
-                           static_cast<const float *>(w.part),
-                           static_cast<const float2 *>(w.part_ml),
-                           static_cast<const Share *>(w.share), plan.grid);
+    const dim3 grid(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + rows - 1) / rows));
+    e = launch_early(combine_kernel<T, D>, grid, 128, 0, stream, p, w.g, w.tokens, part, part_ml, share,
+                     plan.grid);
   } else {
-    e = cudaLaunchKernelEx(&cfg, prompt_join_kernel<T, D>, p, w.tokens,
-                           static_cast<const float *>(w.part),
-                           static_cast<const float2 *>(w.part_ml),
-                           static_cast<const Share *>(w.share), plan.grid);
+    kern<<<plan.grid, kPromptThreads, Prompt<D>::kSmem, stream>>>(w);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (!plan.bytes) return MOE_OK;
+    e = launch_early(prompt_join_kernel<T, D>, dim3(plan.grid, D / 8), 256, 0, stream, p, w.tokens, part,
+                     part_ml, share, plan.grid);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

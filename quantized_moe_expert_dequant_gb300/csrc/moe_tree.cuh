@@ -141,50 +141,68 @@ __device__ __forceinline__ void load_tile(const Params &p, int len, const int (&
       atomicOr(p.err, kDevErrBadId);
 }
 
-// The same for listed pages: see[e] of the 16 positions are seen (the others are not read).
+// Listed pages.  Each warp copies every fourth run of 16 positions of a tile, so that a thread looks up one
+// or two pages a tile and steps through their positions (all threads looking up all pages of a tile: one
+// token's chunk of 512 rows over 100 pages of 16 108 us, so TODO).
 template <int TILE>
-__device__ __forceinline__ void load_listed(const Params &p, const int32_t *list, int seq, int limit,
-                                            int len, int tile, int (&pg)[TILE / 16],
-                                            int (&see)[TILE / 16]) {
+struct Listed {
+  static constexpr int kRuns = TILE / 64;  // of a warp
+  int at[kRuns];    // the next tile's entries of the list
+  int page[kRuns];  // the pages that they name
+  int see[kRuns];   // how many of the 16 positions are seen (the others are not read)
+};
+
+template <int TILE>
+__device__ __forceinline__ void load_entries(const Params &p, const int32_t *list, int len, int tile,
+                                             Listed<TILE> &l) {
 #pragma unroll
-  for (int e = 0; e < TILE / 16; ++e) {
-    const int pos = tile * TILE + 16 * e;
-    const int at = pos < len ? list[pos >> p.page_shift] : -1;
+  for (int e = 0; e < Listed<TILE>::kRuns; ++e) {
+    const int pos = tile * TILE + 16 * ((threadIdx.x >> 5) + 4 * e);
+    l.at[e] = pos < len ? list[pos >> p.page_shift] : -1;
+  }
+}
+
+template <int TILE>
+__device__ __forceinline__ void load_listed(const Params &p, int seq, int limit, int tile,
+                                            Listed<TILE> &l) {
+#pragma unroll
+  for (int e = 0; e < Listed<TILE>::kRuns; ++e) {
+    const int pos = tile * TILE + 16 * ((threadIdx.x >> 5) + 4 * e), at = l.at[e];
     const bool seen = at >= 0 && at <= (limit - 1) >> p.page_shift;
-    pg[e] = seen ? p.table[seq * p.table_stride + at] : -1;
+    l.page[e] = seen ? p.table[seq * p.table_stride + at] : -1;
     const int left = limit - (at << p.page_shift) - (pos & ((1 << p.page_shift) - 1));
-    see[e] = seen ? max(0, min(left, 16)) : 0;
+    l.see[e] = seen ? max(0, min(left, 16)) : 0;
   }
 }
 
 template <typename T, int D, int TILE>
-__device__ __forceinline__ void load_listed_tile(const Params &p, const int (&pg)[TILE / 16],
-                                                 const int (&see)[TILE / 16], int64_t head_off,
-                                                 int tile, uint32_t k_smem, uint32_t v_smem,
-                                                 int *s_see) {
-  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
-  const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+__device__ __forceinline__ void load_listed_tile(const Params &p, const Listed<TILE> &l,
+                                                 int64_t head_off, int tile, uint32_t k_smem,
+                                                 uint32_t v_smem, int *s_see) {
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+  const int c = threadIdx.x % kChunks, r0 = (threadIdx.x & 31) / kChunks, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 0; i < TILE / kStep; ++i) {
-    const int r = r0 + i * kStep, pos = tile * TILE + r;
-    const int page = pg[i * kStep / 16];
-    const bool valid = (r & 15) < see[i * kStep / 16] &&
-                       static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
-    const int64_t off = valid ? page * p.page_stride + head_off +
-                                    (pos & ((1 << p.page_shift) - 1)) * p.tok_stride + 8 * c
-                              : 0;
-    const uint32_t d = swizzled<D>(r, c);
-    cp_async16(k_smem + d, static_cast<const T *>(p.k) + off, valid);
-    cp_async16(v_smem + d, static_cast<const T *>(p.v) + off, valid);
-  }
+  for (int e = 0; e < Listed<TILE>::kRuns; ++e) {
+    const int run = warp + 4 * e, page = l.page[e];
+    const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+    const int see = there ? l.see[e] : 0;
+    const int in_page = (tile * TILE + 16 * run) & ((1 << p.page_shift) - 1);
+    const int64_t off = there ? page * p.page_stride + head_off + (in_page + r0) * p.tok_stride + 8 * c : 0;
+    const T *k = static_cast<const T *>(p.k) + off, *v = static_cast<const T *>(p.v) + off;
+    const int64_t step = there ? kStep * p.tok_stride : 0;
 #pragma unroll
-  for (int e = 0; e < TILE / 16; ++e)
-    if (threadIdx.x == e) {
-      const bool bad =
-          see[e] > 0 && static_cast<unsigned>(pg[e]) >= static_cast<unsigned>(p.n_pages);
-      if (bad && p.err) atomicOr(p.err, kDevErrBadId);
-      s_see[e] = bad ? 0 : see[e];
+    for (int i = 0; i < 16 / kStep; ++i) {
+      const int r = r0 + i * kStep;
+      const uint32_t d = swizzled<D>(16 * run + r, c);
+      cp_async16(k_smem + d, k, r < see);
+      cp_async16(v_smem + d, v, r < see);
+      k += step, v += step;
     }
+    if ((threadIdx.x & 31) == 0) {
+      s_see[run] = see;
+      if (!there && l.see[e] > 0 && p.err) atomicOr(p.err, kDevErrBadId);
+    }
+  }
 }
 
 // Sums v over the block (every thread gets the sum) and gives each thread the sum before it.
@@ -232,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       return load_seq(p, i, report);
   };
   if constexpr (SPARSE) {
+    pdl_wait();
+    if (CS > 0) pdl_launch();
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.n_seqs; i += kThreads) load_seq(p, i, true);
   }
@@ -299,12 +319,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     int64_t head_off;
     int left, seq, kvh, t, nt, len, stage, pg[kTile / 16];
     Item next;
-    int limit, table, see[kTile / 16];  // listed pages: pages is the list, of pages of sequence `table`
+    int limit, table;  // listed pages: pages is the list, of pages of sequence `table`
+    Listed<kTile> list;
+    bool ready;        // the next tile's entries have been read
   } ld;
   const auto look_up = [&]() {
-    if constexpr (SPARSE)
-      load_listed<kTile>(p, ld.pages, ld.table, ld.limit, ld.len, ld.t, ld.pg, ld.see);
-    else
+    if constexpr (SPARSE) {
+      if (!ld.ready) load_entries<kTile>(p, ld.pages, ld.len, ld.t, ld.list);
+      load_listed<kTile>(p, ld.table, ld.limit, ld.t, ld.list);
+      ld.ready = ld.t + 1 < ld.nt;
+      if (ld.ready) load_entries<kTile>(p, ld.pages, ld.len, ld.t + 1, ld.list);
+    } else
       load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
   };
   {
@@ -317,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     ld.stage = 0;
     if constexpr (SPARSE) {
       ld.pages = w.list + (static_cast<int64_t>(ld.seq) * p.hkv + ld.kvh) * w.n_list;
-      ld.limit = q.ctx, ld.table = q.seq;
+      ld.limit = q.ctx, ld.table = q.seq, ld.ready = false;
     } else {
       ld.pages = p.table + ld.seq * p.table_stride;
     }
@@ -349,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     if (ld.left > 0) {
       const uint32_t st = base + ld.stage * 2 * kTileBytes;
       if constexpr (SPARSE)
-        load_listed_tile<T, D, kTile>(p, ld.pg, ld.see, ld.head_off, ld.t, st, st + kTileBytes,
+        load_listed_tile<T, D, kTile>(p, ld.list, ld.head_off, ld.t, st, st + kTileBytes,
                                       s_see[ld.stage]);
       else
         load_tile<T, D, kTile>(p, ld.len, ld.pg, ld.head_off, ld.t, st, st + kTileBytes);
@@ -621,6 +646,7 @@ template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Work w) {
   const Params &p = w.p;
   pdl_wait();
+  pdl_launch();
   const Shared sh = w.shared[blockIdx.x];
   const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int R = r;
@@ -709,20 +735,16 @@ static cudaError_t launch_line(const Work &w, int grid, cudaStream_t stream) {
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
-  e = cudaGetLastError();
+  if (SPARSE) {
+    e = launch_early(kern, dim3(grid), kThreads, Tree<D>::kSmem, stream, w);
+  } else {
+    kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   // the joining blocks are set up while the kernel runs and wait for its end
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 16 * WR / (kThreads / 32));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, 16 * WR>, w);
+  return launch_early(join_kernel<T, D, 16 * WR>, dim3(grid, 16 * WR / (kThreads / 32)), kThreads, 0,
+                      stream, w);
 }
 
 // A cluster of CS CTAs takes each of `items` items.
@@ -737,12 +759,14 @@ static cudaError_t launch_cluster(const Work &w, int items, cudaStream_t stream)
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Tree<D>::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CS;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CS;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPARSE ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, w);
 }
 
