@@ -84,6 +84,53 @@ __device__ __forceinline__ Row load_row(const Params &p, int r, int n_list) {
   return row;
 }
 
+// Groups of sequences whose first pages are the same (moe_prefix_attention).
+struct Prefixes {
+  const int32_t *cu;   // [n_groups + 1] sequences of the groups
+  const int32_t *len;  // [n_groups] positions that a group shares
+  int n_groups;
+};
+
+// The positions that a group shares, whole pages only (the page that a prefix ends in is each sequence's
+// own); -1 when its description is out of range.
+__device__ __forceinline__ int prefix_of(const Params &p, const Prefixes &g, int i) {
+  const int a = g.cu[i], b = g.cu[i + 1], len = g.len[i];
+  // (beside a group whose end is before its beginning, the bounds mean nothing either)
+  const bool ok = a >= 0 && a <= b && b <= p.n_seqs && len >= 0 && (i == 0 || g.cu[i - 1] <= a) &&
+                  (i + 1 == g.n_groups || b <= g.cu[i + 2]) &&
+                  len <= (static_cast<int64_t>(p.table_width) << p.page_shift) && len <= kMaxLen;
+  return ok ? len >> p.page_shift << p.page_shift : -1;
+}
+
+// The group of a sequence and the positions that it shares: 0 without a group, and when the prefix is longer
+// than what the sequence has before its queries.
+__device__ __forceinline__ int shared_by(const Params &p, const Prefixes &g, int s, int ctx, int *group) {
+  int lo = 0, hi = g.n_groups;  // the last group that begins at s or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (g.cu[mid] <= s) lo = mid; else hi = mid;
+  }
+  *group = lo;
+  if (g.n_groups == 0 || s < g.cu[lo] || s >= g.cu[lo + 1]) return 0;
+  const int len = prefix_of(p, g, lo);
+  return len > 0 && len <= ctx ? len : 0;
+}
+
+// A group's rows over its prefix.
+__device__ __forceinline__ Seq load_group(const Params &p, const Prefixes &g, int i, bool report) {
+  Seq r = {};
+  const int len = prefix_of(p, g, i);
+  bool ok = len >= 0;
+  if (len > 0 && g.cu[i] < g.cu[i + 1]) {
+    r.row0 = p.cu[g.cu[i]];
+    const int64_t end = p.cu[g.cu[i + 1]];
+    ok = r.row0 >= 0 && end >= r.row0 && end <= p.n_rows;
+    if (ok) r.nq = static_cast<int>(end - r.row0), r.ctx = r.len = len;
+  }
+  if (!ok && report && p.err) atomicOr(p.err, kDevErrBadId);
+  return r;
+}
+
 __device__ __forceinline__ void pdl_launch() {  // the next kernel may be set up
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -319,6 +366,12 @@ struct SmemLimit {
 
 // Limit of the tiles' waits in cycles; 0: the usual one (moe_debug_attention_wait_cycles).
 inline std::atomic<int64_t> debug_wait_cycles{0};
+
+// moe_prefix_attention of few and short sequences, each by a cluster of CTAs (moe_prefix_cluster.cu): whether it
+// takes a batch, or an error; and the call.
+int takes_prefix_clusters(const moe_kv_cache *cache, const Params &p, bool *takes);
+int run_prefix_clusters(const moe_kv_cache *cache, const Params &p, const Prefixes &g,
+                        cudaStream_t stream);
 
 // Attention in tiles of 128 rows on the 5th-generation tensor cores: causal, or by p.mask
 // (moe_prompt.cu, moe_prompt_tree.cu).

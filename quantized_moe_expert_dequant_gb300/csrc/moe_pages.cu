@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
 // than 2^30).  A score is the fp32 sum of terms Q b: Q a sum over the heads of numbers of one sign, the terms
 // added in at most 10 steps one after the other, so it is off by less than (group + 12) 2^-24 times the sum of
 // the terms' sizes, and that is at most max_d |b_d| times sum_d |Q_d|.
-constexpr int kPagesATurn = 64;      // that a block scores at a time: two for each eight lanes
 constexpr int kMaxPages = 65536;     // of a sequence: a bit each in shared memory
 constexpr int kKeys = 8192;          // scores that are kept in shared memory
 constexpr int kBins = 1024;
@@ -181,61 +180,38 @@ __device__ __forceinline__ V sum_heads(const Params &p, int row, int kvh, V *s_q
   return size;
 }
 
-// Scores of `turns` times kPagesATurn pages for R rows.  Eight lanes take a page, so that what they read is
-// 128 bytes in a row and three exchanges add their parts.  Rows of one sequence share its bounds.
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kBlock) score_kernel(const Select w, int turns) {
-  constexpr int kParts = 2 * D / 64;  // 16-byte parts of a page's bounds that a lane takes
-  constexpr int kPages = kPagesATurn / (kBlock / 8);
-  __shared__ __align__(16) float s_q[R][2 * D];
-  __shared__ float s_size[R];
-  const Params &p = w.p;
-  pdl_wait();
-  pdl_launch();
-  const int first = w.row0 + blockIdx.x * R, kvh = blockIdx.y;
-  const int begin = blockIdx.z * turns * kPagesATurn, part = threadIdx.x & 7;
-  const int n = min(R, w.row0 + w.rows - first);
-  Row row[R];
-  int most = 0;
-  bool one = true;  // sequence
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    row[r] = {};
-    if (r < n) row[r] = load_row(p, first + r, 1);
-    // pages before those at the end that are selected anyway
-    row[r].len = row[r].nq ? ((row[r].ctx - 1) >> p.page_shift) + 1 : 0;
-    row[r].len = row[r].len > w.n_select ? row[r].len - w.recent : 0;
-    if (row[r].len > 0) one &= most == 0 || row[r].seq == row[0].seq;
-    most = max(most, row[r].len);
-  }
-  if (begin >= most || begin + turns * kPagesATurn <= w.sink) return;
-  one &= row[0].len > 0;
-  if (threadIdx.x < R) s_size[threadIdx.x] = 0.f;
-  __syncthreads();
+// The bounds of some pages in registers: eight lanes take a page, so that what they read is 128 bytes in a row
+// and three exchanges add their parts; a block holds 32 PAGES pages, first + 32 t + (thread / 8).
+template <typename T, int D, int PAGES>
+struct Block {
+  static constexpr int kParts = 2 * D / 64;  // 16-byte parts of a page's bounds that a lane takes
+  uint4 x[PAGES][kParts];
+  float top[PAGES];  // the largest size of a bound; -1: no page
 
-  uint4 x[kPages][kParts];
-  float top[kPages];  // largest size of a bound; -1: no page
-  const auto fetch = [&](int seq, int count, int page0) {
-    int at[kPages];
+  // Pages first .. count - 1 of a sequence; those outside the cache are reported.
+  __device__ __forceinline__ void fetch(const Select &w, int seq, int kvh, int first, int count) {
+    const Params &p = w.p;
+    const int part = threadIdx.x & 7;
+    int at[PAGES];
 #pragma unroll
-    for (int t = 0; t < kPages; ++t) {
-      const int j = page0 + t * (kBlock / 8);
+    for (int t = 0; t < PAGES; ++t) {
+      const int j = first + (threadIdx.x >> 3) + t * (kBlock / 8);
       at[t] = j < count ? p.table[seq * p.table_stride + j] : -1;
       top[t] = static_cast<unsigned>(at[t]) < static_cast<unsigned>(p.n_pages) ? 0.f : -1.f;
       if (top[t] < 0.f && j < count && j >= w.sink && part == 0 && p.err)
         atomicOr(p.err, kDevErrBadId);
     }
 #pragma unroll
-    for (int t = 0; t < kPages; ++t) {
+    for (int t = 0; t < PAGES; ++t) {
       const T *src = static_cast<const T *>(w.bounds) +
                      (static_cast<int64_t>(top[t] < 0.f ? 0 : at[t]) * p.hkv + kvh) * 2 * D + 8 * part;
 #pragma unroll
       for (int e = 0; e < kParts; ++e) x[t][e] = load16(src + 64 * e);
     }
-  };
-  const auto sizes = [&]() {
+  }
+  __device__ __forceinline__ void sizes() {
 #pragma unroll
-    for (int t = 0; t < kPages; ++t) {
+    for (int t = 0; t < PAGES; ++t) {
       uint32_t m = 0u;
 #pragma unroll
       for (int e = 0; e < kParts; ++e)
@@ -248,62 +224,110 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w, int turns
       for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
       if (top[t] >= 0.f) top[t] = v;
     }
-  };
-  int page0 = begin + (threadIdx.x >> 3);
-  if (one) fetch(row[0].seq, most, page0);
+  }
+  // Scores for the sums q; -infinity without a page.
+  __device__ __forceinline__ void score(const float *s_q, float (&s)[PAGES]) const {
+    const int part = threadIdx.x & 7;
+    const auto both = [](uint32_t v) {
+      const float2 f = Half<T>::unpack(v);
+      return pair(f.x, f.y);
+    };
+#pragma unroll
+    for (int t = 0; t < PAGES; ++t) {
+      uint64_t sum[kParts];
+#pragma unroll
+      for (int e = 0; e < kParts; ++e) {
+        const float4 *q = reinterpret_cast<const float4 *>(s_q + 64 * e + 8 * part);
+        const float4 a = q[0], b = q[1];
+        sum[e] = mul2(pair(a.x, a.y), both(x[t][e].x));
+        sum[e] = fma2(pair(a.z, a.w), both(x[t][e].y), sum[e]);
+        sum[e] = fma2(pair(b.x, b.y), both(x[t][e].z), sum[e]);
+        sum[e] = fma2(pair(b.z, b.w), both(x[t][e].w), sum[e]);
+      }
+#pragma unroll
+      for (int o = kParts / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < o; ++e) sum[e] = add2(sum[e], sum[e + o]);
+      const float2 f = unpair(sum[0]);
+      s[t] = f.x + f.y;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+      for (int t = 0; t < PAGES; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
+#pragma unroll
+    for (int t = 0; t < PAGES; ++t)
+      if (top[t] < 0.f) s[t] = kNegInf;
+  }
+};
+
+// The sum of sizes of a block's sum_heads, added to *s_size (0 before; its order does not matter: a bound).
+template <int D>
+__device__ __forceinline__ void add_size(float size, float *s_size) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
+  if ((threadIdx.x & 31) == 0 && threadIdx.x < D) atomicAdd(s_size, size);
+}
+
+// Pages between which a row's selection chooses: all but the last `recent`; 0 when it takes every page.
+__device__ __forceinline__ int scored(const Select &w, const Row &row) {
+  const int pages = row.nq ? ((row.ctx - 1) >> w.p.page_shift) + 1 : 0;
+  return pages > w.n_select ? pages - w.recent : 0;
+}
+
+// For chunks, whose rows share what is read: scores of kTurns * 64 pages for kSharing rows into w.score.
+constexpr int kSharing = 4, kTurns = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
+  constexpr int R = kSharing, P = 2, kPages = P * (kBlock / 8);
+  __shared__ __align__(16) float s_q[R][2 * D];
+  __shared__ float s_size[R];
+  const Params &p = w.p;
+  pdl_wait();
+  pdl_launch();
+  const int first = w.row0 + blockIdx.x * R, kvh = blockIdx.y;
+  const int begin = blockIdx.z * kTurns * kPages;
+  const int n = min(R, w.row0 + w.rows - first);
+  int seq[R], count[R], most = 0;
+  bool one = true;  // sequence
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    Row row = {};
+    if (r < n) row = load_row(p, first + r, 1);
+    seq[r] = row.seq, count[r] = scored(w, row);
+    if (count[r] > 0) one &= seq[r] == seq[0];
+    most = max(most, count[r]);
+  }
+  if (begin >= most || begin + kTurns * kPages <= w.sink) return;
+  one &= count[0] > 0;
+  if (threadIdx.x < R) s_size[threadIdx.x] = 0.f;
+  __syncthreads();
+  Block<T, D, P> b;
+  int at = begin;
+  if (one) b.fetch(w, seq[0], kvh, at, most);
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (row[r].len > 0) {
-      float size = sum_heads<T, D>(p, first + r, kvh, s_q[r]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
-      if ((threadIdx.x & 31) == 0 && threadIdx.x < D) atomicAdd(&s_size[r], size);
-    }
+    if (count[r] > 0) add_size<D>(sum_heads<T, D>(p, first + r, kvh, s_q[r]), &s_size[r]);
   __syncthreads();
-  for (int turn = 0; turn < turns && begin + turn * kPagesATurn < most; ++turn) {
-    if (one) sizes();
+  for (int turn = 0; turn < kTurns && at < most; ++turn) {
+    if (one) b.sizes();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (row[r].len == 0) continue;
-      if (!one) fetch(row[r].seq, row[r].len, page0), sizes();
-      float s[kPages];
+      if (count[r] == 0) continue;
+      if (!one) b.fetch(w, seq[r], kvh, at, count[r]), b.sizes();
+      float s[P];
+      b.score(s_q[r], s);
 #pragma unroll
-      for (int t = 0; t < kPages; ++t) {
-        uint64_t sum[kParts];
-#pragma unroll
-        for (int e = 0; e < kParts; ++e) {
-          const float4 *q = reinterpret_cast<const float4 *>(s_q[r] + 64 * e + 8 * part);
-          const float4 a = q[0], b = q[1];
-          const auto both = [](uint32_t v) {
-            const float2 f = Half<T>::unpack(v);
-            return pair(f.x, f.y);
-          };
-          sum[e] = mul2(pair(a.x, a.y), both(x[t][e].x));
-          sum[e] = fma2(pair(a.z, a.w), both(x[t][e].y), sum[e]);
-          sum[e] = fma2(pair(b.x, b.y), both(x[t][e].z), sum[e]);
-          sum[e] = fma2(pair(b.z, b.w), both(x[t][e].w), sum[e]);
-        }
-#pragma unroll
-        for (int o = kParts / 2; o > 0; o >>= 1)
-#pragma unroll
-          for (int e = 0; e < o; ++e) sum[e] = add2(sum[e], sum[e + o]);
-        const float2 f = unpair(sum[0]);
-        s[t] = f.x + f.y;
-      }
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1)
-#pragma unroll
-        for (int t = 0; t < kPages; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
-#pragma unroll
-      for (int t = 0; t < kPages; ++t) {
-        const int j = page0 + t * (kBlock / 8);
-        if (part == 0 && j < row[r].len)
+      for (int t = 0; t < P; ++t) {
+        const int j = at + (threadIdx.x >> 3) + t * (kBlock / 8);
+        if ((threadIdx.x & 7) == 0 && j < count[r])
           w.score[(static_cast<int64_t>(blockIdx.x * R + r) * p.hkv + kvh) * w.width + j] =
-              top[t] >= 0.f ? make_float2(s[t], top[t] * s_size[r]) : make_float2(kNegInf, 0.f);
+              make_float2(s[t], fmaxf(b.top[t], 0.f) * s_size[r]);
       }
     }
-    page0 += kPagesATurn;
-    if (one && turn + 1 < turns) fetch(row[0].seq, most, page0);
+    at += kPages;
+    if (one && turn + 1 < kTurns) b.fetch(w, seq[0], kvh, at, most);
   }
 }
 
@@ -352,77 +376,147 @@ __device__ __forceinline__ int block_below(int v, int *s_sum) {
   return base + x - v;
 }
 
-// One block a row and key/value head.
-template <typename T, int D>
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores to the shared memory of the cluster's first CTA, at this CTA's address.
+__device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "st.shared::cluster.u32 [a], %1;\n\t}" ::"r"(addr),
+      "r"(v)
+      : "memory");
+}
+
+// The pages of a row and key/value head.  CS = 0: one block, the scores are in w.score.  CS > 0: a cluster of
+// CS blocks scores the pages, and its first takes all scores in its shared memory and chooses.
+template <typename T, int D, int CS>
 __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
-  extern __shared__ uint32_t s_dyn[];
-  __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_at[kFew];
-  __shared__ uint32_t s_lo, s_hi;
-  __shared__ float s_size;
+  extern __shared__ __align__(16) uint32_t s_dyn[];
+  __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
+  __shared__ uint32_t s_range[3 * (CS ? CS : 1)];  // of each block's part: least and largest key, largest size
   __shared__ double s_q[2 * D], s_exact[kFew];
   const Params &p = w.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row_i = w.row0 + blockIdx.x, kvh = blockIdx.y;
-  // without scores, this is the call's first kernel (and otherwise the one before has waited for the batch)
-  if (w.width <= w.n_select) pdl_wait();
+  const int rank = CS > 1 ? blockIdx.x % CS : 0;
+  const int row_i = w.row0 + blockIdx.x / (CS ? CS : 1), kvh = blockIdx.y;
+  // behind score_kernel, which has waited for the batch, only the scores are waited for
+  const bool behind = CS == 0 && w.width > w.n_select;
+  if (!behind) pdl_wait();
   pdl_launch();
-  if (row_i == 0 && kvh == 0)
+  if (blockIdx.x == 0 && row_i == 0 && kvh == 0)
     for (int i = threadIdx.x; i < p.n_seqs; i += kBlock) load_seq(p, i, true);
   const Row row = load_row(p, row_i, 1);
   const int pages = row.nq ? ((row.ctx - 1) >> p.page_shift) + 1 : 0;
   int32_t *out = w.out + (static_cast<int64_t>(row_i) * p.hkv + kvh) * w.n_select;
   if (pages <= w.n_select) {
-    pdl_wait();
-    if (row.nq)
+    if (behind) pdl_wait();
+    if (row.nq && rank == 0)
       for (int i = threadIdx.x; i < w.n_select; i += kBlock) out[i] = i < pages ? i : -1;
     return;
   }
   const int words = (pages + 31) / 32, j0 = w.sink, j1 = pages - w.recent, n = j1 - j0;
   const int want = w.n_select - w.sink - w.recent;
+  // keys of 32 bits; where many scores are the same, the exact ones of 64 bits take their place
   uint32_t *s_sel = s_dyn, *s_mid = s_sel + words, *s_bins = s_mid + words, *s_keys = s_bins + kBins;
-  for (int i = threadIdx.x; i < words; i += kBlock) {
-    uint32_t m = 0;
-    for (int b = 0; b < 32; ++b) {
-      const int j = 32 * i + b;
-      if (j < pages && (j < j0 || j >= j1)) m |= 1u << b;
-    }
-    s_sel[i] = m, s_mid[i] = 0u;
-  }
-  if (threadIdx.x == 0) s_lo = ~0u, s_hi = 0u, s_size = 0.f, s_count = 0;
-  __syncthreads();
-  pdl_wait();
-  float2 *score = w.score + (static_cast<int64_t>(blockIdx.x) * p.hkv + kvh) * w.width;
-  const bool kept = n <= kKeys;
+  float2 *score = CS ? reinterpret_cast<float2 *>(s_keys) - j0
+                     : w.score + (static_cast<int64_t>(blockIdx.x) * p.hkv + kvh) * w.width;
+  const bool kept = CS > 0 || n <= kKeys;
   const auto key_at = [&](int i) { return kept ? s_keys[i] : key_of(score[j0 + i].x); };
-  if (want > 0) {
-    uint32_t lo = ~0u, hi = 0u;
-    float size = 0.f;
+  uint32_t lo = ~0u, hi = 0u;
+  float size = 0.f;
+  if constexpr (CS > 0) {
+    constexpr int P = 4, kPages = P * (kBlock / 8);
+    __shared__ __align__(16) float s_sums[2 * D];
+    __shared__ float s_size;
+    if (CS > 1) cluster_arrive();
+    if (threadIdx.x == 0) s_size = 0.f;
+    Block<T, D, P> b;
+    int at = j0 + rank * kPages;
+    if (at < j1 && want > 0) b.fetch(w, row.seq, kvh, at, j1);
+    __syncthreads();
+    add_size<D>(sum_heads<T, D>(p, row_i, kvh, s_sums), &s_size);
+    __syncthreads();
+    if (CS > 1) cluster_wait();  // the first block is there
+    for (; at < j1 && want > 0; at += CS * kPages) {
+      b.sizes();
+      float s[P];
+      b.score(s_sums, s);
+#pragma unroll
+      for (int t = 0; t < P; ++t) {
+        const int i = at - j0 + (threadIdx.x >> 3) + t * (kBlock / 8);
+        if ((threadIdx.x & 7) != 0 || i >= n) continue;
+        const uint32_t key = key_of(s[t]);
+        lo = min(lo, key), hi = max(hi, key);
+        size = b.top[t] <= size ? size : b.top[t];  // (a NaN stays)
+        if (CS > 1)
+          store_first(smem_u32(s_keys + i), key);
+        else
+          s_keys[i] = key;
+      }
+      if (at + CS * kPages < j1) b.fetch(w, row.seq, kvh, at + CS * kPages, j1);
+    }
+    size *= s_size;
+  }
+  if (rank == 0) {
+    for (int i = threadIdx.x; i < words; i += kBlock) {
+      // all 32 bits from bit 32 i on that are before j0 or from j1 to the end
+      uint32_t m = 0;
+      const int from = 32 * i;
+      if (from < j0) m |= j0 - from >= 32 ? ~0u : (1u << (j0 - from)) - 1;
+      if (from + 32 > j1) m |= from >= j1 ? ~0u : ~0u << (j1 - from);
+      if (from + 32 > pages) m &= (1u << (pages - from)) - 1;
+      s_sel[i] = m, s_mid[i] = 0u;
+    }
+    for (int i = threadIdx.x; i < kBins; i += kBlock) s_bins[i] = 0u;
+    if (threadIdx.x == 0) s_count = s_in = s_mid_count = 0;
+  }
+  if (behind) pdl_wait();
+  if (CS == 0 && want > 0) {
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kBlock) {
       const float2 s = score[j0 + i];
       const uint32_t key = key_of(s.x);
       if (kept) s_keys[i] = key;
       lo = min(lo, key), hi = max(hi, key);
-      size = s.y <= size ? size : s.y;  // (a NaN stays)
+      size = s.y <= size ? size : s.y;
     }
-    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
-    // sizes are positive or NaN: their order is that of their bits
-    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
-    if (lane == 0) {
-      atomicMin(&s_lo, lo), atomicMax(&s_hi, hi);
-      atomicMax(reinterpret_cast<uint32_t *>(&s_size), most);
+  }
+  // sizes are positive or NaN: their order is that of their bits
+  lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+  __shared__ uint32_t s_part[3][kWarps];
+  if (lane == 0) s_part[0][warp] = lo, s_part[1][warp] = hi, s_part[2][warp] = most;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v)
+    lo = min(lo, s_part[0][v]), hi = max(hi, s_part[1][v]), most = max(most, s_part[2][v]);
+  if constexpr (CS > 1) {
+    if (threadIdx.x == 0) {
+      store_first(smem_u32(s_range + 3 * rank), lo);
+      store_first(smem_u32(s_range + 3 * rank + 1), hi);
+      store_first(smem_u32(s_range + 3 * rank + 2), most);
     }
-    __syncthreads();
-    // [lo, hi]: keys among which the want-th largest is; `above` keys are larger than those
-    lo = s_lo, hi = s_hi;
-    size = s_size;
+    cluster_arrive();
+    cluster_wait();
+    if (rank > 0) return;
+#pragma unroll
+    for (int v = 0; v < CS; ++v)
+      lo = min(lo, s_range[3 * v]), hi = max(hi, s_range[3 * v + 1]), most = max(most, s_range[3 * v + 2]);
+  }
+  if (want > 0) {
+    size = __uint_as_float(most);
     if (!(size <= 3e38f)) size = -kNegInf;
     const float error = 2.f * w.error * size + 1e-40f;  // (products below fp32's range)
+    // [lo, hi]: keys among which the want-th largest is; `above` keys are larger than those
     int above = 0, inside = n;
     while (lo < hi && inside > 1) {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
-      for (int i = threadIdx.x; i < kBins; i += kBlock) s_bins[i] = 0u;
-      __syncthreads();
       for (int i = threadIdx.x; i < n; i += kBlock) {
         const uint32_t key = key_at(i);
         if (lo <= key && key <= hi) atomicAdd(&s_bins[(key - lo) >> shift], 1u);
@@ -439,6 +533,7 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
         if (before < want && want <= before + static_cast<int>(c[e]))
           s_bin = kBins - 1 - 4 * threadIdx.x - e, s_above = before, s_in_bin = c[e];
         before += c[e];
+        s_bins[kBins - 1 - 4 * threadIdx.x - e] = 0u;
       }
       __syncthreads();
       const uint32_t from = lo + (static_cast<uint32_t>(s_bin) << shift);
@@ -446,28 +541,29 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
       hi = min(hi, from + ((1u << shift) - 1));
       above = s_above, inside = s_in_bin;
     }
-    // certainly in, and those that only fp64 can tell
+    // certainly in, and those that only fp64 can tell; a warp takes 32 pages, a word of the masks
     const float t_hi = score_of(hi) + error, t_lo = score_of(lo) - error;
     int in = 0, mid = 0;
-    const int whole = (n + 31) / 32 * 32;
-    for (int i = threadIdx.x; i < whole; i += kBlock) {
+    for (int i = warp; i < words; i += kWarps) {
+      const int j = 32 * i + lane;
       bool is_in = false, is_mid = false;
-      if (i < n) {
-        const float s = score_of(key_at(i));
+      if (j >= j0 && j < j1) {
+        const float s = score_of(key_at(j - j0));
         is_in = s > t_hi;
         is_mid = !is_in && !(s < t_lo);
       }
-      in += is_in, mid += is_mid;
-      const int j = j0 + i;
-      if (is_in) atomicOr(&s_sel[j >> 5], 1u << (j & 31));
+      const uint32_t m_in = __ballot_sync(0xffffffffu, is_in);
+      const uint32_t m_mid = __ballot_sync(0xffffffffu, is_mid);
+      in += __popc(m_in), mid += __popc(m_mid);
+      if (lane == 0) s_sel[i] |= m_in, s_mid[i] = m_mid;
       if (is_mid) {
-        atomicOr(&s_mid[j >> 5], 1u << (j & 31));
         const int at = atomicAdd(&s_count, 1);
         if (at < kFew) s_at[at] = j;
       }
     }
-    in = block_sum(in, s_sum);
-    mid = block_sum(mid, s_sum);
+    if (lane == 0) atomicAdd(&s_in, in), atomicAdd(&s_mid_count, mid);
+    __syncthreads();
+    in = s_in, mid = s_mid_count;
     const int need = want - in;  // of the mid ones: 1 .. mid
     if (need >= mid) {
       for (int i = threadIdx.x; i < words; i += kBlock) s_sel[i] |= s_mid[i];
@@ -528,7 +624,8 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
         const int i0 = min(words, static_cast<int>(threadIdx.x) * each), i1 = min(words, i0 + each);
         int mine = 0;
         for (int i = i0; i < i1; ++i)
-          for (uint32_t m = s_mid[i]; m; m &= m - 1) mine += !any || key[32 * i + __ffs(m) - 1] == last;
+          for (uint32_t m = s_mid[i]; m; m &= m - 1)
+            mine += !any || key[32 * i + __ffs(m) - 1] == last;
         int before = block_below(mine, s_sum);
         for (int i = i0; i < i1; ++i)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
@@ -537,8 +634,8 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
           }
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   // the pages in order
   int done = 0;
   for (int b = 0; b < words; b += kBlock) {
@@ -547,11 +644,12 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     int at = done + block_below(__popc(mine), s_sum);
     for (uint32_t m = mine; m; m &= m - 1, ++at)
       if (at < w.n_select) out[at] = 32 * i + __ffs(m) - 1;
-    done += block_sum(__popc(mine), s_sum);
+    if (b + kBlock < words) done += block_sum(__popc(mine), s_sum);
   }
 }
 
 struct SelectPlan {
+  int cluster;    // blocks that take a row and head; 0: scores go through the workspace
   int rows;       // of one launch
   int64_t bytes;
 };
@@ -561,35 +659,78 @@ constexpr int64_t kMostScores = 1ll << 28;
 
 static int plan_select(const Params &p, SelectPlan *plan) {
   if (p.table_width > kMaxPages || p.hkv > 65535) return MOE_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  plan->bytes = 0;
+  plan->rows = p.n_rows;
+  // Sequences of some rows share what is read; a token by itself is taken by one kernel, with as many blocks as
+  // there is room for.
+  if (p.n_rows < 4 * static_cast<int64_t>(p.n_seqs) && p.table_width <= kKeys) {
+    plan->cluster = 16;
+    while (plan->cluster > 1 && static_cast<int64_t>(p.n_rows) * p.hkv * plan->cluster > 2 * sms)
+      plan->cluster /= 2;
+    return MOE_OK;
+  }
+  plan->cluster = 0;
   const int64_t row = 8ll * p.hkv * p.table_width;
   plan->rows = static_cast<int>(std::min<int64_t>(p.n_rows, std::max<int64_t>(1, kMostScores / row)));
   plan->bytes = row * plan->rows;
   return MOE_OK;
 }
 
+template <typename T, int D, int CS>
+static cudaError_t launch_cluster(const Select &w, cudaStream_t stream) {
+  const auto pick = pick_kernel<T, D, CS>;
+  const auto smem = [](int pages) { return 4 * (2 * ((pages + 31) / 32) + kBins) + 8 * pages; };
+  static SmemLimit limit;
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(pick), smem(kKeys), CS > 8);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(w.rows * CS, w.p.hkv);
+  cfg.blockDim = dim3(kBlock);
+  cfg.dynamicSmemBytes = smem(w.width);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, pick, w);
+}
+
 template <typename T, int D>
 static cudaError_t launch_select(Select w, const SelectPlan &plan, cudaStream_t stream) {
   const Params &p = w.p;
-  const int words = (p.table_width + 31) / 32;
-  const int smem = 4 * (2 * words + kBins + std::min(p.table_width, kKeys));
-  const auto pick = pick_kernel<T, D>;
+  w.row0 = 0;
+  w.rows = p.n_rows;
+  switch (plan.cluster) {
+    case 16: return launch_cluster<T, D, 16>(w, stream);
+    case 8: return launch_cluster<T, D, 8>(w, stream);
+    case 4: return launch_cluster<T, D, 4>(w, stream);
+    case 2: return launch_cluster<T, D, 2>(w, stream);
+    case 1: return launch_cluster<T, D, 1>(w, stream);
+  }
+  const auto pick = pick_kernel<T, D, 0>;
+  const auto smem = [](int pages) {
+    return 4 * (2 * ((pages + 31) / 32) + kBins + std::min(pages, kKeys));
+  };
   static SmemLimit limit;
-  cudaError_t e = limit.set(reinterpret_cast<const void *>(pick),
-                            4 * (2 * (kMaxPages / 32) + kBins + kKeys));
+  cudaError_t e = limit.set(reinterpret_cast<const void *>(pick), smem(kMaxPages));
   if (e != cudaSuccess) return e;
-  const unsigned turns = (p.table_width + kPagesATurn - 1) / kPagesATurn;
-  for (w.row0 = 0; w.row0 < p.n_rows; w.row0 += plan.rows) {
+  constexpr int kPages = kTurns * 64;
+  for (; w.row0 < p.n_rows; w.row0 += plan.rows) {
     w.rows = std::min(plan.rows, p.n_rows - w.row0);
     if (p.table_width > w.n_select) {  // (otherwise every page of every row is selected)
-      // sequences of some rows share what is read
-      if (p.n_rows >= 4 * static_cast<int64_t>(p.n_seqs))
-        e = launch_early(score_kernel<T, D, 4>, dim3((w.rows + 3) / 4, p.hkv, (turns + 3) / 4), kBlock,
-                         0, stream, w, 4);
-      else
-        e = launch_early(score_kernel<T, D, 1>, dim3(w.rows, p.hkv, turns), kBlock, 0, stream, w, 1);
+      const dim3 grid((w.rows + kSharing - 1) / kSharing, p.hkv, (p.table_width + kPages - 1) / kPages);
+      e = launch_early(score_kernel<T, D>, grid, kBlock, 0, stream, w);
       if (e != cudaSuccess) return e;
     }
-    e = launch_early(pick, dim3(w.rows, p.hkv), kBlock, smem, stream, w);
+    e = launch_early(pick, dim3(w.rows, p.hkv), kBlock, smem(w.width), stream, w);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -650,7 +791,7 @@ extern "C" int moe_select_pages(const moe_kv_cache *cache, const moe_attention *
   attn::SelectPlan plan;
   rc = attn::plan_select(w.p, &plan);
   if (rc != MOE_OK) return rc;
-  if (!workspace || workspace_bytes < plan.bytes) return MOE_ERR_INVALID_ARG;
+  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MOE_ERR_INVALID_ARG;
   w.bounds = bounds;
   w.score = static_cast<float2 *>(workspace);
   w.out = pages;

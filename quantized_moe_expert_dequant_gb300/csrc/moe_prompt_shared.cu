@@ -31,8 +31,11 @@ extern "C" int moe_prefix_attention_workspace(const moe_kv_cache *cache, const m
   if (!bytes) return MOE_ERR_INVALID_ARG;
   *bytes = 0;
   if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
+  bool clusters;
+  int err = attn::takes_prefix_clusters(cache, p, &clusters);
+  if (err != MOE_OK || clusters) return err;
   attn::PromptPlan plan;
-  const int err = attn::make_plan(cache, p, &plan, n_groups);
+  err = attn::make_plan(cache, p, &plan, n_groups);
   if (err == MOE_OK) *bytes = plan.bytes;
   return err;
 }
@@ -50,13 +53,14 @@ extern "C" int moe_prefix_attention(const moe_kv_cache *cache, const moe_attenti
   if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
   if (n_groups > 0 && (!cu_group || !prefix_len)) return MOE_ERR_INVALID_ARG;
   p.mask = tree_mask;
-  attn::PromptPlan plan;
-  const int err = attn::make_plan(cache, p, &plan, n_groups);
+  const attn::Prefixes g = {cu_group, prefix_len, n_groups};
+  bool clusters;
+  int err = attn::takes_prefix_clusters(cache, p, &clusters);
   if (err != MOE_OK) return err;
-  attn::Prefixes g = {};
-  g.cu = cu_group;
-  g.len = prefix_len;
-  g.n_groups = n_groups;
+  if (clusters) return attn::run_prefix_clusters(cache, p, g, static_cast<cudaStream_t>(stream));
+  attn::PromptPlan plan;
+  err = attn::make_plan(cache, p, &plan, n_groups);
+  if (err != MOE_OK) return err;
   return attn::run_planned<attn::kShared>(cache, p, g, plan, workspace, workspace_bytes,
                                           static_cast<cudaStream_t>(stream));
 }

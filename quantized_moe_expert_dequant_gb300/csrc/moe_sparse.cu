@@ -16,8 +16,8 @@ template <typename T, int D>
 static cudaError_t launch_rows(const Work &w, const Plan &plan, cudaStream_t stream) {
   if (plan.cluster)
     return launch_listed_clusters<T, D>(w, plan.rows, plan.cluster, stream);
-  return plan.rows == 16 ? launch_line<T, D, 1, true>(w, plan.grid, stream)
-                         : launch_line<T, D, 2, true>(w, plan.grid, stream);
+  return plan.rows == 16 ? launch_line<T, D, 1, kListed>(w, plan.grid, stream)
+                         : launch_line<T, D, 2, kListed>(w, plan.grid, stream);
 }
 
 static int check_sparse(const moe_kv_cache *cache, const moe_attention *a, int n_select, Params *p) {
@@ -60,6 +60,7 @@ extern "C" int moe_sparse_attention(const moe_kv_cache *cache, const moe_attenti
   attn::use_workspace(plan, workspace, &w);
   w.list = pages;
   w.n_list = n_select;
+  w.g = {};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == MOE_DTYPE_BF16)

@@ -60,15 +60,16 @@ struct Prompt {
 // kShared: sequences whose first pages are the same (moe_prefix_attention).  The rows of all sequences of a
 // group are one tall sequence over the shared positions, read once for all; each sequence's other
 // positions are items of their own, and combine_kernel joins the two.
+//
+// An item of a sequence's own positions has few rows, one tile.  Two such items in a row are taken together, one
+// a tile, each with its own K and V: a tile by itself waits for its softmax between its products, and an item
+// for the end of the one before.
 enum Mode { kCausal, kTree, kShared };
 
-struct Prefixes {
-  const int32_t *cu;   // [n_groups + 1] sequences of the groups
-  const int32_t *len;  // [n_groups] positions that a group shares
-  int n_groups;
-  // what whole items leave, for the prefix and for the rest: rows' outputs [2][n_rows][hq][D], their (maximum,
-  // sum) [2][n_rows][hq], and where a row's parts begin, [2][n_rows][hkv]: kInRows, or the CTA in which its item
-  // begins
+// What whole items leave, for the prefix and for the rest: rows' outputs [2][n_rows][hq][D], their (maximum,
+// sum) [2][n_rows][hq], and where a row's parts begin, [2][n_rows][hkv]: kInRows, or the CTA in which its item
+// begins.
+struct RowParts {
   float *out;
   float2 *ml;
   int32_t *begin;
@@ -78,6 +79,7 @@ constexpr int kInRows = -1;
 struct PromptParams {
   Params p;
   Prefixes g;
+  RowParts rows;
   CUtensorMap q, k, v;
   int tokens;        // of a tile: 128 / group
   float *part;       // [2 G][2][D / 4][128][4]: parts of outputs, four columns of a tile's rows together
@@ -108,46 +110,6 @@ constexpr int kShareSteps = 9;
 struct Part : Seq {
   int seq, page0, rest;  // rest: 0 for a group's prefix
 };
-
-// The positions that a group shares, whole pages only (the page that a prefix ends in is each sequence's
-// own); -1 when its description is out of range.
-__device__ __forceinline__ int prefix_of(const Params &p, const Prefixes &g, int i) {
-  const int a = g.cu[i], b = g.cu[i + 1], len = g.len[i];
-  // (beside a group whose end is before its beginning, the bounds mean nothing either)
-  const bool ok = a >= 0 && a <= b && b <= p.n_seqs && len >= 0 && (i == 0 || g.cu[i - 1] <= a) &&
-                  (i + 1 == g.n_groups || b <= g.cu[i + 2]) &&
-                  len <= (static_cast<int64_t>(p.table_width) << p.page_shift) && len <= kMaxLen;
-  return ok ? len >> p.page_shift << p.page_shift : -1;
-}
-
-// The group of a sequence and the positions that it shares: 0 without a group, and when the prefix is longer
-// than what the sequence has before its queries.
-__device__ __forceinline__ int shared_by(const Params &p, const Prefixes &g, int s, int ctx, int *group) {
-  int lo = 0, hi = g.n_groups;  // the last group that begins at s or before
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (g.cu[mid] <= s) lo = mid; else hi = mid;
-  }
-  *group = lo;
-  if (g.n_groups == 0 || s < g.cu[lo] || s >= g.cu[lo + 1]) return 0;
-  const int len = prefix_of(p, g, lo);
-  return len > 0 && len <= ctx ? len : 0;
-}
-
-// A group's rows over its prefix.
-__device__ __forceinline__ Seq load_group(const Params &p, const Prefixes &g, int i, bool report) {
-  Seq r = {};
-  const int len = prefix_of(p, g, i);
-  bool ok = len >= 0;
-  if (len > 0 && g.cu[i] < g.cu[i + 1]) {
-    r.row0 = p.cu[g.cu[i]];
-    const int64_t end = p.cu[g.cu[i + 1]];
-    ok = r.row0 >= 0 && end >= r.row0 && end <= p.n_rows;
-    if (ok) r.nq = static_cast<int>(end - r.row0), r.ctx = r.len = len;
-  }
-  if (!ok && report && p.err) atomicOr(p.err, kDevErrBadId);
-  return r;
-}
 
 template <int MODE>
 __device__ __forceinline__ int part_count(const PromptParams &w) {
@@ -305,7 +267,7 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_
 // An item as the warps work on it: the sequence, its first token here, the steps from `a` on that are
 // this CTA's, and how many of them each tile has.  more = 0: the CTA's part of the line is done.
 struct alignas(16) Item {
-  int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, page0, rest, pad;
+  int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, page0, rest, pair;
 };
 static_assert(sizeof(Item) == 64, "read as four 16-byte words");
 
@@ -451,7 +413,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t s_q[2], s_q_free[2], s_full[C::kStages], s_empty[C::kStages],
       s_s[2], s_x[2], s_p[2], s_o[2], s_end, s_item_full[kItems], s_item_free[kItems];
-  __shared__ Item s_item[kItems];
+  __shared__ Item s_item[kItems], s_other[MODE == kShared ? kItems : 1];  // (of a pair: tile 1's)
   __shared__ int64_t s_warp[kPromptThreads / 32];
   __shared__ Spot s_spot[2];
   __shared__ uint32_t s_tmem;
@@ -510,11 +472,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const auto p_col = [](int i) { return C::kBeside ? 2 * kPos + 2 * D + i * (kPos / 2) : i * kPos; };
 
   int taken = 0;  // items
-  const auto take = [&](Item &item) {  // a whole warp; false: no more, or a wait gave up
+  // a whole warp; false: no more, or a wait gave up; other: tile 1's item of a pair
+  const auto take = [&](Item &item, Item *other = nullptr) {
     const int at = taken % kItems;
     const bool ok = tc::bar_wait(bar(s_item_full[at]), (taken / kItems) & 1, &s_gone);
     if (!__all_sync(0xffffffffu, ok)) return false;
     item = s_item[at];
+    if (MODE == kShared && other && item.pair) *other = s_other[at];
     __syncwarp();
     if (lane == 0) tc::bar_arrive(bar(s_item_free[at]));
     ++taken;
@@ -526,9 +490,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // ---------------------------------------------------------------- items, ahead of the others
     if (lane == 0) {
       Walk<MODE> walk(w, s_spot);
+      Item ahead;  // kShared: the item that was not taken with the one before it
+      bool held = false;
       for (int it = 0;; ++it) {
-        const Item item = walk.next();
+        Item item = MODE == kShared && held ? ahead : walk.next();
+        held = false;
+        if (MODE == kShared && item.more && item.count[1] == 0) {
+          ahead = walk.next();
+          held = !(ahead.more && ahead.count[1] == 0);
+          item.pair = !held;
+        }
         if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone)) break;
+        if (MODE == kShared && item.pair) ahead.pair = 1, s_other[it % kItems] = ahead;
         s_item[it % kItems] = item;
         tc::bar_arrive(bar(s_item_full[it % kItems]));
         if (!item.more) break;
@@ -549,8 +522,71 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return tc::bar_wait(b, parity, &s_gone, w.limit) && !*static_cast<volatile int *>(&s_gone);
     };
     bool ok = true;
-    Item item;
-    while (ok && take(item)) {
+    Item item, other;
+    // one tile of K or V (kv = 1); pg: the lane's page
+    const auto copy_kv = [&](const Item &x, int t, int kv, int pg) {
+      const int st = issued % C::kStages, pos = t * kPos + b_row;
+      ok = ok && free(bar(s_empty[st]), ((issued / C::kStages) & 1) ^ 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) tc::bar_expect(bar(s_full[st]), C::kTileBytes);
+      __syncwarp();
+      if (lane < boxes)
+        tc::copy_4d(ring + st * C::kTileBytes + half * kPos * 128 + b_row * 128, kv ? &w.v : &w.k,
+                    64 * half, pos & ((1 << p.page_shift) - 1), x.kvh, pg, bar(s_full[st]));
+      ++issued;
+    };
+    while (ok && take(item, &other)) {
+      if (MODE == kShared && item.pair) {
+        const auto page_of = [&](const Item &x, int t) {
+          const int pos = (x.a + t) * kPos + b_row;
+          if (lane >= boxes || t >= x.count[0] || pos >= x.len) return p.n_pages;
+          return p.table[x.seq * p.table_stride + x.page0 + (pos >> p.page_shift)];
+        };
+        const auto checked = [&](const Item &x, int t, int pg) {  // outside the cache: reads zeros
+          if (static_cast<unsigned>(pg) < static_cast<unsigned>(p.n_pages)) return pg;
+          if (lane < boxes && (x.a + t) * kPos + b_row < x.len && p.err) atomicOr(p.err, kDevErrBadId);
+          return p.n_pages;
+        };
+        int page[2], next[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Item &x = i ? other : item;
+          page[i] = page_of(x, 0), next[i] = page_of(x, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Item &x = i ? other : item;
+          page[i] = checked(x, 0, page[i]);
+          copy_kv(x, x.a, 0, page[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Item &x = i ? other : item;
+          ok = ok && free(bar(s_q_free[i]), (q_loads[i] & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) {
+            tc::bar_expect(bar(s_q[i]), static_cast<uint32_t>(w.tokens * p.group * D * 2));
+            for (int h = 0; h < D / 64; ++h)
+              tc::copy_3d(base + i * C::kTileBytes + h * kPos * 128, &w.q, 64 * h, x.kvh * p.group,
+                          x.row0 + x.tok0, bar(s_q[i]));
+          }
+          if (ok) ++q_loads[i];
+        }
+        const int last = max(item.count[0], other.count[0]);
+        for (int t = 0; ok && t < last; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const Item &x = i ? other : item;
+            if (t >= x.count[0]) continue;
+            copy_kv(x, x.a + t, 1, page[i]);
+            if (t + 1 >= x.count[0]) continue;
+            page[i] = checked(x, t + 1, next[i]);
+            next[i] = page_of(x, t + 2);
+            copy_kv(x, x.a + t + 1, 0, page[i]);
+          }
+        continue;
+      }
       const int32_t *pages = p.table + item.seq * p.table_stride + (MODE == kShared ? item.page0 : 0);
       const auto page_of = [&](int t) {
         const int pos = t * kPos + b_row;
@@ -630,9 +666,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     int n_q[2] = {0, 0}, n_p[2] = {0, 0};  // tiles of Q, steps so far
     int k_before = 0, v_before = -1;       // stages to give back: this step's K, the last one's V
     bool gone = false;
-    Item item;
-    while (!gone && take(item)) {
-      const int u[2] = {uniform(item.count[0]), uniform(item.count[1])}, last = uniform(item.steps);
+    Item item, other;
+    while (!gone && take(item, &other)) {
+      const bool pair = MODE == kShared && uniform(item.pair);
+      const int u[2] = {uniform(item.count[0]), uniform(pair ? other.count[0] : item.count[1])};
+      const int last = pair ? max(u[0], u[1]) : uniform(item.steps);
       const int valid = uniform(item.len - item.a * kPos);  // positions from the first step on
       const auto issue_s = [&](int i, int t, uint32_t k) {
         const uint32_t k_lo = tc::desc_lo(k, 16);
@@ -645,6 +683,72 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc::mma_commit(one, bar(s_s[i]));
         if (t == u[i] - 1) tc::mma_commit(one, bar(s_q_free[i]));
       };
+      // positions behind the sequence have weight 0, but what their page holds may be NaN
+      const auto clear_behind = [&](uint32_t v, int left) {
+        if (left >= kPos) return;
+        for (int x = left * 128 + lane * 16; x < kPos * 128; x += 512)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * kPos * 128 + x), "r"(0)
+                         : "memory");
+        tc::fence_async_proxy();
+        __syncwarp();
+      };
+      if (pair) {
+        const int left[2] = {valid, uniform(other.len - other.a * kPos)};
+        if (v_before >= 0) tc::mma_commit(one, bar(s_empty[v_before]));
+        v_before = -1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          wait(bar(s_full[st]), phase);
+          wait(bar(s_q[i]), n_q[i] & 1);
+          ++n_q[i];
+          if (C::kBeside && n_p[i] > 0) {  // the last item's S has been read
+            wait(bar(s_x[i]), (n_p[i] - 1) & 1);
+            tc::fence_after();
+          }
+          issue_s(i, 0, stage(st));
+          tc::mma_commit(one, bar(s_empty[st]));
+          turn();
+        }
+        for (int t = 0; t < last; ++t) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (t >= u[i]) continue;
+            const int v_st = st, v_phase = phase;
+            turn();
+            const int k_st = st, k_phase = phase;
+            const bool more = t + 1 < u[i];
+            if (more) turn();
+            const auto next_s = [&]() {
+              wait(bar(s_full[k_st]), k_phase);
+              if (C::kBeside) {
+                wait(bar(s_x[i]), n_p[i] & 1);
+                tc::fence_after();
+              }
+              issue_s(i, t + 1, stage(k_st));
+              tc::mma_commit(one, bar(s_empty[k_st]));
+            };
+            if (C::kBeside && more) next_s();
+            wait(bar(s_full[v_st]), v_phase);
+            clear_behind(stage(v_st), left[i] - t * kPos);
+            const uint32_t v_lo = tc::desc_lo(stage(v_st), kPos * 128);
+            wait(bar(s_p[i]), n_p[i] & 1);
+            tc::fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kPos / 16; ++kk)
+              tc::mma_tmem(one, tm + 2 * kPos + i * D, tm + p_col(i) + kk * 8, v_lo + kk * 128, hi, i_o,
+                           t > 0 || kk > 0);
+            if (C::kBeside || !more) tc::mma_commit(one, bar(s_o[i]));
+            tc::mma_commit(one, bar(s_empty[v_st]));
+            if (!C::kBeside && more) next_s();
+            ++n_p[i];
+          }
+          gone = __any_sync(0xffffffffu, *static_cast<volatile int *>(&s_gone));
+          if (gone) break;
+        }
+        continue;
+      }
       wait(bar(s_full[st]), phase);
       k_before = st;
 #pragma unroll
@@ -745,11 +849,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     int n_s = 0, n_o = 0;  // steps, commits of O so far
     bool ok = true;
     Item item;
-    while (ok && take(item)) {
-      const int n = i ? item.count[1] : item.count[0], tok_first = item.tok0 + i * w.tokens;
+    while (ok && take(item, i ? &item : nullptr)) {
+      const int j = MODE == kShared && item.pair ? 0 : i;  // the item's tile that is in tile i
+      const int n = j ? item.count[1] : item.count[0], tok_first = item.tok0 + j * w.tokens;
       if (n == 0) {
         if (!item.whole && tok_first < item.nq)  // a piece in which this tile has no part
-          w.part_ml[(2 * static_cast<int64_t>(blockIdx.x) + (item.a > 0 ? 0 : 1)) * 256 + i * 128 +
+          w.part_ml[(2 * static_cast<int64_t>(blockIdx.x) + (item.a > 0 ? 0 : 1)) * 256 + j * 128 +
                     r] = make_float2(kNegInf, 0.f);
         continue;
       }
@@ -877,11 +982,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (MODE == kShared && r < rows && item.a == 0) {
         const int64_t row = static_cast<int64_t>(item.rest) * p.n_rows + item.row0 + tok;
         const int head = r - r_tok * p.group;
-        if (head == 0) w.g.begin[row * p.hkv + item.kvh] = item.whole ? kInRows : blockIdx.x;
-        if (item.whole) w.g.ml[row * p.hq + item.kvh * p.group + head] = make_float2(m, l);
+        if (head == 0) w.rows.begin[row * p.hkv + item.kvh] = item.whole ? kInRows : blockIdx.x;
+        if (item.whole) w.rows.ml[row * p.hq + item.kvh * p.group + head] = make_float2(m, l);
       }
       if (MODE == kShared && item.whole) {
-        float4 *dst = reinterpret_cast<float4 *>(w.g.out) +
+        float4 *dst = reinterpret_cast<float4 *>(w.rows.out) +
                       ((static_cast<int64_t>(item.rest) * p.n_rows + item.row0 + tok) * p.hq +
                        item.kvh * p.group + r - r_tok * p.group) * (D / 4);
 #pragma unroll 1
@@ -898,7 +1003,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                               __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
         }
       } else if (!item.whole) {
-        float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + i) * (D / 4) * 128 + r;
+        float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + j) * (D / 4) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -959,7 +1064,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                   make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
         }
       }
-      if (!item.whole && r < rows) w.part_ml[slot * 256 + i * 128 + r] = make_float2(m, l);
+      if (!item.whole && r < rows) w.part_ml[slot * 256 + j * 128 + r] = make_float2(m, l);
     }
   }
   tc::fence_before();
@@ -1040,7 +1145,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int to
 // kShared: joins what the items over the prefix and over the rest have left of a sequence's rows, one block a
 // sequence and key/value head, eight columns of a row a thread; parts are added in the order of the positions.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const Params p, const Prefixes g, int tokens,
+__global__ void __launch_bounds__(128) combine_kernel(const Params p, const Prefixes g, const RowParts rows,
+                                                      int tokens,
                                                       const float *part, const float2 *part_ml,
                                                       const Share *share, int ctas) {
   __shared__ uint32_t s_head[kMaxCtas / 32], s_ends[kMaxCtas / 32];
@@ -1078,10 +1184,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p, const Pref
       for (int k = 0; k < 2; ++k) {
         if (k == 0 && !first) continue;
         const int64_t at = k * static_cast<int64_t>(p.n_rows) + row;
-        const int c = g.begin[at * p.hkv + kvh];
+        const int c = rows.begin[at * p.hkv + kvh];
         if (c == kInRows) {
           const int64_t i = at * p.hq + kvh * p.group + head;
-          f(g.ml + i, reinterpret_cast<const float4 *>(g.out) + i * (D / 4) + 2 * c8, 1);
+          f(rows.ml + i, reinterpret_cast<const float4 *>(rows.out) + i * (D / 4) + 2 * c8, 1);
           continue;
         }
         if (static_cast<unsigned>(c) >= static_cast<unsigned>(ctas)) continue;  // (a wait gave up)
@@ -1174,9 +1280,9 @@ static int launch(const moe_kv_cache *c, const Params &p, const Prefixes &g, con
   w.split = plan.split;
   w.g = g;
   if (MODE == kShared) {
-    w.g.out = reinterpret_cast<float *>(ws + plan.out);
-    w.g.ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
-    w.g.begin = reinterpret_cast<int32_t *>(ws + plan.begin);
+    w.rows.out = reinterpret_cast<float *>(ws + plan.out);
+    w.rows.ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
+    w.rows.begin = reinterpret_cast<int32_t *>(ws + plan.begin);
   }
   if (const int64_t cycles = debug_wait_cycles.load(std::memory_order_relaxed))
     w.limit.cycles = cycles, w.limit.nap_ns = 0;
@@ -1203,10 +1309,10 @@ static int launch(const moe_kv_cache *c, const Params &p, const Prefixes &g, con
   if constexpr (MODE == kShared) {
     e = launch_early(kern, dim3(plan.grid), kPromptThreads, Prompt<D>::kSmem, stream, w);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    const int rows = 128 / (D / 8);  // of a block at a time
-    const dim3 grid(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + rows - 1) / rows));
-    e = launch_early(combine_kernel<T, D>, grid, 128, 0, stream, p, w.g, w.tokens, part, part_ml, share,
-                     plan.grid);
+    const int at_once = 128 / (D / 8);  // rows of a block
+    const dim3 grid(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + at_once - 1) / at_once));
+    e = launch_early(combine_kernel<T, D>, grid, 128, 0, stream, p, w.g, w.rows, w.tokens, part,
+                     part_ml, share, plan.grid);
   } else {
     kern<<<plan.grid, kPromptThreads, Prompt<D>::kSmem, stream>>>(w);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;

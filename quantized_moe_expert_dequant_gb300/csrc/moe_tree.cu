@@ -17,8 +17,8 @@ static int plan_tree(const moe_kv_cache *c, const Params &p, Plan *plan) {
 
 template <typename T, int D>
 static cudaError_t launch_rows(const Work &w, const Plan &plan, cudaStream_t stream) {
-  if (plan.rows == 16) return launch_line<T, D, 1, false>(w, plan.grid, stream);
-  return launch_line<T, D, 2, false>(w, plan.grid, stream);
+  if (plan.rows == 16) return launch_line<T, D, 1, kSeqs>(w, plan.grid, stream);
+  return launch_line<T, D, 2, kSeqs>(w, plan.grid, stream);
 }
 
 }  // namespace attn
@@ -65,6 +65,7 @@ extern "C" int moe_tree_attention(const moe_kv_cache *cache, const moe_attention
   attn::use_workspace(plan, workspace, &w);
   w.list = nullptr;
   w.n_list = 0;
+  w.g = {};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (plan.cluster)

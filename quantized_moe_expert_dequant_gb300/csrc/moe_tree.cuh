@@ -65,9 +65,14 @@ struct Work {
   float *part;      // [2 G][ROWS][D] partial outputs: slot 2c the CTA's first item, 2c + 1 its last
   float2 *part_ml;  // [2 G][ROWS] (maximum, sum)
   Shared *shared;   // [G]
-  const int32_t *list;  // [n_rows][hkv][n_list] pages of each row, of its table; null: all of them
+  const int32_t *list;  // kListed: [n_rows][hkv][n_list] pages of each row, of its table
   int n_list;
+  Prefixes g;           // kGrouped
 };
+
+// What an item is: a sequence, a row and its list of pages (moe_sparse_attention), or a sequence whose first
+// pages are those of its group's first one (moe_prefix_attention).
+enum Items { kSeqs, kListed, kGrouped };
 
 // All threads of the cluster's CTAs.  The aligned form wants converged warps, and the code before it may have
 // split them (half a warp of a tile's rows, the last of a loop).
@@ -111,6 +116,17 @@ __device__ __forceinline__ void load_pages(const Params &p, const int32_t *pages
   for (int e = 0; e < TILE / 16; ++e) {
     const int pos = tile * TILE + 16 * e;
     pg[e] = pos < len ? pages[pos >> p.page_shift] : -1;
+  }
+}
+
+// The same where the first `shared` positions are on other pages than the sequence's own.
+template <int TILE>
+__device__ __forceinline__ void load_pages(const Params &p, const int32_t *first, int shared,
+                                           const int32_t *own, int len, int tile, int (&pg)[TILE / 16]) {
+#pragma unroll
+  for (int e = 0; e < TILE / 16; ++e) {
+    const int pos = tile * TILE + 16 * e;
+    pg[e] = pos < len ? (pos < shared ? first : own)[pos >> p.page_shift] : -1;
   }
 }
 
@@ -228,9 +244,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 }
 
 // CS > 0: a cluster of CS CTAs takes an item, each an even part of its tiles, and joins the parts in
-// distributed shared memory.  SPARSE: items are rows and their lists of pages (w.list).
-template <typename T, int D, int WR, int CS, bool SPARSE>
+// distributed shared memory.
+template <typename T, int D, int WR, int CS, int ITEMS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w) {
+  constexpr bool SPARSE = ITEMS == kListed;
+  static_assert(ITEMS != kGrouped || CS > 0, "one item a CTA");
   constexpr int kTile = Tree<D>::kTile;
   constexpr int ROWS = 16 * WR, WT = 4 / WR, TW = kTile / WT;  // TW positions of a warp per tile
   constexpr int kStages = Tree<D>::kStages, kTileBytes = Tree<D>::kTileBytes;
@@ -249,9 +267,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     else
       return load_seq(p, i, report);
   };
-  if constexpr (SPARSE) {
+  if constexpr (ITEMS != kSeqs) {
     pdl_wait();
     if (CS > 0) pdl_launch();
+  }
+  if constexpr (ITEMS == kGrouped) {
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < w.g.n_groups; i += kThreads) load_group(p, w.g, i, true);
+  }
+  if constexpr (SPARSE) {
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.n_seqs; i += kThreads) load_seq(p, i, true);
   }
@@ -322,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     int limit, table;  // listed pages: pages is the list, of pages of sequence `table`
     Listed<kTile> list;
     bool ready;        // the next tile's entries have been read
+    const int32_t *first;  // grouped: the pages of positions before `limit`
   } ld;
   const auto look_up = [&]() {
     if constexpr (SPARSE) {
@@ -329,8 +354,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       load_listed<kTile>(p, ld.table, ld.limit, ld.t, ld.list);
       ld.ready = ld.t + 1 < ld.nt;
       if (ld.ready) load_entries<kTile>(p, ld.pages, ld.len, ld.t + 1, ld.list);
-    } else
+    } else if constexpr (ITEMS == kGrouped) {
+      load_pages<kTile>(p, ld.first, ld.limit, ld.pages, ld.len, ld.t, ld.pg);
+    } else {
       load_pages<kTile>(p, ld.pages, ld.len, ld.t, ld.pg);
+    }
   };
   {
     const int64_t in_seq = at - s_before;
@@ -345,6 +373,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       ld.limit = q.ctx, ld.table = q.seq, ld.ready = false;
     } else {
       ld.pages = p.table + ld.seq * p.table_stride;
+    }
+    if constexpr (ITEMS == kGrouped) {
+      int group;
+      ld.limit = shared_by(p, w.g, ld.seq, q.ctx, &group);
+      ld.first = ld.limit ? p.table + w.g.cu[group] * p.table_stride : ld.pages;
     }
     ld.head_off = ld.kvh * p.head_stride;
     look_up();
@@ -729,13 +762,13 @@ inline void use_workspace(const Plan &plan, void *workspace, Work *w) {
 }
 
 // All CTAs share all items.
-template <typename T, int D, int WR, bool SPARSE>
+template <typename T, int D, int WR, int ITEMS>
 static cudaError_t launch_line(const Work &w, int grid, cudaStream_t stream) {
-  const auto kern = tree_kernel<T, D, WR, 0, SPARSE>;
+  const auto kern = tree_kernel<T, D, WR, 0, ITEMS>;
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem);
   if (e != cudaSuccess) return e;
-  if (SPARSE) {
+  if (ITEMS != kSeqs) {
     e = launch_early(kern, dim3(grid), kThreads, Tree<D>::kSmem, stream, w);
   } else {
     kern<<<grid, kThreads, Tree<D>::kSmem, stream>>>(w);
@@ -748,9 +781,9 @@ static cudaError_t launch_line(const Work &w, int grid, cudaStream_t stream) {
 }
 
 // A cluster of CS CTAs takes each of `items` items.
-template <typename T, int D, int WR, int CS, bool SPARSE>
+template <typename T, int D, int WR, int CS, int ITEMS>
 static cudaError_t launch_cluster(const Work &w, int items, cudaStream_t stream) {
-  const auto kern = tree_kernel<T, D, WR, CS, SPARSE>;
+  const auto kern = tree_kernel<T, D, WR, CS, ITEMS>;
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(kern), Tree<D>::kSmem, CS > 8);
   if (e != cudaSuccess) return e;
@@ -766,7 +799,7 @@ static cudaError_t launch_cluster(const Work &w, int items, cudaStream_t stream)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = SPARSE ? 2 : 1;
+  cfg.numAttrs = ITEMS != kSeqs ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, w);
 }
 

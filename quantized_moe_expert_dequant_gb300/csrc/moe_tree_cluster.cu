@@ -7,10 +7,10 @@ template <typename T, int D>
 static cudaError_t launch_rows(const Work &w, int rows, int cs, cudaStream_t stream) {
   const int items = w.p.n_seqs * w.p.hkv;
   if (rows == 16)
-    return cs == 8 ? launch_cluster<T, D, 1, 8, false>(w, items, stream)
-                   : launch_cluster<T, D, 1, 16, false>(w, items, stream);
-  return cs == 8 ? launch_cluster<T, D, 2, 8, false>(w, items, stream)
-                 : launch_cluster<T, D, 2, 16, false>(w, items, stream);
+    return cs == 8 ? launch_cluster<T, D, 1, 8, kSeqs>(w, items, stream)
+                   : launch_cluster<T, D, 1, 16, kSeqs>(w, items, stream);
+  return cs == 8 ? launch_cluster<T, D, 2, 8, kSeqs>(w, items, stream)
+                 : launch_cluster<T, D, 2, 16, kSeqs>(w, items, stream);
 }
 
 cudaError_t launch_clusters(const moe_kv_cache *c, const Work &w, int rows, int cs,

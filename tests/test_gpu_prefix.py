@@ -183,9 +183,25 @@ def test_streams_graphs_and_workspaces():
     C.assert_within(out[:sum(b.lens[:20])], ref[:sum(b.lens[:20])], tol[:sum(b.lens[:20])])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 1, 64), (4, 4, 64), (16, 1, 128)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_few_sequences_in_both_forms(dtype, Hq, Hkv, D, page):
+    """A narrow table goes to clusters, one that could hold long sequences to the tiles.  Sequences of one step
+    and of many, an odd number of them, with a group in between that has none."""
+    lens, after = [1, 2, 1, 1, 2, 1, 1], [0, 700, 1, 127, 128, 300, 40]
+    G = Groups(13 + D, [0, 2, 2, 6], [400, 99, 260], lens, after, Hq, Hkv, D, page, dtype)
+    masks = tree_masks(5, lens)
+    ref, tol = G.b.reference(0.1, masks)
+    C.assert_within(G.run(2, masks, 0.1), ref, tol)
+    wide = torch.full((7, 9000 // page), -4, dtype=torch.int32, device="cuda")
+    wide[:, :G.hidden.shape[1]] = G.hidden
+    C.assert_within(G.run(2, masks, 0.1, table=wide), ref, tol)
+
+
 def test_waits_that_give_up():
     """With a limit that its waits run into, the call ends with the time-out bit and the next is right."""
-    G = Groups(12, [0, 8], [3000], [1] * 8, [100] * 8, 8, 2, 128, 64, BF16)
+    G = Groups(12, [0, 8], [6000], [1] * 8, [100] * 8, 8, 2, 128, 64, BF16)  # (on the tiles)
     b = G.b
     ref, tol = b.reference(128 ** -0.5)
     cache = Bn.KvCache(b.k, b.v)
