@@ -91,41 +91,56 @@ struct Prefixes {
   int n_groups;
 };
 
-// The positions that a group shares, whole pages only (the page that a prefix ends in is each sequence's
-// own); -1 when its description is out of range.
-__device__ __forceinline__ int prefix_of(const Params &p, const Prefixes &g, int i) {
-  const int a = g.cu[i], b = g.cu[i + 1], len = g.len[i];
+// A group's description, all of it read at once.
+struct Group {
+  int begin, end;  // sequences
+  int shared;      // positions, whole pages only (the page that a prefix ends in is each sequence's own); -1 when
+                   // the description is out of range
+};
+
+__device__ __forceinline__ Group group_at(const Params &p, const Prefixes &g, int i) {
+  Group r;
+  const int before = g.cu[max(i - 1, 0)], after = g.cu[min(i + 2, g.n_groups)], len = g.len[i];
+  r.begin = g.cu[i], r.end = g.cu[i + 1];
   // (beside a group whose end is before its beginning, the bounds mean nothing either)
-  const bool ok = a >= 0 && a <= b && b <= p.n_seqs && len >= 0 && (i == 0 || g.cu[i - 1] <= a) &&
-                  (i + 1 == g.n_groups || b <= g.cu[i + 2]) &&
+  const bool ok = r.begin >= 0 && r.begin <= r.end && r.end <= p.n_seqs && len >= 0 &&
+                  (i == 0 || before <= r.begin) && (i + 1 == g.n_groups || r.end <= after) &&
                   len <= (static_cast<int64_t>(p.table_width) << p.page_shift) && len <= kMaxLen;
-  return ok ? len >> p.page_shift << p.page_shift : -1;
+  r.shared = ok ? len >> p.page_shift << p.page_shift : -1;
+  return r;
 }
 
-// The group of a sequence and the positions that it shares: 0 without a group, and when the prefix is longer
-// than what the sequence has before its queries.
-__device__ __forceinline__ int shared_by(const Params &p, const Prefixes &g, int s, int ctx, int *group) {
+// The group of a sequence; one of no positions for a sequence without.
+__device__ __forceinline__ Group group_of(const Params &p, const Prefixes &g, int s, int *index) {
+  Group r = {0, 0, 0};
+  *index = 0;
+  if (g.n_groups == 0) return r;
   int lo = 0, hi = g.n_groups;  // the last group that begins at s or before
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (g.cu[mid] <= s) lo = mid; else hi = mid;
   }
-  *group = lo;
-  if (g.n_groups == 0 || s < g.cu[lo] || s >= g.cu[lo + 1]) return 0;
-  const int len = prefix_of(p, g, lo);
-  return len > 0 && len <= ctx ? len : 0;
+  *index = lo;
+  r = group_at(p, g, lo);
+  if (s < r.begin || s >= r.end) r.shared = 0;
+  return r;
+}
+
+// The positions that a sequence shares: none when the prefix is longer than what it has before its queries.
+__device__ __forceinline__ int shared_by(const Group &g, int ctx) {
+  return g.shared > 0 && g.shared <= ctx ? g.shared : 0;
 }
 
 // A group's rows over its prefix.
 __device__ __forceinline__ Seq load_group(const Params &p, const Prefixes &g, int i, bool report) {
   Seq r = {};
-  const int len = prefix_of(p, g, i);
-  bool ok = len >= 0;
-  if (len > 0 && g.cu[i] < g.cu[i + 1]) {
-    r.row0 = p.cu[g.cu[i]];
-    const int64_t end = p.cu[g.cu[i + 1]];
+  const Group d = group_at(p, g, i);
+  bool ok = d.shared >= 0;
+  if (d.shared > 0 && d.begin < d.end) {
+    r.row0 = p.cu[d.begin];
+    const int64_t end = p.cu[d.end];
     ok = r.row0 >= 0 && end >= r.row0 && end <= p.n_rows;
-    if (ok) r.nq = static_cast<int>(end - r.row0), r.ctx = r.len = len;
+    if (ok) r.nq = static_cast<int>(end - r.row0), r.ctx = r.len = d.shared;
   }
   if (!ok && report && p.err) atomicOr(p.err, kDevErrBadId);
   return r;

@@ -75,6 +75,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 // ------------------------------------------------------------------ tensor copies
+// Brings a tensor map near before its first copy.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // Tile of a 4-d tensor map; c0 * element size is a multiple of 16 bytes.  Coordinates outside the
 // tensor read zeros.
 __device__ __forceinline__ void copy_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,

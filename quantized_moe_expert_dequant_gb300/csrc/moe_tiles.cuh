@@ -99,6 +99,11 @@ struct PromptParams {
 // the item's edge when fewer than kMinSteps steps would be cut off.  (16 packed prompts of 62 to 1984
 // tokens, cost 160, 224, 320: 96.9, 94.7, 96.3 us; least 2, 4 steps: 93.5, 94.7.)
 constexpr int kItemCost = 224;
+// kShared: a step of both tiles takes as long as the products, one of a tile by itself (of two that are taken
+// together) what K and V take from memory.
+// (us, heads of 128: a step of both tiles 1.75 to 2, of one 1.0 to 1.1, an item 1; heads of 64: 1.6, 0.83, 1.3.)
+constexpr int kBothTiles = 3, kOneTile = 2;
+__device__ constexpr int shared_item_cost(int dim) { return dim == 64 ? 192 : 128; }
 constexpr int kMinSteps = 2;
 // Steps of the longest item that the table allows, from which items are shared at all: below, a boundary
 // moves to the nearer edge of its item, and no parts are joined.  (32 query, 8 key/value heads of 128,
@@ -127,14 +132,22 @@ __device__ __forceinline__ Part load_part(const PromptParams &w, int i, bool rep
     return r;
   }
   if (MODE == kShared) r.seq = i -= w.g.n_groups;
+  int index;
+  Group group;  // (read before the sequence is looked at: one latency, not two)
+  if (MODE == kShared) group = group_of(w.p, w.g, i, &index);
   static_cast<Seq &>(r) = load_seq(w.p, i, report);
   if (MODE == kShared && r.nq) {
-    int group;
-    const int base = shared_by(w.p, w.g, i, r.ctx, &group);
+    const int base = shared_by(group, r.ctx);
     r.ctx -= base, r.len -= base;
     r.page0 = base >> w.p.page_shift;
   }
   return r;
+}
+
+// Of numbers that are not negative; a division of 64 bits takes some 400 cycles, and one thread makes eight
+// before a CTA knows its part.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return (x | y) >> 32 ? x / y : static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
 }
 
 struct Spot {  // the place before a step of an item
@@ -159,13 +172,21 @@ struct Share {
 };
 
 // Cost of the first k of a head's `tiles` items; per tokens an item.
-__device__ __forceinline__ int64_t head_cost(const Seq &s, bool tree, int per, int tiles, int k) {
-  if (tree) return static_cast<int64_t>(k) * (s.len + kItemCost);
+template <int MODE>
+__device__ __forceinline__ int64_t head_cost(const Seq &s, int per, int tiles, int k, int item_cost) {
+  if (MODE == kShared) {  // a last item of one tile
+    const bool one = k == tiles && 2 * (s.nq - (tiles - 1) * per) <= per;
+    return (k * kBothTiles - (one ? kBothTiles - kOneTile : 0)) *
+           static_cast<int64_t>(s.len + item_cost);
+  }
+  if (MODE == kTree) return static_cast<int64_t>(k) * (s.len + kItemCost);
   const int64_t full = k < tiles ? k : k - 1;
   return static_cast<int64_t>(k) * (s.ctx + kItemCost) + per * (full * (full + 1) / 2) +
          (k == tiles ? s.nq : 0);
 }
-__device__ __forceinline__ int item_steps(const Seq &s, bool tree, int per, int tile) {
+template <int MODE>
+__device__ __forceinline__ int item_steps(const Seq &s, int per, int tile) {
+  constexpr bool tree = MODE != kCausal;
   const int64_t seen =
       tree ? s.len
            : s.ctx + min(static_cast<int64_t>(tile + 1) * per, static_cast<int64_t>(s.nq));
@@ -173,24 +194,27 @@ __device__ __forceinline__ int item_steps(const Seq &s, bool tree, int per, int 
 }
 __device__ __forceinline__ int item_count(const Seq &s, int per) { return (s.nq + per - 1) / per; }
 
-__device__ __forceinline__ Spot spot_at(const Seq &s, bool tree, bool shared, int seq, int per,
+template <int MODE>
+__device__ __forceinline__ Spot spot_at(const Seq &s, bool shared, int seq, int per, int item_cost,
                                         int64_t y) {
   const int tiles = item_count(s, per);
-  const int64_t whole = head_cost(s, tree, per, tiles, tiles);
+  const int64_t whole = head_cost<MODE>(s, per, tiles, tiles, item_cost);
   Spot r;
   r.seq = seq;
-  r.head = static_cast<int>(y / whole);
+  r.head = static_cast<int>(quotient(y, whole));
   y -= r.head * whole;
   // k (ctx + kItemCost) + per k (k + 1) / 2 = y, then the exact k next to it
   const float b = s.ctx + kItemCost + 0.5f * per;
-  int k = tree ? static_cast<int>(y / (s.len + kItemCost))
-               : static_cast<int>((sqrtf(b * b + 2.f * per * static_cast<float>(y)) - b) / per);
+  int k = MODE == kShared ? static_cast<int>(quotient(y, kBothTiles * static_cast<int64_t>(s.len + item_cost)))
+          : MODE == kTree ? static_cast<int>(quotient(y, s.len + kItemCost))
+                          : static_cast<int>((sqrtf(b * b + 2.f * per * static_cast<float>(y)) - b) / per);
   k = max(0, min(k, tiles - 1));
-  while (k > 0 && head_cost(s, tree, per, tiles, k) > y) --k;
-  while (k + 1 < tiles && head_cost(s, tree, per, tiles, k + 1) <= y) ++k;
-  const int64_t at = head_cost(s, tree, per, tiles, k), cost = head_cost(s, tree, per, tiles, k + 1) - at;
-  const int n = item_steps(s, tree, per, k);
-  int step = static_cast<int>((y - at) * n / cost);
+  while (k > 0 && head_cost<MODE>(s, per, tiles, k, item_cost) > y) --k;
+  while (k + 1 < tiles && head_cost<MODE>(s, per, tiles, k + 1, item_cost) <= y) ++k;
+  const int64_t at = head_cost<MODE>(s, per, tiles, k, item_cost);
+  const int64_t cost = head_cost<MODE>(s, per, tiles, k + 1, item_cost) - at;
+  const int n = item_steps<MODE>(s, per, k);
+  int step = static_cast<int>(quotient((y - at) * n, cost));
   if (!shared) step = 2 * (y - at) < cost ? 0 : n;  // the nearer edge
   if (step < kMinSteps) step = 0;
   r.tile = k;
@@ -223,19 +247,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 
 // The CTA's part of the line: from s_spot[0] to s_spot[1].  False when there is nothing at all.
 template <int MODE>
-__device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_t *s_warp,
-                                          Spot *s_spot) {
+__device__ __forceinline__ bool find_part(const PromptParams &w, int per, int item_cost,
+                                          int64_t *s_warp, Spot *s_spot, Part *s_first) {
   const Params &p = w.p;
-  constexpr bool tree = MODE != kCausal;
   const bool shared = w.split;
   const int parts = part_count<MODE>(w);
   const auto cost = [&](const Seq &s) {
     if (s.nq == 0) return static_cast<int64_t>(0);
     const int tiles = item_count(s, per);
-    return p.hkv * head_cost(s, tree, per, tiles, tiles);
+    return p.hkv * head_cost<MODE>(s, per, tiles, tiles, item_cost);
   };
   int64_t total = 0, below = 0, mine = 0;
-  Seq s = {0, 0, 0, 0};
+  std::conditional_t<MODE == kShared, Part, Seq> s = {};
   for (int b = 0; b < parts; b += kPromptThreads) {
     const int i = b + threadIdx.x;
     mine = 0;
@@ -243,7 +266,8 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_
     total += block_scan(mine, s_warp, &below);
   }
   if (total == 0) return false;
-  const int64_t edge[2] = {blockIdx.x * total / gridDim.x, (blockIdx.x + 1) * total / gridDim.x};
+  const int64_t edge[2] = {quotient(blockIdx.x * total, gridDim.x),
+                           quotient((blockIdx.x + 1) * total, gridDim.x)};
   if (threadIdx.x == 0 && edge[1] == total) s_spot[1] = {parts, 0, 0, 0};
   int64_t sum = 0;
   for (int b = 0; b < parts; b += kPromptThreads) {
@@ -255,10 +279,13 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_
       below += sum;
       sum += all;
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (below <= edge[e] && edge[e] < below + mine)
-        s_spot[e] = spot_at(s, tree, shared, i, per, edge[e] - below);
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e)  // (rolled up: fetching code that runs once takes longer than running it)
+      if (below <= edge[e] && edge[e] < below + mine) {
+        s_spot[e] = spot_at<MODE>(s, shared, i, per, item_cost, edge[e] - below);
+        if constexpr (MODE == kShared)
+          if (e == 0) *s_first = s;
+      }
   }
   __syncthreads();
   return true;
@@ -266,6 +293,11 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int64_
 
 // An item as the warps work on it: the sequence, its first token here, the steps from `a` on that are
 // this CTA's, and how many of them each tile has.  more = 0: the CTA's part of the line is done.
+// Items of a pair: two, or the halves of a piece of one (what a piece leaves is joined with other parts anyway),
+// of a long one, or one that has no other beside it.
+constexpr int kTwo = 1, kHalves = 2;
+constexpr int kHalfSteps = 16;
+
 struct alignas(16) Item {
   int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, page0, rest, pair;
 };
@@ -281,9 +313,9 @@ struct Walk {
   Part s;
   int tiles;
 
-  __device__ __forceinline__ Walk(const PromptParams &w, const Spot *spot)
+  __device__ __forceinline__ Walk(const PromptParams &w, const Spot *spot, const Part &first)
       : w(w), tokens(w.tokens), per(2 * tokens), parts(part_count<MODE>(w)), at(spot[0]), end(spot[1]) {
-    s = load_part<MODE>(w, min(at.seq, parts - 1), false);
+    s = MODE == kShared ? first : load_part<MODE>(w, min(at.seq, parts - 1), false);
     tiles = item_count(s, per);
   }
   __device__ __forceinline__ Item next() {
@@ -305,7 +337,7 @@ struct Walk {
     r.row0 = s.row0, r.ctx = s.ctx, r.nq = s.nq, r.len = s.len;
     r.tok0 = at.tile * per;
     r.a = at.step;
-    const int n = item_steps(s, tree, per, at.tile);
+    const int n = item_steps<MODE>(s, per, at.tile);
     const int b = same_item(at, end) ? end.step : n;
     r.whole = r.a == 0 && b == n;
     const int n0 = tree ? n : (s.ctx + min(r.tok0 + tokens, s.nq) + kPos - 1) / kPos;
@@ -416,6 +448,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ Item s_item[kItems], s_other[MODE == kShared ? kItems : 1];  // (of a pair: tile 1's)
   __shared__ int64_t s_warp[kPromptThreads / 32];
   __shared__ Spot s_spot[2];
+  __shared__ Part s_first;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gone;
   const Params &p = w.p;
@@ -443,9 +476,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     s_gone = 0;
     tc::bar_fence_init();
   }
-  if (MODE == kShared) pdl_wait();
-  pdl_launch();
-  const bool any = find_part<MODE>(w, 2 * w.tokens, s_warp, s_spot);
+  if (MODE == kShared) {
+    if (threadIdx.x == 32 * (kSoftmaxWarps + 1)) tc::prefetch_map(&w.q), tc::prefetch_map(&w.k), tc::prefetch_map(&w.v);
+    pdl_wait();
+  } else {
+    pdl_launch();
+  }
+  const bool any = find_part<MODE>(w, 2 * w.tokens, shared_item_cost(D), s_warp, s_spot, &s_first);
   if (w.share && threadIdx.x == 0) {
     Share sh = {};
     if (any && before(s_spot[0], s_spot[1])) {
@@ -489,19 +526,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == kSoftmaxWarps + 2) {
     // ---------------------------------------------------------------- items, ahead of the others
     if (lane == 0) {
-      Walk<MODE> walk(w, s_spot);
-      Item ahead;  // kShared: the item that was not taken with the one before it
+      Walk<MODE> walk(w, s_spot, s_first);
+      Item ahead, other;  // kShared: the item that was not taken with the one before it; tile 1's
       bool held = false;
       for (int it = 0;; ++it) {
         Item item = MODE == kShared && held ? ahead : walk.next();
         held = false;
         if (MODE == kShared && item.more && item.count[1] == 0) {
-          ahead = walk.next();
-          held = !(ahead.more && ahead.count[1] == 0);
-          item.pair = !held;
+          if (item.whole || item.count[0] < kHalfSteps) {
+            ahead = walk.next();
+            held = !(ahead.more && ahead.count[1] == 0 &&
+                     (ahead.whole || ahead.count[0] < kHalfSteps));
+            other = ahead;
+            item.pair = held ? 0 : kTwo;
+          }
+          if (!item.pair && !item.whole && item.count[0] >= 2 * kMinSteps) {
+            const int half = item.count[0] / 2;
+            other = item;
+            other.steps = item.a;  // where the two begin
+            other.a += half, other.count[0] -= half;
+            item.count[0] = half;
+            item.pair = kHalves;
+          }
         }
         if (!tc::bar_wait(bar(s_item_free[it % kItems]), ((it / kItems) & 1) ^ 1, &s_gone)) break;
-        if (MODE == kShared && item.pair) ahead.pair = 1, s_other[it % kItems] = ahead;
+        if (MODE == kShared && item.pair) other.pair = item.pair, s_other[it % kItems] = other;
         s_item[it % kItems] = item;
         tc::bar_arrive(bar(s_item_full[it % kItems]));
         if (!item.more) break;
@@ -978,11 +1027,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // The next item's first P V overwrites O only after this warp has handed over that P.
       // Short loops: this code runs once an item, and fetching a long stretch of it took longer than
       // running it (16 packed prompts of 1024 tokens 88 us unrolled, 76 so).
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (item.a > 0 ? 0 : 1);
+      const bool second = MODE == kShared && i && item.pair == kHalves;
+      const int64_t slot =
+          2 * static_cast<int64_t>(blockIdx.x) + ((second ? item.steps : item.a) > 0 ? 0 : 1);
+      const int js = second ? 1 : j;  // the second half has the place of a second tile
       if (MODE == kShared && r < rows && item.a == 0) {
         const int64_t row = static_cast<int64_t>(item.rest) * p.n_rows + item.row0 + tok;
         const int head = r - r_tok * p.group;
-        if (head == 0) w.rows.begin[row * p.hkv + item.kvh] = item.whole ? kInRows : blockIdx.x;
+        if (head == 0) w.rows.begin[row * p.hkv + item.kvh] = item.whole ? kInRows : static_cast<int>(blockIdx.x);
         if (item.whole) w.rows.ml[row * p.hq + item.kvh * p.group + head] = make_float2(m, l);
       }
       if (MODE == kShared && item.whole) {
@@ -1003,7 +1055,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                               __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
         }
       } else if (!item.whole) {
-        float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + j) * (D / 4) * 128 + r;
+        float4 *part = reinterpret_cast<float4 *>(w.part) + (slot * 2 + js) * (D / 4) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -1064,11 +1116,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                   make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
         }
       }
-      if (!item.whole && r < rows) w.part_ml[slot * 256 + j * 128 + r] = make_float2(m, l);
+      if (!item.whole && r < rows) w.part_ml[slot * 256 + js * 128 + r] = make_float2(m, l);
+      if (MODE == kShared && !item.whole && item.pair != kHalves && tok_first + w.tokens >= item.nq && j == 0 &&
+          r < rows)
+        w.part_ml[slot * 256 + 128 + r] = make_float2(kNegInf, 0.f);  // no second half
     }
   }
   tc::fence_before();
   __syncthreads();
+  // Only now: blocks of the next kernel that find room before the last CTA ends crowd the SMs that are done first.
+  if (MODE == kShared) pdl_launch();
   if (threadIdx.x == 0 && s_gone && p.err) atomicOr(p.err, kDevErrTimeout);
   if (warp == kSoftmaxWarps) {
     tc::fence_after();
@@ -1142,94 +1199,131 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int to
                              8 * blockIdx.y) = v;
 }
 
-// kShared: joins what the items over the prefix and over the rest have left of a sequence's rows, one block a
-// sequence and key/value head, eight columns of a row a thread; parts are added in the order of the positions.
+// kShared: joins what the items over the prefix and over the rest have left of a token's rows, one block a
+// token and key/value head.  Two warps list the parts; then eight lanes take 64 columns of a row, and four times
+// eight every fourth part.  Parts are in the order of the positions.  (Short, since code that runs once is bound by
+// fetching it: a walk over the parts in each thread took 4 to 10 us, TODO so.)
+constexpr int kCombineThreads = 256;  // at most; two warps at least
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const Params p, const Prefixes g, const RowParts rows,
-                                                      int tokens,
-                                                      const float *part, const float2 *part_ml,
-                                                      const Share *share, int ctas) {
-  __shared__ uint32_t s_head[kMaxCtas / 32], s_ends[kMaxCtas / 32];
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Params p, const Prefixes g,
+                                                                  const RowParts rows, int tokens,
+                                                                  const float *part,
+                                                                  const float2 *part_ml,
+                                                                  const Share *share, int ctas) {
+  __shared__ int s_list[2][2 * kMaxCtas + 2], s_count[2];  // places of parts; kInRows
+  // (the batch is not the kernel's before this one, which has waited for it)
+  const int s = blockIdx.x / p.hkv, kvh = blockIdx.x % p.hkv, tok = blockIdx.y;
+  int group;
+  const Group described = group_of(p, g, s, &group);
+  const Seq q = load_seq(p, s, false);
+  const int base = q.nq ? shared_by(described, q.ctx) : 0;
+  Seq own = {};  // the rows over the prefix
+  if (base > 0) own = load_group(p, g, group, false);
   pdl_wait();
   pdl_launch();
-  const int s = blockIdx.x / p.hkv, kvh = blockIdx.x % p.hkv;
-  const Seq q = load_seq(p, s, false);
-  if (q.nq == 0) return;
-  for (int c0 = 0; c0 < kMaxCtas; c0 += 128) {
-    const int c = c0 + threadIdx.x;
-    const bool head = c < ctas && share[c].head;
-    const uint32_t heads = __ballot_sync(0xffffffffu, head);
-    const uint32_t ends = __ballot_sync(0xffffffffu, head && share[c].head_ends);
-    if (threadIdx.x % 32 == 0) s_head[c / 32] = heads, s_ends[c / 32] = ends;
-  }
-  int group;
-  const int base = shared_by(p, g, s, q.ctx, &group);
-  Seq both[2] = {{}, q};  // what the rows are counted in: the group, the sequence
-  if (base > 0) both[0] = load_group(p, g, group, false);
+  if (tok >= q.nq) return;
   // rows outside their group's: offsets of the batch that do not fit together
-  const bool first = base > 0 && q.row0 >= both[0].row0 && q.row0 + q.nq <= both[0].row0 + both[0].nq;
-  if (base > 0 && !first) {
+  if (base > 0 && (q.row0 < own.row0 || q.row0 + q.nq > own.row0 + own.nq)) {
     if (threadIdx.x == 0 && p.err) atomicOr(p.err, kDevErrBadId);
     return;
   }
-  __syncthreads();
-  const int c8 = threadIdx.x % (D / 8);
-  for (int R = blockIdx.y * (128 / (D / 8)) + threadIdx.x / (D / 8); R < q.nq * p.group;
-       R += gridDim.y * (128 / (D / 8))) {
-    const int tok = R / p.group, head = R - tok * p.group;
-    const int64_t row = q.row0 + tok;
-    // the parts, one after the other: f(maximum and sum, eight columns)
-    const auto each = [&](auto f) {
+  const int64_t row = q.row0 + tok;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the row's place among its item's, and its item's tiles, over the prefix and over the rest
+  int first[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (k == 0 && !first) continue;
-        const int64_t at = k * static_cast<int64_t>(p.n_rows) + row;
-        const int c = rows.begin[at * p.hkv + kvh];
-        if (c == kInRows) {
-          const int64_t i = at * p.hq + kvh * p.group + head;
-          f(rows.ml + i, reinterpret_cast<const float4 *>(rows.out) + i * (D / 4) + 2 * c8, 1);
-          continue;
+  for (int k = 0; k < 2; ++k) {
+    const int at = k ? tok : q.row0 - own.row0 + tok, of = k ? q.nq : own.nq;
+    const int in_item = at % (2 * tokens), tile = in_item / tokens;
+    first[k] = (in_item - tile * tokens) * p.group;
+    if (warp != k) continue;
+    // an item of one tile may have been taken in halves, the second in the place of a second tile
+    const int halves = of - (at - in_item) <= tokens ? 2 : 1;
+    int n = 0;
+    if (k == 1 || base > 0) {
+      const int c = rows.begin[(k * static_cast<int64_t>(p.n_rows) + row) * p.hkv + kvh];
+      const auto put = [&](int place, int slot) {
+        for (int h = 0; h < halves; ++h) s_list[k][place * halves + h] = 2 * slot + tile + h;
+      };
+      if (static_cast<unsigned>(c) >= static_cast<unsigned>(ctas)) {  // (or a wait gave up)
+        if (lane == 0) s_list[k][0] = kInRows;
+        n = 1;
+      } else {
+        if (lane == 0) put(0, 2 * c + 1);
+        n = 1;
+        for (int c0 = c + 1; c0 < ctas; c0 += 32) {
+          const int i = c0 + lane;
+          const bool head = i < ctas && share[i].head;
+          const uint32_t stop = __ballot_sync(0xffffffffu, head && share[i].head_ends);
+          uint32_t parts = __ballot_sync(0xffffffffu, head);  // without: a CTA that had no work
+          if (stop) parts &= 0xffffffffu >> (32 - __ffs(stop));
+          if (parts >> lane & 1) put(n + __popc(parts & ((1u << lane) - 1)), 2 * i);
+          n += __popc(parts);
+          if (stop) break;
         }
-        if (static_cast<unsigned>(c) >= static_cast<unsigned>(ctas)) continue;  // (a wait gave up)
-        const int in_item = (q.row0 - both[k].row0 + tok) % (2 * tokens), i = in_item / tokens;
-        const int r = (in_item - i * tokens) * p.group + head;
-        const auto one = [&](int slot) {
-          f(part_ml + slot * 256 + i * 128 + r,
-            reinterpret_cast<const float4 *>(part) +
-                ((static_cast<int64_t>(slot) * 2 + i) * (D / 4) + 2 * c8) * 128 + r,
-            128);
-        };
-        one(2 * c + 1);
-        for (int n = c + 1; n < ctas; ++n) {
-          if (!(s_head[n / 32] >> (n % 32) & 1)) continue;  // a CTA that had no work
-          one(2 * n);
-          if (s_ends[n / 32] >> (n % 32) & 1) break;
+        n *= halves;
+      }
+    }
+    if (lane == 0) s_count[k] = n;
+  }
+  __syncthreads();
+  constexpr int kThreadsARow = D / 2;  // D / 8 columns, four times
+  const int at_once = blockDim.x / kThreadsARow;
+  const int fourth = lane >> 3, c8 = (threadIdx.x % kThreadsARow) / 32 * 8 + (lane & 7);
+#pragma unroll 1
+  for (int head = threadIdx.x / kThreadsARow; head < p.group; head += at_once) {  // (a warp has one)
+    float m = kNegInf, l = 0.f, o[8] = {};
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+#pragma unroll 2
+      for (int i = fourth; i < s_count[k]; i += 4) {
+        const int at = s_list[k][i];
+        int64_t from = static_cast<int64_t>(at) * 128 + first[k] + head;
+        const float2 *ml = part_ml + from;
+        const float4 *x = reinterpret_cast<const float4 *>(part) + from +
+                          (static_cast<int64_t>(at) * (D / 4 - 1) + 2 * c8) * 128;
+        int apart = 128;
+        if (at == kInRows) {
+          from = (k * static_cast<int64_t>(p.n_rows) + row) * p.hq + kvh * p.group + head;
+          ml = rows.ml + from;
+          x = reinterpret_cast<const float4 *>(rows.out) + from * (D / 4) + 2 * c8;
+          apart = 1;
         }
+        const float2 v = *ml;
+        const float4 a = x[0], b = x[apart];
+        // a part without weight may not have been written; a sum that is NaN counts
+        const bool none = v.y == 0.f;
+        const float top = none ? m : fmaxf(m, v.x);
+        const float f = none ? 0.f : exp2_approx((v.x - top) * p.scale_log2);
+        const float old = m == kNegInf ? 0.f : exp2_approx((m - top) * p.scale_log2);
+        m = top;
+        l = none ? l : fmaf(v.y, f, l * old);
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = none ? o[e] : fmaf(y[e], f, o[e] * old);
       }
-    };
-    float m = kNegInf;
-    each([&](const float2 *ml, const float4 *, int) { m = fmaxf(m, ml->x); });
-    float l = 0.f, o[8] = {};
-    each([&](const float2 *ml, const float4 *x, int apart) {
-      const float2 v = *ml;
-      const float4 a = x[0], b = x[apart];
-      if (!(v.y == 0.f)) {  // a part without weight may not have been written; a sum that is NaN counts
-        const float f = exp2_approx((v.x - m) * p.scale_log2);
-        l = fmaf(v.y, f, l);
-        o[0] = fmaf(a.x, f, o[0]), o[1] = fmaf(a.y, f, o[1]);
-        o[2] = fmaf(a.z, f, o[2]), o[3] = fmaf(a.w, f, o[3]);
-        o[4] = fmaf(b.x, f, o[4]), o[5] = fmaf(b.y, f, o[5]);
-        o[6] = fmaf(b.z, f, o[6]), o[7] = fmaf(b.w, f, o[7]);
-      }
-    });
+    __syncwarp();
+#pragma unroll 1
+    for (int w = 8; w < 32; w <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, w), l2 = __shfl_xor_sync(0xffffffffu, l, w);
+      const float top = fmaxf(m, m2);
+      const float f = m == kNegInf ? 0.f : exp2_approx((m - top) * p.scale_log2);
+      const float f2 = m2 == kNegInf ? 0.f : exp2_approx((m2 - top) * p.scale_log2);
+      m = top;
+      l = l * f + l2 * f2;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], w) * f2;
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint4 v;
     v.x = Half<T>::pack(o[0] * inv, o[1] * inv);
     v.y = Half<T>::pack(o[2] * inv, o[3] * inv);
     v.z = Half<T>::pack(o[4] * inv, o[5] * inv);
     v.w = Half<T>::pack(o[6] * inv, o[7] * inv);
-    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.o_row + (kvh * p.group + head) * p.o_head +
-                               8 * c8) = v;
+    if (fourth == 0)
+      *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.o_row +
+                                 (kvh * p.group + head) * p.o_head + 8 * c8) = v;
   }
 }
 
@@ -1309,9 +1403,9 @@ static int launch(const moe_kv_cache *c, const Params &p, const Prefixes &g, con
   if constexpr (MODE == kShared) {
     e = launch_early(kern, dim3(plan.grid), kPromptThreads, Prompt<D>::kSmem, stream, w);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    const int at_once = 128 / (D / 8);  // rows of a block
-    const dim3 grid(p.n_seqs * p.hkv, std::min(8, (p.max_q * p.group + at_once - 1) / at_once));
-    e = launch_early(combine_kernel<T, D>, grid, 128, 0, stream, p, w.g, w.rows, w.tokens, part,
+    const dim3 grid(p.n_seqs * p.hkv, p.max_q);
+    const int threads = std::max(64, std::min(kCombineThreads, p.group * (D / 2)));
+    e = launch_early(combine_kernel<T, D>, grid, threads, 0, stream, p, w.g, w.rows, w.tokens, part,
                      part_ml, share, plan.grid);
   } else {
     kern<<<plan.grid, kPromptThreads, Prompt<D>::kSmem, stream>>>(w);

@@ -375,9 +375,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       ld.pages = p.table + ld.seq * p.table_stride;
     }
     if constexpr (ITEMS == kGrouped) {
-      int group;
-      ld.limit = shared_by(p, w.g, ld.seq, q.ctx, &group);
-      ld.first = ld.limit ? p.table + w.g.cu[group] * p.table_stride : ld.pages;
+      int index;
+      const Group group = group_of(p, w.g, ld.seq, &index);
+      ld.limit = shared_by(group, q.ctx);
+      ld.first = ld.limit ? p.table + group.begin * p.table_stride : ld.pages;
     }
     ld.head_off = ld.kvh * p.head_stride;
     look_up();
