@@ -139,9 +139,8 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
 // The order of two pages may hang on the last bit of their scores, so it is decided in two steps: fp32 scores
 // with a bound on their error tell which pages are certainly among the k best and which are certainly
 // not; what lies between is compared by scores in fp64 (exact but for bounds and queries that differ by more
-// than 2^30).  A score is the fp32 sum of terms Q b: Q a sum over the heads of numbers of one sign, the terms
-// added in at most 10 steps one after the other, so it is off by less than (group + 12) 2^-24 times the sum of
-// the terms' sizes, and that is at most max_d |b_d| times sum_d |Q_d|.
+// than 2^30).  A score is the fp32 sum of terms Q b, Q a sum over the heads of numbers of one sign.  It is off by
+// less than `error` times the sum of the terms' sizes, and that is at most max_d |b_d| times sum_d |Q_d|.
 constexpr int kMaxPages = 65536;     // of a sequence: a bit each in shared memory
 constexpr int kKeys = 8192;          // scores that are kept in shared memory
 constexpr int kBins = 1024;
@@ -167,7 +166,7 @@ __device__ __forceinline__ V sum_heads(const Params &p, int row, int kvh, V *s_q
   const T *q = static_cast<const T *>(p.q) + row * p.q_row +
                static_cast<int64_t>(kvh) * p.group * p.q_head;
   V size = 0;
-  for (int d = threadIdx.x; d < D; d += kBlock) {
+  for (int d = threadIdx.x; d < D; d += blockDim.x) {
     V down = 0, up = 0;
 #pragma unroll 8
     for (int h = 0; h < p.group; ++h) {
@@ -275,59 +274,154 @@ __device__ __forceinline__ int scored(const Select &w, const Row &row) {
   return pages > w.n_select ? pages - w.recent : 0;
 }
 
-// For chunks, whose rows share what is read: scores of kTurns * 64 pages for kSharing rows into w.score.
-constexpr int kSharing = 4, kTurns = 4;
+// For chunks, whose rows share what is read: scores of 16 rows and kTurns * 128 pages a block into w.score, on
+// mma.sync.  The sums Q of a row, scaled by a power of two so that the type holds the largest, are split in two
+// numbers of 16 bits (error 2^-18 of each Q; bounds are exact), rows are the rows of the products, pages the
+// columns; each truncation of an fp32 sum counts 2^-23.  A lane's 16 bytes of a bound are its places of two
+// products: the order of the dimensions is the same for both factors.  (In fp32 on the other units, four rows a
+// block: 512 rows, 2000 pages, 2 heads of 64: 85 us; TODO so.)
+constexpr int kRowTile = 16, kTurns = 2, kPagesATurn = 128;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
-  constexpr int R = kSharing, P = 2, kPages = P * (kBlock / 8);
-  __shared__ __align__(16) float s_q[R][2 * D];
-  __shared__ float s_size[R];
+  constexpr int kStride = 2 * D + 32;  // elements: 64 bytes of padding keep the rows' banks apart
+  constexpr int kSteps = 2 * D / 32;   // of 32 dimensions, two products
+  __shared__ __align__(16) T s_q[2][kRowTile][kStride];  // larger and smaller part
+  __shared__ float s_size[kRowTile], s_scale[kRowTile];
+  __shared__ int s_seq[kRowTile], s_count[kRowTile];
   const Params &p = w.p;
   pdl_wait();
   pdl_launch();
-  const int first = w.row0 + blockIdx.x * R, kvh = blockIdx.y;
-  const int begin = blockIdx.z * kTurns * kPages;
-  const int n = min(R, w.row0 + w.rows - first);
-  int seq[R], count[R], most = 0;
-  bool one = true;  // sequence
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
+  const int first = w.row0 + blockIdx.x * kRowTile, kvh = blockIdx.y;
+  const int begin = blockIdx.z * kTurns * kPagesATurn;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < kRowTile) {
+    const int r = threadIdx.x;
     Row row = {};
-    if (r < n) row = load_row(p, first + r, 1);
-    seq[r] = row.seq, count[r] = scored(w, row);
-    if (count[r] > 0) one &= seq[r] == seq[0];
-    most = max(most, count[r]);
+    if (blockIdx.x * kRowTile + r < w.rows) row = load_row(p, first + r, 1);
+    s_seq[r] = row.seq, s_count[r] = scored(w, row);
   }
-  if (begin >= most || begin + kTurns * kPages <= w.sink) return;
-  one &= count[0] > 0;
-  if (threadIdx.x < R) s_size[threadIdx.x] = 0.f;
   __syncthreads();
-  Block<T, D, P> b;
-  int at = begin;
-  if (one) b.fetch(w, seq[0], kvh, at, most);
+  int most = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (count[r] > 0) add_size<D>(sum_heads<T, D>(p, first + r, kvh, s_q[r]), &s_size[r]);
+  for (int r = 0; r < kRowTile; ++r) most = max(most, s_count[r]);
+  if (begin >= most || begin + kTurns * kPagesATurn <= w.sink) return;
+  const int g = lane >> 2, q4 = lane & 3;
+  uint4 b[2][kSteps];
+  bool there[2];
+  const auto fetch = [&](int seq, int count, int at) {  // the bounds of two times eight pages
+    int page[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int j = at + 8 * t + g;
+      page[t] = j < count ? p.table[seq * p.table_stride + j] : -1;
+      there[t] = static_cast<unsigned>(page[t]) < static_cast<unsigned>(p.n_pages);
+      if (!there[t] && j < count && j >= w.sink && q4 == 0 && p.err) atomicOr(p.err, kDevErrBadId);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const T *src = static_cast<const T *>(w.bounds) +
+                     (static_cast<int64_t>(there[t] ? page[t] : 0) * p.hkv + kvh) * 2 * D + 8 * q4;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) b[t][k] = load16(src + 32 * k);
+    }
+  };
+  const auto end_of = [&](int r0, int *count) {  // of the rows from r0 on that are of one sequence
+    int r1 = r0;
+    for (*count = 0; r1 < kRowTile && s_seq[r1] == s_seq[r0]; ++r1) *count = max(*count, s_count[r1]);
+    return r1;
+  };
+  int count, r1 = end_of(0, &count);
+  fetch(s_seq[0], count, begin + 16 * warp);  // on its way during the sums
+  // a warp takes two rows' sums, a lane some neighbouring dimensions
+  constexpr int V = D / 32;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * warp + e;
+    float down[V] = {}, up[V] = {}, size = 0.f, top = 0.f;
+    if (s_count[r] > 0) {
+      const T *q = static_cast<const T *>(p.q) + (first + r) * p.q_row +
+                   static_cast<int64_t>(kvh) * p.group * p.q_head + V * lane;
+#pragma unroll 4
+      for (int h = 0; h < p.group; ++h)
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+          const float2 x = Half<T>::unpack(*reinterpret_cast<const uint32_t *>(q + h * p.q_head + v));
+          if (x.x < 0.f) down[v] += x.x; else up[v] += x.x;  // (a NaN goes up)
+          if (x.y < 0.f) down[v + 1] += x.y; else up[v + 1] += x.y;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) size += up[v] - down[v], top = fmaxf(top, fmaxf(up[v], -down[v]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      size += __shfl_xor_sync(0xffffffffu, size, o);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    // fp16: the largest is brought to 2^14 .. 2^15
+    int exponent = 0;
+    if (sizeof(T) == 2 && Half<T>::kRow > 0.f && top > 0.f && top < 3e38f)
+      frexpf(top, &exponent), exponent -= 15;
+    if (lane == 0) s_size[r] = size, s_scale[r] = ldexpf(1.f, exponent);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const float x = ldexpf(s ? up[v] : down[v], -exponent);
+        const float y = ldexpf(s ? up[v + 1] : down[v + 1], -exponent);
+        const uint32_t large = Half<T>::pack(x, y);
+        const float2 f = Half<T>::unpack(large);
+        const uint32_t small = Half<T>::pack(x - f.x, y - f.y);
+        *reinterpret_cast<uint32_t *>(&s_q[0][r][s * D + V * lane + v]) = large;
+        *reinterpret_cast<uint32_t *>(&s_q[1][r][s * D + V * lane + v]) = small;
+      }
+  }
   __syncthreads();
-  for (int turn = 0; turn < kTurns && at < most; ++turn) {
-    if (one) b.sizes();
+  for (int r0 = 0; r0 < kRowTile; r0 = r1) {
+    const int seq = s_seq[r0];
+    r1 = end_of(r0, &count);
+    for (int turn = 0; turn < kTurns; ++turn) {
+      const int at = begin + turn * kPagesATurn + 16 * warp;
+      if (at >= count) break;
+      if (r0 + turn > 0) fetch(seq, count, at);
+      float large[2][4] = {}, small[2][4] = {};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (count[r] == 0) continue;
-      if (!one) b.fetch(w, seq[r], kvh, at, count[r]), b.sizes();
-      float s[P];
-      b.score(s_q[r], s);
+      for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int t = 0; t < P; ++t) {
-        const int j = at + (threadIdx.x >> 3) + t * (kBlock / 8);
-        if ((threadIdx.x & 7) == 0 && j < count[r])
-          w.score[(static_cast<int64_t>(blockIdx.x * R + r) * p.hkv + kvh) * w.width + j] =
-              make_float2(s[t], fmaxf(b.top[t], 0.f) * s_size[r]);
+        for (int s = 0; s < 2; ++s) {
+          const uint4 lo = *reinterpret_cast<const uint4 *>(&s_q[s][g][32 * k + 8 * q4]);
+          const uint4 hi = *reinterpret_cast<const uint4 *>(&s_q[s][g + 8][32 * k + 8 * q4]);
+          const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            Half<T>::mma(s ? small[t] : large[t], a0, b[t][k].x, b[t][k].y);
+            Half<T>::mma(s ? small[t] : large[t], a1, b[t][k].z, b[t][k].w);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          m = max2<T>(max2<T>(m, b[t][k].x & 0x7fff7fffu),
+                      max2<T>(max2<T>(b[t][k].y & 0x7fff7fffu, b[t][k].z & 0x7fff7fffu),
+                              b[t][k].w & 0x7fff7fffu));
+        const float2 f = Half<T>::unpack(m);
+        float top = fmaxf(f.x, f.y);  // the largest size of a bound of page g
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (!there[t]) top = -1.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // row g or g + 8, page 2 q4 or 2 q4 + 1
+          const float size = __shfl_sync(0xffffffffu, top, 4 * (2 * q4 + (c & 1)));
+          const int r = g + 8 * (c >> 1), j = at + 8 * t + 2 * q4 + (c & 1);
+          if (r >= r0 && r < r1 && j < s_count[r])
+            w.score[(static_cast<int64_t>(blockIdx.x * kRowTile + r) * p.hkv + kvh) * w.width + j] =
+                size < 0.f ? make_float2(kNegInf, 0.f)
+                           : make_float2((large[t][c] + small[t][c]) * s_scale[r], size * s_size[r]);
+        }
       }
     }
-    at += kPages;
-    if (one && turn + 1 < kTurns) b.fetch(w, seq[0], kvh, at, most);
   }
 }
 
@@ -347,6 +441,7 @@ __device__ __forceinline__ uint64_t key_of(double s) {
 }
 
 // Sum over the block, for every thread.
+template <int WARPS>
 __device__ __forceinline__ int block_sum(int v, int *s_sum) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
@@ -354,10 +449,11 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
   __syncthreads();
   int all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += s_sum[w];
+  for (int w = 0; w < WARPS; ++w) all += s_sum[w];
   return all;
 }
 // Sum over the threads before this one.
+template <int WARPS>
 __device__ __forceinline__ int block_below(int v, int *s_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -371,7 +467,7 @@ __device__ __forceinline__ int block_below(int v, int *s_sum) {
   __syncthreads();
   int base = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
+  for (int w = 0; w < WARPS; ++w)
     if (w < warp) base += s_sum[w];
   return base + x - v;
 }
@@ -393,14 +489,18 @@ __device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
       : "memory");
 }
 
+constexpr int kFewThreads = 256;
+
 // The pages of a row and key/value head.  CS = 0: one block, the scores are in w.score.  CS > 0: a cluster of
 // CS blocks scores the pages, and its first takes all scores in its shared memory and chooses.
 template <typename T, int D, int CS>
-__global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
+__global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const Select w) {
+  constexpr int kThreads = CS ? kBlock : kFewThreads, kN = kThreads / 32;
   extern __shared__ __align__(16) uint32_t s_dyn[];
-  __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
+  __shared__ int s_sum[kN], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
   __shared__ uint32_t s_range[3 * (CS ? CS : 1)];  // of each block's part: least and largest key, largest size
   __shared__ double s_q[2 * D], s_exact[kFew];
+  __shared__ float s_edge[2];
   const Params &p = w.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = CS > 1 ? blockIdx.x % CS : 0;
@@ -410,14 +510,14 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
   if (!behind) pdl_wait();
   pdl_launch();
   if (blockIdx.x == 0 && row_i == 0 && kvh == 0)
-    for (int i = threadIdx.x; i < p.n_seqs; i += kBlock) load_seq(p, i, true);
+    for (int i = threadIdx.x; i < p.n_seqs; i += kThreads) load_seq(p, i, true);
   const Row row = load_row(p, row_i, 1);
   const int pages = row.nq ? ((row.ctx - 1) >> p.page_shift) + 1 : 0;
   int32_t *out = w.out + (static_cast<int64_t>(row_i) * p.hkv + kvh) * w.n_select;
   if (pages <= w.n_select) {
     if (behind) pdl_wait();
     if (row.nq && rank == 0)
-      for (int i = threadIdx.x; i < w.n_select; i += kBlock) out[i] = i < pages ? i : -1;
+      for (int i = threadIdx.x; i < w.n_select; i += kThreads) out[i] = i < pages ? i : -1;
     return;
   }
   const int words = (pages + 31) / 32, j0 = w.sink, j1 = pages - w.recent, n = j1 - j0;
@@ -464,7 +564,7 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     size *= s_size;
   }
   if (rank == 0) {
-    for (int i = threadIdx.x; i < words; i += kBlock) {
+    for (int i = threadIdx.x; i < words; i += kThreads) {
       // all 32 bits from bit 32 i on that are before j0 or from j1 to the end
       uint32_t m = 0;
       const int from = 32 * i;
@@ -473,13 +573,13 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
       if (from + 32 > pages) m &= (1u << (pages - from)) - 1;
       s_sel[i] = m, s_mid[i] = 0u;
     }
-    for (int i = threadIdx.x; i < kBins; i += kBlock) s_bins[i] = 0u;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s_bins[i] = 0u;
     if (threadIdx.x == 0) s_count = s_in = s_mid_count = 0;
   }
   if (behind) pdl_wait();
   if (CS == 0 && want > 0) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kBlock) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += kThreads) {
       const float2 s = score[j0 + i];
       const uint32_t key = key_of(s.x);
       if (kept) s_keys[i] = key;
@@ -490,11 +590,11 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
   // sizes are positive or NaN: their order is that of their bits
   lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
   uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
-  __shared__ uint32_t s_part[3][kWarps];
+  __shared__ uint32_t s_part[3][kN];
   if (lane == 0) s_part[0][warp] = lo, s_part[1][warp] = hi, s_part[2][warp] = most;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < kWarps; ++v)
+  for (int v = 0; v < kN; ++v)
     lo = min(lo, s_part[0][v]), hi = max(hi, s_part[1][v]), most = max(most, s_part[2][v]);
   if constexpr (CS > 1) {
     if (threadIdx.x == 0) {
@@ -515,25 +615,27 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     const float error = 2.f * w.error * size + 1e-40f;  // (products below fp32's range)
     // [lo, hi]: keys among which the want-th largest is; `above` keys are larger than those
     int above = 0, inside = n;
-    while (lo < hi && inside > 1) {
+    while (lo < hi && inside > kFew / 4) {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
-      for (int i = threadIdx.x; i < n; i += kBlock) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint32_t key = key_at(i);
         if (lo <= key && key <= hi) atomicAdd(&s_bins[(key - lo) >> shift], 1u);
       }
       __syncthreads();
-      // bins from the largest keys down, four a thread
-      uint32_t c[4];
+      // bins from the largest keys down, some a thread
+      constexpr int kEach = kBins / kThreads;
+      uint32_t c[kEach];
       int sum = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = s_bins[kBins - 1 - 4 * threadIdx.x - e], sum += c[e];
-      int before = above + block_below(sum, s_sum);
+      for (int e = 0; e < kEach; ++e) c[e] = s_bins[kBins - 1 - kEach * threadIdx.x - e], sum += c[e];
+      int before = above + block_below<kN>(sum, s_sum);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kEach; ++e) {
         if (before < want && want <= before + static_cast<int>(c[e]))
-          s_bin = kBins - 1 - 4 * threadIdx.x - e, s_above = before, s_in_bin = c[e];
+          s_bin = kBins - 1 - kEach * threadIdx.x - e, s_above = before, s_in_bin = c[e];
         before += c[e];
-        s_bins[kBins - 1 - 4 * threadIdx.x - e] = 0u;
+        s_bins[kBins - 1 - kEach * threadIdx.x - e] = 0u;
       }
       __syncthreads();
       const uint32_t from = lo + (static_cast<uint32_t>(s_bin) << shift);
@@ -544,7 +646,8 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     // certainly in, and those that only fp64 can tell; a warp takes 32 pages, a word of the masks
     const float t_hi = score_of(hi) + error, t_lo = score_of(lo) - error;
     int in = 0, mid = 0;
-    for (int i = warp; i < words; i += kWarps) {
+#pragma unroll 4
+    for (int i = warp; i < words; i += kN) {
       const int j = 32 * i + lane;
       bool is_in = false, is_mid = false;
       if (j >= j0 && j < j1) {
@@ -564,14 +667,40 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
     if (lane == 0) atomicAdd(&s_in, in), atomicAdd(&s_mid_count, mid);
     __syncthreads();
     in = s_in, mid = s_mid_count;
-    const int need = want - in;  // of the mid ones: 1 .. mid
-    if (need >= mid) {
-      for (int i = threadIdx.x; i < words; i += kBlock) s_sel[i] |= s_mid[i];
-    } else {
+    int need = want - in;  // of the mid ones: 1 .. mid
+    // A few: fp32 tells those that are further than the error from the first that is left out, or from the last
+    // that is taken.
+    const bool told = need >= mid;
+    if (told) {
+      for (int i = threadIdx.x; i < words; i += kThreads) s_sel[i] |= s_mid[i];
+    } else if (mid <= kFew) {
+      float s = 0.f;
+      int j = 0, ahead = 0;
+      if (threadIdx.x < mid) {
+        j = s_at[threadIdx.x];
+        s = score_of(key_at(j - j0));
+        for (int i = 0; i < mid; ++i) {
+          const float other = score_of(key_at(s_at[i] - j0));
+          ahead += other > s || (other == s && s_at[i] < j);
+        }
+        if (ahead == need - 1) s_edge[0] = s;
+        if (ahead == need) s_edge[1] = s;
+      }
+      __syncthreads();
+      const bool taken = threadIdx.x < mid && s > s_edge[1] + error;
+      const bool left = threadIdx.x < mid && !taken && !(s < s_edge[0] - error);
+      if (taken) atomicOr(&s_sel[j >> 5], 1u << (j & 31));
+      if (threadIdx.x == 0) s_count = 0;
+      need -= __syncthreads_count(taken);
+      mid = __syncthreads_count(left);
+      if (left) s_at[atomicAdd(&s_count, 1)] = j;
+      __syncthreads();
+    }
+    if (!told && need > 0) {
       sum_heads<T, D>(p, row_i, kvh, s_q);
       __syncthreads();
       bool any = false;
-      for (int d = threadIdx.x; d < 2 * D; d += kBlock) any |= s_q[d] != 0.;
+      for (int d = threadIdx.x; d < 2 * D; d += kThreads) any |= s_q[d] != 0.;
       any = __syncthreads_or(any);  // without (a row of padding), all scores are 0
       const auto exact = [&](int j) {  // a whole warp
         const int page = p.table[row.seq * p.table_stride + j];
@@ -587,7 +716,7 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
         return x == x ? x : -__builtin_huge_val();
       };
       if (any && mid <= kFew) {
-        for (int i = warp; i < mid; i += kWarps) {
+        for (int i = warp; i < mid; i += kN) {
           const double x = exact(s_at[i]);
           if (lane == 0) s_exact[i] = x;
         }
@@ -603,7 +732,7 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
         // Many pages with the same score but for rounding.  Their fp64 keys take the scores' place, and
         // the need-th largest is found bit by bit.
         uint64_t *key = reinterpret_cast<uint64_t *>(score);
-        for (int i = warp; any && i < words; i += kWarps)
+        for (int i = warp; any && i < words; i += kN)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
             const int j = 32 * i + __ffs(m) - 1;
             const double x = exact(j);
@@ -612,21 +741,21 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
         __syncthreads();
         const auto count = [&](uint64_t least) {
           int c = 0;
-          for (int i = threadIdx.x; i < words; i += kBlock)
+          for (int i = threadIdx.x; i < words; i += kThreads)
             for (uint32_t m = s_mid[i]; m; m &= m - 1) c += key[32 * i + __ffs(m) - 1] >= least;
-          return block_sum(c, s_sum);
+          return block_sum<kN>(c, s_sum);
         };
         uint64_t last = 0;
         for (int b = 63; any && b >= 0; --b)
           if (count(last | 1ull << b) >= need) last |= 1ull << b;
         const int ties = any ? need - count(last + 1) : need;  // the lower pages
-        const int each = (words + kBlock - 1) / kBlock;
+        const int each = (words + kThreads - 1) / kThreads;
         const int i0 = min(words, static_cast<int>(threadIdx.x) * each), i1 = min(words, i0 + each);
         int mine = 0;
         for (int i = i0; i < i1; ++i)
           for (uint32_t m = s_mid[i]; m; m &= m - 1)
             mine += !any || key[32 * i + __ffs(m) - 1] == last;
-        int before = block_below(mine, s_sum);
+        int before = block_below<kN>(mine, s_sum);
         for (int i = i0; i < i1; ++i)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
             const uint64_t x = any ? key[32 * i + __ffs(m) - 1] : last;
@@ -638,13 +767,13 @@ __global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
   __syncthreads();
   // the pages in order
   int done = 0;
-  for (int b = 0; b < words; b += kBlock) {
+  for (int b = 0; b < words; b += kThreads) {
     const int i = b + threadIdx.x;
     const uint32_t mine = i < words ? s_sel[i] : 0u;
-    int at = done + block_below(__popc(mine), s_sum);
+    int at = done + block_below<kN>(__popc(mine), s_sum);
     for (uint32_t m = mine; m; m &= m - 1, ++at)
       if (at < w.n_select) out[at] = 32 * i + __ffs(m) - 1;
-    if (b + kBlock < words) done += block_sum(__popc(mine), s_sum);
+    if (b + kThreads < words) done += block_sum<kN>(__popc(mine), s_sum);
   }
 }
 
@@ -722,15 +851,16 @@ static cudaError_t launch_select(Select w, const SelectPlan &plan, cudaStream_t 
   static SmemLimit limit;
   cudaError_t e = limit.set(reinterpret_cast<const void *>(pick), smem(kMaxPages));
   if (e != cudaSuccess) return e;
-  constexpr int kPages = kTurns * 64;
+  constexpr int kPages = kTurns * kPagesATurn;
+  w.error = (2 * D + 64 + p.group) * 1.2e-7f;  // (the split counts 32 truncations, the sums' group of them)
   for (; w.row0 < p.n_rows; w.row0 += plan.rows) {
     w.rows = std::min(plan.rows, p.n_rows - w.row0);
     if (p.table_width > w.n_select) {  // (otherwise every page of every row is selected)
-      const dim3 grid((w.rows + kSharing - 1) / kSharing, p.hkv, (p.table_width + kPages - 1) / kPages);
+      const dim3 grid((w.rows + kRowTile - 1) / kRowTile, p.hkv, (p.table_width + kPages - 1) / kPages);
       e = launch_early(score_kernel<T, D>, grid, kBlock, 0, stream, w);
       if (e != cudaSuccess) return e;
     }
-    e = launch_early(pick, dim3(w.rows, p.hkv), kBlock, smem(w.width), stream, w);
+    e = launch_early(pick, dim3(w.rows, p.hkv), kFewThreads, smem(w.width), stream, w);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -799,7 +929,7 @@ extern "C" int moe_select_pages(const moe_kv_cache *cache, const moe_attention *
   w.n_select = n_select;
   w.sink = sink;
   w.recent = recent;
-  w.error = (w.p.group + 12) * 6e-8f;
+  w.error = (w.p.group + 12) * 6e-8f;  // group roundings of Q, 10 of a score (Block), one way after the other
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == MOE_DTYPE_BF16)

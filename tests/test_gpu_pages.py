@@ -211,3 +211,35 @@ def test_captured():
     want = S.bounds(b, before)
     assert torch.equal(bnd, want)
     assert torch.equal(out.cpu(), S.select(b, want, 6, 1, 1))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_for_chunks_of_odd_kinds(dtype, D):
+    """Rows in tiles of 16 that two sequences share: large, tiny, zero and tied ones side by side."""
+    b = C.batch(15 + D, [21, 9, 40], [16 * 150, 16 * 90 + 3, 16 * 300], 12, 2, D, 16, dtype)
+    bnd = random_bounds(b, 15)
+    bnd[b.table[2, 40:200].long()] = bnd[b.table[2, 40:41].long()]  # pages alike
+    b.q[3] *= 2.0 ** 12
+    b.q[4] *= 2.0 ** -14
+    b.q[5] = 0.0
+    b.q[22:25] = b.q[22]
+    for n_select in (5, 60):
+        got, err = run_select(b, bnd, n_select, 1, 2)
+        assert err == 0 and torch.equal(got, S.select(b, bnd, n_select, 1, 2))
+    if dtype == BF16:
+        b.q[6] *= 2.0 ** 120  # sums and scores beyond fp32
+        got, err = run_select(b, bnd, 9, 1, 2)
+        assert err == 0 and torch.equal(got, S.select(b, bnd, 9, 1, 2))
+
+
+def test_select_beyond_fp32_for_chunks():
+    b = C.batch(16, [8], [16 * 900], 2, 1, 64, 16, BF16)
+    b.q[:] = torch.tensor([1.0, -1.0], device="cuda")[None, :, None].to(BF16) * 2.0 ** -6
+    b.q[:, :, 0] = 1024.0
+    gen = torch.Generator().manual_seed(9)
+    bnd = torch.randint(-3, 4, shape(b), generator=gen).sort(2).values.to(BF16).cuda() / 16
+    bnd[..., 0] = 512.0
+    for n_select in (12, 500):
+        got, err = run_select(b, bnd, n_select)
+        assert err == 0 and torch.equal(got, S.select(b, bnd, n_select, 1, 1))
