@@ -5,17 +5,23 @@
 
 namespace attn {
 
-// Up to which a sequence's positions may go.
-constexpr int64_t kShortPositions = 4096;
+// Up to which a sequence's positions may go, for clusters of 8.  (us by clusters and by the tiles, with a table
+// that could hold more.  32 query, 8 key/value heads of 128, 2 tokens behind 600, 4000, 8000 and 14000 positions,
+// clusters of 8: 7.8, 18.0; 14.2, 22.2; 22.1, 26.5; 33.7, 28.7.  Drafts of 8: 11.2, 18.3; 19.1, 22.4; 29.0, 25.0.  2
+// key/value heads, clusters of 16: 7.1, 16.9; 10.3, 22.3; 13.3, 26.7; 18.0, 31.4.)
+constexpr int64_t kFewRows = 8192, kMoreRows = 4096;
 
 int takes_prefix_clusters(const moe_kv_cache *c, const Params &p, bool *takes) {
   const int64_t positions = static_cast<int64_t>(p.table_width) << p.page_shift;
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.group;
   *takes = false;
-  if (rows > 32 || positions > kShortPositions) return MOE_OK;
+  if (rows > 32) return MOE_OK;
   Plan plan;
   const int rc = make_plan(c, p, p.n_seqs, p.n_rows, rows, positions, &plan);
-  *takes = rc == MOE_OK && plan.cluster > 0;
+  // (304 CTAs in clusters of 8 are not all resident at once: 38 drafts of 4 behind 4000 positions, one key/value
+  // head: 33.7 us, 25.3 on the tiles; 256 are)
+  *takes = rc == MOE_OK && plan.cluster > 0 && 4 * static_cast<int64_t>(plan.grid) <= 7 * plan.sms &&
+           (plan.cluster == 16 || positions <= (rows <= 16 ? kFewRows : kMoreRows));
   return rc;
 }
 

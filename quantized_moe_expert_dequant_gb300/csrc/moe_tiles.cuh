@@ -103,6 +103,7 @@ constexpr int kItemCost = 224;
 // together) what K and V take from memory.
 // (us, heads of 128: a step of both tiles 1.75 to 2, of one 1.0 to 1.1, an item 1; heads of 64: 1.6, 0.83, 1.3.)
 constexpr int kBothTiles = 3, kOneTile = 2;
+constexpr float kStepCost = 2.5f * kPos;
 __device__ constexpr int shared_item_cost(int dim) { return dim == 64 ? 192 : 128; }
 constexpr int kMinSteps = 2;
 // Steps of the longest item that the table allows, from which items are shared at all: below, a boundary
@@ -266,8 +267,17 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int it
     total += block_scan(mine, s_warp, &below);
   }
   if (total == 0) return false;
-  const int64_t edge[2] = {quotient(blockIdx.x * total, gridDim.x),
-                           quotient((blockIdx.x + 1) * total, gridDim.x)};
+  unsigned ctas = gridDim.x;
+  if constexpr (MODE == kShared) {
+    // A CTA's time grows with its steps, that of combine_kernel with an item's parts, 0.4 us each: with n steps an
+    // item the shortest is near sqrt(n) / 2 steps a CTA.  (2 key/value heads of 128, two tokens behind 7168 and 13248
+    // positions: 43.9, 52.1 us on all CTAs, 26.7, 31.4 so.)
+    const float steps = static_cast<float>(total) / (kStepCost * static_cast<float>(parts) * p.hkv);
+    const float least = kStepCost * fmaxf(1.f, 0.5f * sqrtf(steps));
+    ctas = max(1u, min(ctas, static_cast<unsigned>(static_cast<float>(total) / least)));
+    if (blockIdx.x >= ctas) return false;
+  }
+  const int64_t edge[2] = {quotient(blockIdx.x * total, ctas), quotient((blockIdx.x + 1) * total, ctas)};
   if (threadIdx.x == 0 && edge[1] == total) s_spot[1] = {parts, 0, 0, 0};
   int64_t sum = 0;
   for (int b = 0; b < parts; b += kPromptThreads) {
@@ -1202,7 +1212,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int to
 // kShared: joins what the items over the prefix and over the rest have left of a token's rows, one block a
 // token and key/value head.  Two warps list the parts; then eight lanes take 64 columns of a row, and four times
 // eight every fourth part.  Parts are in the order of the positions.  (Short, since code that runs once is bound by
-// fetching it: a walk over the parts in each thread took 4 to 10 us, TODO so.)
+// fetching it: a walk over the parts in each thread took 5 to 10 us for 512 blocks, 3 to 5 so.)
 constexpr int kCombineThreads = 256;  // at most; two warps at least
 
 template <typename T, int D>

@@ -158,8 +158,8 @@ __device__ __forceinline__ void load_tile(const Params &p, int len, const int (&
 }
 
 // Listed pages.  Each warp copies every fourth run of 16 positions of a tile, so that a thread looks up one
-// or two pages a tile and steps through their positions (all threads looking up all pages of a tile: one
-// token's chunk of 512 rows over 100 pages of 16 108 us, so TODO).
+// or two pages a tile and steps through their positions.  (All threads looking up all pages of a tile: a chunk of
+// 512 rows over 100 pages of 16, heads of 64, 108 us; 62 so.)
 template <int TILE>
 struct Listed {
   static constexpr int kRuns = TILE / 64;  // of a warp
@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Work w) {
 }
 
 struct Plan {
+  int sms;
   int grid, rows;  // CTAs, rows of a tile
   int cluster;     // CTAs of an item's cluster; 0: all CTAs share all items
   int64_t part, ml, shared, bytes;  // offsets in the workspace
@@ -729,6 +730,7 @@ inline int make_plan(const moe_kv_cache *c, const Params &p, int64_t n, int64_t 
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MOE_ERR_CUDA;
+  plan->sms = sms;
   plan->rows = rows <= 16 ? 16 : 32;
   // With few items a cluster takes each, when the 16 or 8 CTAs of every one can be resident at once: one
   // kernel instead of two.  (32 query, 8 key/value heads of 128, one token, shared line against clusters

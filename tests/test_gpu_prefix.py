@@ -194,14 +194,14 @@ def test_few_sequences_in_both_forms(dtype, Hq, Hkv, D, page):
     masks = tree_masks(5, lens)
     ref, tol = G.b.reference(0.1, masks)
     C.assert_within(G.run(2, masks, 0.1), ref, tol)
-    wide = torch.full((7, 9000 // page), -4, dtype=torch.int32, device="cuda")
+    wide = torch.full((7, 20000 // page), -4, dtype=torch.int32, device="cuda")
     wide[:, :G.hidden.shape[1]] = G.hidden
     C.assert_within(G.run(2, masks, 0.1, table=wide), ref, tol)
 
 
 def test_waits_that_give_up():
     """With a limit that its waits run into, the call ends with the time-out bit and the next is right."""
-    G = Groups(12, [0, 8], [6000], [1] * 8, [100] * 8, 8, 2, 128, 64, BF16)  # (on the tiles)
+    G = Groups(12, [0, 8], [6000], [1] * 8, [100] * 8, 8, 2, 128, 64, BF16)
     b = G.b
     ref, tol = b.reference(128 ** -0.5)
     cache = Bn.KvCache(b.k, b.v)
@@ -210,7 +210,8 @@ def test_waits_that_give_up():
 
     def call():
         err = torch.zeros(1, **i32)
-        out = Bn.prefix_attention(cache, b.q, b.cu, b.ctx, G.hidden, cu, prefix, 1, device_error=err)
+        out = Bn.prefix_attention(cache, b.q, b.cu, b.ctx, G.hidden, cu, prefix, 16,
+                                  device_error=err)  # (room for 64 rows: on the tiles)
         torch.cuda.synchronize()
         return out, int(err)
 
