@@ -596,6 +596,7 @@ class KvCache:
         self._dev = k.get_device()
         self._heads = (self.n_kv_heads, self.head_dim)
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self._bounds = torch.Size((self.n_pages, self.n_kv_heads, 2, self.head_dim))
         self._shape = (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, _DTYPES[k.dtype])
         self._c = _pack_kv_cache(k.data_ptr(), v.data_ptr(), *st, self.n_pages, self.page_size,
                                  self.n_kv_heads, self.head_dim, _DTYPES[k.dtype])
@@ -697,16 +698,33 @@ def _workspace_bytes(fn: str, dev: int, shape, n: int, width: int, T: int, Hq: i
     return size.value
 
 
-def _scratch(fn: str, cache, workspace, stream, page_table, shape, *more):
-    """(address, bytes, tensor) of the caller's workspace, or of a new one for a batch of q's shape."""
-    if workspace is None:
-        n = _workspace_bytes(fn, cache._dev, cache._shape, *page_table.shape, shape[0], shape[1], *more)
-        if n == 0:
-            return 0, 0, None
-        workspace = _empty_on(n, torch.uint8, cache.device, stream)
-        return workspace.data_ptr(), n, workspace
-    n = workspace.numel()
-    return _vector(workspace, torch.uint8, n, cache._dev, "workspace"), n, workspace
+def _run(fn: str, cache, stream, workspace, page_table, shape, more, *args) -> None:
+    """fn(cache, *args, workspace, its bytes, stream) for a batch of q's shape; `more`: what else its workspace goes
+    by.  Without the caller's workspace, memory of torch's allocator, given back behind the call in the order of
+    its stream as a tensor's is that goes out of scope (making a tensor takes longer than the launches)."""
+    dev = cache._dev
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if workspace is not None:
+        n = workspace.numel()
+        _on(dev, fn, cache._c, *args, _vector(workspace, torch.uint8, n, dev, "workspace"), n, stream)
+        return
+    n = _workspace_bytes(fn + "_workspace", dev, cache._shape, *page_table.shape, shape[0], shape[1],
+                         *more)
+    if n == 0:
+        _on(dev, fn, cache._c, *args, 0, 0, stream)
+        return
+    if torch._C._cuda_getDevice() == dev:
+        ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, int(stream))
+    try:
+        _on(dev, fn, cache._c, *args, ptr, n, stream)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ptr)
 
 
 def _workspace(fn: str, cache, workspace, stream, *args):
@@ -775,19 +793,17 @@ def prefix_attention(cache: KvCache, q, cu_q, ctx_len, page_table, cu_group, pre
     dev, groups = cache._dev, prefix_len.numel()
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
-    mask = _tree_mask(tree_mask, q.shape[0], dev)
-    ws = _scratch("moe_prefix_attention_workspace", cache, workspace, stream, page_table, q.shape, groups,
-                  max_q)
-    _call("moe_prefix_attention", dev, stream, cache._c, args,
-          _vector(cu_group, torch.int32, groups + 1, dev, "cu_group"),
-          _vector(prefix_len, torch.int32, groups, dev, "prefix_len"), groups, mask, max_q, *ws[:2])
+    shape = q.shape
+    _run("moe_prefix_attention", cache, stream, workspace, page_table, shape, (groups, max_q), args,
+         _vector(cu_group, torch.int32, groups + 1, dev, "cu_group"),
+         _vector(prefix_len, torch.int32, groups, dev, "prefix_len"), groups,
+         _tree_mask(tree_mask, shape[0], dev), max_q)
     return out
 
 
 def _bounds(cache, bounds) -> int:
-    shape = (cache.n_pages, cache.n_kv_heads, 2, cache.head_dim)
-    if bounds.shape != shape:
-        raise ValueError(f"bounds: {shape} is wanted, not {tuple(bounds.shape)}")
+    if bounds.shape != cache._bounds:
+        raise ValueError(f"bounds: {tuple(cache._bounds)} is wanted, not {tuple(bounds.shape)}")
     return _vector(bounds, cache.dtype, 0, cache._dev, "bounds")
 
 
@@ -822,9 +838,8 @@ def select_pages(cache: KvCache, bounds, q, cu_q, ctx_len, page_table, n_select:
         to = _vector(out, torch.int32, 0, dev, "out")
     args = _batch_args(cache, _rows(q, shape, cache.dtype, dev, "q"), _NONE, T, Hq, 0.0, cu_q, ctx_len,
                        page_table, device_error)
-    ws = _scratch("moe_select_pages_workspace", cache, workspace, stream, page_table, shape)
-    _call("moe_select_pages", dev, stream, cache._c, args, _bounds(cache, bounds), n_select, sink,
-          recent, to, *ws[:2])
+    _run("moe_select_pages", cache, stream, workspace, page_table, shape, (), args,
+         _bounds(cache, bounds), n_select, sink, recent, to)
     return out
 
 
@@ -839,7 +854,6 @@ def sparse_attention(cache: KvCache, q, cu_q, ctx_len, page_table, pages,
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     n = pages.shape[2]
-    ws = _scratch("moe_sparse_attention_workspace", cache, workspace, stream, page_table, q.shape, n)
-    _call("moe_sparse_attention", cache._dev, stream, cache._c, args,
-          _vector(pages, torch.int32, pages.numel(), cache._dev, "pages"), n, *ws[:2])
+    _run("moe_sparse_attention", cache, stream, workspace, page_table, q.shape, (n,), args,
+         _vector(pages, torch.int32, 0, cache._dev, "pages"), n)
     return out

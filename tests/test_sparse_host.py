@@ -3,6 +3,7 @@ anything is enqueued (or has nothing to enqueue), so that the addresses are neve
 import ctypes
 
 import pytest
+import torch
 
 from quantized_moe_expert_dequant_gb300 import binding as Bn
 from tests.test_attention_host import BAD_CACHE, INV, L, UNS, attention, cache  # noqa: F401
@@ -120,3 +121,88 @@ def test_bounds_go_without_queries(L):
     assert L.moe_page_bounds(ref(cache()), ref(a), None, None) == INV
     a.n_rows = 0
     assert L.moe_page_bounds(ref(cache()), ref(a), 0x8000, None) == Bn.MOE_OK
+
+
+@pytest.mark.parametrize("kind", ["prefix", "select", "sparse", "bounds"])
+def test_every_call_is_made_with_the_caches_gpu_current(monkeypatch, kind):
+    """What a call asks, allocates and launches goes by the cache's GPU.  (No GPU here: the library, the current
+    device, the allocator and the tensors' place are stand-ins.)"""
+    now, calls, held = [0], [], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.dev
+
+        def __exit__(self, *e):
+            now[0] = self.before
+
+    class OnGpu1(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def entry(fn):
+        def call(*args):
+            calls.append((fn, now[0]))
+            if fn.endswith("_workspace"):
+                args[-1]._obj.value = 64
+            return Bn.MOE_OK
+        return call
+
+    def alloc(n, stream):
+        held.append(n)
+        calls.append((n, now[0]))
+        return 4096
+
+    monkeypatch.setattr(Bn, "_entry", entry)
+    for name, f in (("_cuda_getDevice", lambda: now[0]), ("_cuda_getCurrentRawStream", lambda dev: 0),
+                    ("_cuda_cudaCachingAllocator_raw_alloc", alloc),
+                    ("_cuda_cudaCachingAllocator_raw_delete", lambda p: held.pop())):
+        monkeypatch.setattr(torch._C, name, f, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    Bn._workspace_bytes.cache_clear()
+    t = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype).as_subclass(OnGpu1)
+    bf16 = torch.bfloat16
+    c = type("Cache", (), dict(_dev=1, head_dim=64, n_pages=3, n_kv_heads=8, page_size=16, dtype=bf16, _c=b"",
+                               device="cpu", _shape=(3, 8, 16, 64, 0), _bounds=(3, 8, 2, 64)))()
+    q, batch = t(1, 8, 64, dtype=bf16), (t(2), t(1), t(1, 4))
+    bounds = t(3, 8, 2, 64, dtype=bf16)
+    if kind == "prefix":
+        Bn.prefix_attention(c, q, *batch, t(2), t(1), max_q=1, out=t(1, 8, 64, dtype=bf16))
+    elif kind == "select":
+        Bn.select_pages(c, bounds, q, *batch, n_select=4, out=t(1, 8, 4))
+    elif kind == "sparse":
+        Bn.sparse_attention(c, q, *batch, t(1, 8, 4), out=t(1, 8, 64, dtype=bf16))
+    else:
+        Bn.page_bounds(c, bounds, *batch, n_rows=1)
+    name = {"prefix": "moe_prefix_attention", "select": "moe_select_pages",
+            "sparse": "moe_sparse_attention", "bounds": "moe_page_bounds"}[kind]
+    asked = [] if kind == "bounds" else [(name + "_workspace", 1), (64, 1)]
+    assert calls == asked + [(name, 1)] and now == [0] and held == []
+    Bn._workspace_bytes.cache_clear()
+
+
+def test_the_binding_checks_shapes():
+    t = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype)
+    bf16 = torch.bfloat16
+    c = type("Cache", (), dict(_dev=-1, head_dim=64, n_pages=3, n_kv_heads=2, page_size=16, dtype=bf16, _c=b"",
+                               device="cpu", _shape=(3, 2, 16, 64, 0), _bounds=(3, 2, 2, 64)))()
+    q, batch, bounds = t(1, 4, 64, dtype=bf16), (t(2), t(1), t(1, 4)), t(3, 2, 2, 64, dtype=bf16)
+    for f in (lambda: Bn.page_bounds(c, t(3, 2, 64, dtype=bf16), *batch, n_rows=1),
+              lambda: Bn.page_bounds(c, bounds.half(), *batch, n_rows=1),
+              lambda: Bn.page_bounds(c, bounds, t(1), *batch[1:], n_rows=1),
+              lambda: Bn.page_bounds(c, bounds, batch[0].long(), *batch[1:], n_rows=1),
+              lambda: Bn.select_pages(c, bounds, t(1, 4, 32, dtype=bf16), *batch, n_select=4),
+              lambda: Bn.select_pages(c, bounds, q.half(), *batch, n_select=4),
+              lambda: Bn.select_pages(c, bounds, q, *batch, n_select=4, out=t(1, 2, 5)),
+              lambda: Bn.select_pages(c, bounds[:2], q, *batch, n_select=4, out=t(1, 2, 4)),
+              lambda: Bn.sparse_attention(c, q, *batch, t(1, 3, 4)),
+              lambda: Bn.sparse_attention(c, q, *batch, t(1, 8)),
+              lambda: Bn.sparse_attention(c, q, *batch, t(1, 2, 4).long()),
+              lambda: Bn.prefix_attention(c, q, *batch, t(1), t(1), max_q=1),
+              lambda: Bn.prefix_attention(c, q, *batch, t(2), t(1).long(), max_q=1),
+              lambda: Bn.prefix_attention(c, q, *batch, t(2), t(1), max_q=1, tree_mask=t(1))):
+        with pytest.raises(ValueError):
+            f()
