@@ -101,10 +101,11 @@ struct PromptParams {
 constexpr int kItemCost = 224;
 // kShared: a step of both tiles takes as long as the products, one of a tile by itself (of two that are taken
 // together) what K and V take from memory.
-// (us, heads of 128: a step of both tiles 1.75 to 2, of one 1.0 to 1.1, an item 1; heads of 64: 1.6, 0.83, 1.3.)
-constexpr int kBothTiles = 3, kOneTile = 2;
-constexpr float kStepCost = 2.5f * kPos;
-__device__ constexpr int shared_item_cost(int dim) { return dim == 64 ? 192 : 128; }
+// (us, heads of 128: a step of both tiles 1.5 to 2.1, of one 1.0 to 1.2, an item 0.8; heads of 64: 1.6 to 1.9, 0.9,
+// 1.4.)
+constexpr int kBothTiles = 8, kOneTile = 5;
+constexpr float kStepCost = 6.5f * kPos;
+__device__ constexpr int shared_item_cost(int dim) { return dim == 64 ? 192 : 96; }
 constexpr int kMinSteps = 2;
 // Steps of the longest item that the table allows, from which items are shared at all: below, a boundary
 // moves to the nearer edge of its item, and no parts are joined.  (32 query, 8 key/value heads of 128,
@@ -172,13 +173,17 @@ struct Share {
   int row0, nq, kvh, tok0;
 };
 
+__device__ __forceinline__ int64_t shared_length(const Seq &s) {  // of kShared's items: whole steps
+  return (s.len + static_cast<int64_t>(kPos) - 1) & -kPos;
+}
+
 // Cost of the first k of a head's `tiles` items; per tokens an item.
 template <int MODE>
 __device__ __forceinline__ int64_t head_cost(const Seq &s, int per, int tiles, int k, int item_cost) {
   if (MODE == kShared) {  // a last item of one tile
     const bool one = k == tiles && 2 * (s.nq - (tiles - 1) * per) <= per;
     return (k * kBothTiles - (one ? kBothTiles - kOneTile : 0)) *
-           static_cast<int64_t>(s.len + item_cost);
+           (shared_length(s) + item_cost);
   }
   if (MODE == kTree) return static_cast<int64_t>(k) * (s.len + kItemCost);
   const int64_t full = k < tiles ? k : k - 1;
@@ -206,7 +211,7 @@ __device__ __forceinline__ Spot spot_at(const Seq &s, bool shared, int seq, int 
   y -= r.head * whole;
   // k (ctx + kItemCost) + per k (k + 1) / 2 = y, then the exact k next to it
   const float b = s.ctx + kItemCost + 0.5f * per;
-  int k = MODE == kShared ? static_cast<int>(quotient(y, kBothTiles * static_cast<int64_t>(s.len + item_cost)))
+  int k = MODE == kShared ? static_cast<int>(quotient(y, kBothTiles * (shared_length(s) + item_cost)))
           : MODE == kTree ? static_cast<int>(quotient(y, s.len + kItemCost))
                           : static_cast<int>((sqrtf(b * b + 2.f * per * static_cast<float>(y)) - b) / per);
   k = max(0, min(k, tiles - 1));
@@ -249,7 +254,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 // The CTA's part of the line: from s_spot[0] to s_spot[1].  False when there is nothing at all.
 template <int MODE>
 __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int item_cost,
-                                          int64_t *s_warp, Spot *s_spot, Part *s_first) {
+                                          int64_t *s_warp, Spot *s_spot, Part *s_first, int *s_period) {
   const Params &p = w.p;
   const bool shared = w.split;
   const int parts = part_count<MODE>(w);
@@ -276,6 +281,8 @@ __device__ __forceinline__ bool find_part(const PromptParams &w, int per, int it
     const float least = kStepCost * fmaxf(1.f, 0.5f * sqrtf(steps));
     ctas = max(1u, min(ctas, static_cast<unsigned>(static_cast<float>(total) / least)));
     if (blockIdx.x >= ctas) return false;
+    if (threadIdx.x == 0)
+      *s_period = max(1, static_cast<int>(quotient(total, static_cast<int64_t>(ctas) * kBothTiles * kPos)));
   }
   const int64_t edge[2] = {quotient(blockIdx.x * total, ctas), quotient((blockIdx.x + 1) * total, ctas)};
   if (threadIdx.x == 0 && edge[1] == total) s_spot[1] = {parts, 0, 0, 0};
@@ -309,6 +316,11 @@ constexpr int kTwo = 1, kHalves = 2;
 constexpr int kHalfSteps = 16;
 
 struct alignas(16) Item {
+  // kShared: the piece's first steps are processed last, more - 1 of them (Walk::next).
+  __device__ __forceinline__ int step(int t) const {
+    const int n = max(count[0], count[1]), at = t + more - 1;
+    return a + (at < n ? at : at - n);
+  }
   int more, seq, kvh, row0, ctx, nq, len, tok0, a, count[2], steps, whole, page0, rest, pair;
 };
 static_assert(sizeof(Item) == 64, "read as four 16-byte words");
@@ -319,12 +331,14 @@ struct Walk {
   static constexpr bool tree = MODE != kCausal;
   const PromptParams &w;
   const int tokens, per, parts;
+  const int period;  // kShared: steps of a CTA
   Spot at, end;
   Part s;
   int tiles;
 
-  __device__ __forceinline__ Walk(const PromptParams &w, const Spot *spot, const Part &first)
-      : w(w), tokens(w.tokens), per(2 * tokens), parts(part_count<MODE>(w)), at(spot[0]), end(spot[1]) {
+  __device__ __forceinline__ Walk(const PromptParams &w, const Spot *spot, const Part &first, int period)
+      : w(w), tokens(w.tokens), per(2 * tokens), parts(part_count<MODE>(w)), period(period), at(spot[0]),
+        end(spot[1]) {
     s = MODE == kShared ? first : load_part<MODE>(w, min(at.seq, parts - 1), false);
     tiles = item_count(s, per);
   }
@@ -354,6 +368,13 @@ struct Walk {
     r.count[0] = max(0, min(b, n0) - r.a);
     r.count[1] = r.tok0 + tokens < s.nq ? b - r.a : 0;
     r.steps = max(r.count[0], r.count[1]);
+    // The items of a head read the same K and V.  Their pieces do not begin at the same steps, but are as long:
+    // each begins with a multiple of that length and goes around, so that all are at the same step at a time and
+    // memory is read once for them.  (32 drafts of 8 behind 65536 positions, 4 items a head: 260 us, 240 so.)
+    if (MODE == kShared && r.rest == 0 && r.count[1] > 0) {
+      const int from = (r.a + period - 1) / period * period;
+      if (from < b) r.more = 1 + from - r.a;
+    }
     at.step = 0;
     ++at.tile;
     return r;
@@ -459,6 +480,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ int64_t s_warp[kPromptThreads / 32];
   __shared__ Spot s_spot[2];
   __shared__ Part s_first;
+  __shared__ int s_period;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gone;
   const Params &p = w.p;
@@ -492,7 +514,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else {
     pdl_launch();
   }
-  const bool any = find_part<MODE>(w, 2 * w.tokens, shared_item_cost(D), s_warp, s_spot, &s_first);
+  const bool any = find_part<MODE>(w, 2 * w.tokens, shared_item_cost(D), s_warp, s_spot, &s_first, &s_period);
   if (w.share && threadIdx.x == 0) {
     Share sh = {};
     if (any && before(s_spot[0], s_spot[1])) {
@@ -536,7 +558,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == kSoftmaxWarps + 2) {
     // ---------------------------------------------------------------- items, ahead of the others
     if (lane == 0) {
-      Walk<MODE> walk(w, s_spot, s_first);
+      Walk<MODE> walk(w, s_spot, s_first, MODE == kShared ? s_period : 0);
       Item ahead, other;  // kShared: the item that was not taken with the one before it; tile 1's
       bool held = false;
       for (int it = 0;; ++it) {
@@ -651,14 +673,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int pos = t * kPos + b_row;
         return lane < boxes && pos < item.len ? pages[pos >> p.page_shift] : p.n_pages;
       };
-      int page = page_of(item.a);
-      for (int t = item.a; ok && t < item.a + item.steps; ++t) {
-        const int pos = t * kPos + b_row;
+      const auto step = [&](int i) { return MODE == kShared ? item.step(i) : item.a + i; };
+      int page = page_of(step(0));
+      for (int i = 0; ok && i < item.steps; ++i) {
+        const int t = step(i), pos = t * kPos + b_row;
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
           if (lane < boxes && pos < item.len && p.err) atomicOr(p.err, kDevErrBadId);
           page = p.n_pages;  // outside the cache: reads zeros
         }
-        const int next_page = page_of(t + 1);  // on its way while this step waits for the ring
+        // on its way while this step waits for the ring
+        const int next_page = page_of(MODE == kShared && i + 1 < item.steps ? step(i + 1) : t + 1);
         const int in_page = pos & ((1 << p.page_shift) - 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -672,20 +696,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tc::copy_4d(ring + st * C::kTileBytes + half * kPos * 128 + b_row * 128,
                         kv ? &w.v : &w.k, 64 * half, in_page, item.kvh, page, bar(s_full[st]));
           ++issued;
-          if (kv == 1 || t > item.a) continue;
+          if (kv == 1 || i > 0) continue;
           // Q between the first K and the first V: its place is free only shortly before
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (item.count[i] == 0) continue;
-            ok = ok && free(bar(s_q_free[i]), (q_loads[i] & 1) ^ 1);
+          for (int j = 0; j < 2; ++j) {
+            if (item.count[j] == 0) continue;
+            ok = ok && free(bar(s_q_free[j]), (q_loads[j] & 1) ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && lane == 0) {
-              tc::bar_expect(bar(s_q[i]), static_cast<uint32_t>(w.tokens * p.group * D * 2));
+              tc::bar_expect(bar(s_q[j]), static_cast<uint32_t>(w.tokens * p.group * D * 2));
               for (int h = 0; h < D / 64; ++h)
-                tc::copy_3d(base + i * C::kTileBytes + h * kPos * 128, &w.q, 64 * h,
-                            item.kvh * p.group, item.row0 + item.tok0 + i * w.tokens, bar(s_q[i]));
+                tc::copy_3d(base + j * C::kTileBytes + h * kPos * 128, &w.q, 64 * h,
+                            item.kvh * p.group, item.row0 + item.tok0 + j * w.tokens, bar(s_q[j]));
             }
-            if (ok) ++q_loads[i];
+            if (ok) ++q_loads[j];
           }
         }
         page = next_page;
@@ -826,9 +850,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int t = 0; t < last; ++t) {
         const int v_st = st;
         const uint32_t v = stage(v_st);
-        if (valid - t * kPos < kPos) {
+        const int left = MODE == kShared ? valid - uniform(item.step(t) - item.a) * kPos : valid - t * kPos;
+        if (left < kPos) {
           // positions behind the sequence have weight 0, but what their page holds may be NaN
-          for (int x = (valid - t * kPos) * 128 + lane * 16; x < kPos * 128; x += 512)
+          for (int x = left * 128 + lane * 16; x < kPos * 128; x += 512)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
               asm volatile(
@@ -960,7 +985,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
           if (lane == 0) tc::bar_arrive(bar(s_x[i]));
         }
-        const int pos0 = (item.a + t) * kPos;
+        const int pos0 = (MODE == kShared && !item.pair ? item.step(t) : item.a + t) * kPos;
         if (tree) {
           if (pos0 + kPos > item.ctx) {  // drafted positions, and those behind the sequence
 #pragma unroll
