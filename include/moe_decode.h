@@ -414,7 +414,8 @@ int moe_prompt_attention(const moe_kv_cache *cache, const moe_attention *args, v
  * device).  Those are read once for the group, from the pages that its first sequence's row of the page table
  * names; the others' rows are not read there.  Whole pages are shared: positions on the page that a
  * prefix ends in are each sequence's own.  A sequence with fewer than prefix_len[g] positions before its
- * queries is computed by itself.  out as by moe_tree_attention up to rounding.  workspace as for
+ * queries is computed by itself.  Offsets of cu_q that are out of range at a group's ends may refuse all
+ * of its sequences.  out as by moe_tree_attention up to rounding.  workspace as for
  * moe_tree_attention, of moe_prefix_attention_workspace bytes. */
 int moe_prefix_attention_workspace(const moe_kv_cache *cache, const moe_attention *args,
                                    int32_t n_groups, int32_t max_q, int64_t *bytes);
