@@ -596,6 +596,7 @@ class KvCache:
         self._dev = k.get_device()
         self._heads = (self.n_kv_heads, self.head_dim)
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self._sizes = {}  # of workspaces, by what they go by
         self._bounds = torch.Size((self.n_pages, self.n_kv_heads, 2, self.head_dim))
         self._shape = (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, _DTYPES[k.dtype])
         self._c = _pack_kv_cache(k.data_ptr(), v.data_ptr(), *st, self.n_pages, self.page_size,
@@ -654,7 +655,7 @@ def _batch_args(cache, a, b, T, Hq, scale, cu_q, ctx_len, page_table, device_err
     dev, i32 = cache._dev, torch.int32
     n, width = page_table.shape
     st = page_table.stride()
-    if page_table.dtype != i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
+    if page_table.dtype is not i32 or page_table.get_device() != dev or (st[1] != 1 and width > 1):
         raise ValueError(f"page_table: int32 [n_seqs, width] on cuda:{dev} is wanted")
     # the checks of _vector in one expression for the calls that pass them: on small batches the host is
     # what takes time
@@ -686,35 +687,41 @@ def _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_erro
                        page_table, device_error), out
 
 
-@functools.lru_cache(maxsize=4096)
-def _workspace_bytes(fn: str, dev: int, shape, n: int, width: int, T: int, Hq: int, *more) -> int:
-    """What fn answers for a cache of shape (pages, heads, positions of a page, head_dim, dtype) and a batch of
-    n sequences, T rows and Hq query heads: it goes by nothing else, and no address is read."""
-    n_pages, kv_heads, page, dim, dtype = shape
+def _workspace_bytes(fn: str, cache, table, shape, more) -> int:
+    """What fn answers for a page table and queries of these shapes: it goes by nothing else, and no address is
+    read.  The cache keeps the answers."""
+    n_pages, kv_heads, page, dim, dtype = cache._shape
     c = _pack_kv_cache(16, 16, 0, 0, 0, n_pages, page, kv_heads, dim, dtype)
-    a = _pack_attention(16, 16, 0, 0, 0, 0, 16, 16, 16, width, width, n, T, Hq, 1.0, 0)
+    a = _pack_attention(16, 16, 0, 0, 0, 0, 16, 16, 16, table[1], table[1], table[0], shape[0], shape[1],
+                        1.0, 0)
     size = ctypes.c_int64()
-    _on(dev, fn, c, a, *more, ctypes.byref(size))
+    _on(cache._dev, fn + "_workspace", c, a, *more, ctypes.byref(size))
+    if len(cache._sizes) >= 4096:
+        cache._sizes.clear()
+    cache._sizes[fn, table, shape, more] = size.value
     return size.value
 
 
-def _run(fn: str, cache, stream, workspace, page_table, shape, more, *args) -> None:
-    """fn(cache, *args, workspace, its bytes, stream) for a batch of q's shape; `more`: what else its workspace goes
-    by.  Without the caller's workspace, memory of torch's allocator, given back behind the call in the order of
-    its stream as a tensor's is that goes out of scope (making a tensor takes longer than the launches)."""
+def _run(fn: str, cache, stream, workspace, table, shape, more, *args) -> None:
+    """fn(cache, *args, workspace, its bytes, stream) for a page table and queries of these shapes; `more`: what else
+    its workspace goes by.  Without the caller's workspace, memory of torch's allocator, given back behind the
+    call in the order of its stream as a tensor's is that goes out of scope (making a tensor takes as long as a
+    launch)."""
     dev = cache._dev
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if workspace is not None:
+    ptr = 0
+    if workspace is None:
+        n = cache._sizes.get((fn, table, shape, more))
+        if n is None:
+            n = _workspace_bytes(fn, cache, table, shape, more)
+    else:
         n = workspace.numel()
-        _on(dev, fn, cache._c, *args, _vector(workspace, torch.uint8, n, dev, "workspace"), n, stream)
-        return
-    n = _workspace_bytes(fn + "_workspace", dev, cache._shape, *page_table.shape, shape[0], shape[1],
-                         *more)
-    if n == 0:
-        _on(dev, fn, cache._c, *args, 0, 0, stream)
+        ptr = _vector(workspace, torch.uint8, n, dev, "workspace")
+    if n == 0 or ptr:
+        _on(dev, fn, cache._c, *args, ptr, n, stream)
         return
     if torch._C._cuda_getDevice() == dev:
         ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, int(stream))
@@ -794,7 +801,7 @@ def prefix_attention(cache: KvCache, q, cu_q, ctx_len, page_table, cu_group, pre
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     shape = q.shape
-    _run("moe_prefix_attention", cache, stream, workspace, page_table, shape, (groups, max_q), args,
+    _run("moe_prefix_attention", cache, stream, workspace, page_table.shape, shape, (groups, max_q), args,
          _vector(cu_group, torch.int32, groups + 1, dev, "cu_group"),
          _vector(prefix_len, torch.int32, groups, dev, "prefix_len"), groups,
          _tree_mask(tree_mask, shape[0], dev), max_q)
@@ -838,7 +845,7 @@ def select_pages(cache: KvCache, bounds, q, cu_q, ctx_len, page_table, n_select:
         to = _vector(out, torch.int32, 0, dev, "out")
     args = _batch_args(cache, _rows(q, shape, cache.dtype, dev, "q"), _NONE, T, Hq, 0.0, cu_q, ctx_len,
                        page_table, device_error)
-    _run("moe_select_pages", cache, stream, workspace, page_table, shape, (), args,
+    _run("moe_select_pages", cache, stream, workspace, page_table.shape, shape, (), args,
          _bounds(cache, bounds), n_select, sink, recent, to)
     return out
 
@@ -854,6 +861,6 @@ def sparse_attention(cache: KvCache, q, cu_q, ctx_len, page_table, pages,
     args, out = _attention_args(cache, q, cu_q, ctx_len, page_table, scale, out, device_error,
                                 stream)
     n = pages.shape[2]
-    _run("moe_sparse_attention", cache, stream, workspace, page_table, q.shape, (n,), args,
+    _run("moe_sparse_attention", cache, stream, workspace, page_table.shape, q.shape, (n,), args,
          _vector(pages, torch.int32, 0, cache._dev, "pages"), n)
     return out

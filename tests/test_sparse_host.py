@@ -162,11 +162,10 @@ def test_every_call_is_made_with_the_caches_gpu_current(monkeypatch, kind):
                     ("_cuda_cudaCachingAllocator_raw_delete", lambda p: held.pop())):
         monkeypatch.setattr(torch._C, name, f, raising=False)
     monkeypatch.setattr(torch.cuda, "device", Device)
-    Bn._workspace_bytes.cache_clear()
     t = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype).as_subclass(OnGpu1)
     bf16 = torch.bfloat16
     c = type("Cache", (), dict(_dev=1, head_dim=64, n_pages=3, n_kv_heads=8, page_size=16, dtype=bf16, _c=b"",
-                               device="cpu", _shape=(3, 8, 16, 64, 0), _bounds=(3, 8, 2, 64)))()
+                               device="cpu", _shape=(3, 8, 16, 64, 0), _bounds=(3, 8, 2, 64), _sizes={}))()
     q, batch = t(1, 8, 64, dtype=bf16), (t(2), t(1), t(1, 4))
     bounds = t(3, 8, 2, 64, dtype=bf16)
     if kind == "prefix":
@@ -181,14 +180,13 @@ def test_every_call_is_made_with_the_caches_gpu_current(monkeypatch, kind):
             "sparse": "moe_sparse_attention", "bounds": "moe_page_bounds"}[kind]
     asked = [] if kind == "bounds" else [(name + "_workspace", 1), (64, 1)]
     assert calls == asked + [(name, 1)] and now == [0] and held == []
-    Bn._workspace_bytes.cache_clear()
 
 
 def test_the_binding_checks_shapes():
     t = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype)
     bf16 = torch.bfloat16
     c = type("Cache", (), dict(_dev=-1, head_dim=64, n_pages=3, n_kv_heads=2, page_size=16, dtype=bf16, _c=b"",
-                               device="cpu", _shape=(3, 2, 16, 64, 0), _bounds=(3, 2, 2, 64)))()
+                               device="cpu", _shape=(3, 2, 16, 64, 0), _bounds=(3, 2, 2, 64), _sizes={}))()
     q, batch, bounds = t(1, 4, 64, dtype=bf16), (t(2), t(1), t(1, 4)), t(3, 2, 2, 64, dtype=bf16)
     for f in (lambda: Bn.page_bounds(c, t(3, 2, 64, dtype=bf16), *batch, n_rows=1),
               lambda: Bn.page_bounds(c, bounds.half(), *batch, n_rows=1),
