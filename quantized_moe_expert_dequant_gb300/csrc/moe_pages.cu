@@ -149,7 +149,9 @@ constexpr int kFew = 64;             // pages compared in fp64 one against the o
 struct Select {
   Params p;
   const void *bounds;  // [n_pages][hkv][2][D]
-  float2 *score;       // [rows of this launch][hkv][width]: score, bound of the sum of its terms' sizes
+  // [rows of this launch][hkv][2 width]: scores of the pages, then for each 16 the largest bound of the sum of a
+  // score's terms' sizes
+  float *score;
   int32_t *out;        // [n_rows][hkv][n_select]
   int row0, rows, width, n_select, sink, recent;
   float error;         // of a score, relative to the sizes' sum
@@ -186,16 +188,23 @@ struct Block {
   static constexpr int kParts = 2 * D / 64;  // 16-byte parts of a page's bounds that a lane takes
   uint4 x[PAGES][kParts];
   float top[PAGES];  // the largest size of a bound; -1: no page
+  int at[PAGES];     // of the pages that are fetched next
 
-  // Pages first .. count - 1 of a sequence; those outside the cache are reported.
-  __device__ __forceinline__ void fetch(const Select &w, int seq, int kvh, int first, int count) {
-    const Params &p = w.p;
-    const int part = threadIdx.x & 7;
-    int at[PAGES];
+  // Looks up pages first .. count - 1 of a sequence.
+  __device__ __forceinline__ void look(const Select &w, int seq, int first, int count) {
 #pragma unroll
     for (int t = 0; t < PAGES; ++t) {
       const int j = first + (threadIdx.x >> 3) + t * (kBlock / 8);
-      at[t] = j < count ? p.table[seq * p.table_stride + j] : -1;
+      at[t] = j < count ? w.p.table[seq * w.p.table_stride + j] : -1;
+    }
+  }
+  // The bounds of those pages; pages outside the cache are reported.
+  __device__ __forceinline__ void fetch(const Select &w, int kvh, int first, int count) {
+    const Params &p = w.p;
+    const int part = threadIdx.x & 7;
+#pragma unroll
+    for (int t = 0; t < PAGES; ++t) {
+      const int j = first + (threadIdx.x >> 3) + t * (kBlock / 8);
       top[t] = static_cast<unsigned>(at[t]) < static_cast<unsigned>(p.n_pages) ? 0.f : -1.f;
       if (top[t] < 0.f && j < count && j >= w.sink && part == 0 && p.err)
         atomicOr(p.err, kDevErrBadId);
@@ -384,9 +393,11 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
       const int at = begin + turn * kPagesATurn + 16 * warp;
       if (at >= count) break;
       if (r0 + turn > 0) fetch(seq, count, at);
-      float large[2][4] = {}, small[2][4] = {};
+      // of the larger parts 32 products are summed by themselves, so that the error does not grow with the dimensions
+      float sum[2][4] = {}, small[2][4] = {};
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k)
+      for (int k = 0; k < kSteps; ++k) {
+        float large[2][4] = {};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const uint4 lo = *reinterpret_cast<const uint4 *>(&s_q[s][g][32 * k + 8 * q4]);
@@ -399,6 +410,12 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
           }
         }
 #pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[t][c] += large[t][c];
+      }
+      float most[2];
+#pragma unroll
       for (int t = 0; t < 2; ++t) {
         uint32_t m = 0u;
 #pragma unroll
@@ -410,17 +427,23 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
         float top = fmaxf(f.x, f.y);  // the largest size of a bound of page g
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (!there[t]) top = -1.f;
+        const bool none = !there[t];
+        most[t] = none ? 0.f : top;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // row g or g + 8, page 2 q4 or 2 q4 + 1
-          const float size = __shfl_sync(0xffffffffu, top, 4 * (2 * q4 + (c & 1)));
+          const bool left = __shfl_sync(0xffffffffu, none, 4 * (2 * q4 + (c & 1)));
           const int r = g + 8 * (c >> 1), j = at + 8 * t + 2 * q4 + (c & 1);
           if (r >= r0 && r < r1 && j < s_count[r])
-            w.score[(static_cast<int64_t>(blockIdx.x * kRowTile + r) * p.hkv + kvh) * w.width + j] =
-                size < 0.f ? make_float2(kNegInf, 0.f)
-                           : make_float2((large[t][c] + small[t][c]) * s_scale[r], size * s_size[r]);
+            w.score[(static_cast<int64_t>(blockIdx.x * kRowTile + r) * p.hkv + kvh) * 2 * w.width + j] =
+                left ? kNegInf : (sum[t][c] + small[t][c]) * s_scale[r];
         }
       }
+      float size = fmaxf(most[0], most[1]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+      if (lane >= r0 && lane < r1 && at < s_count[lane])
+        w.score[((static_cast<int64_t>(blockIdx.x * kRowTile + lane) * p.hkv + kvh) * 2 + 1) * w.width +
+                at / 16] = size * s_size[lane];
     }
   }
 }
@@ -524,10 +547,9 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
   const int want = w.n_select - w.sink - w.recent;
   // keys of 32 bits; where many scores are the same, the exact ones of 64 bits take their place
   uint32_t *s_sel = s_dyn, *s_mid = s_sel + words, *s_bins = s_mid + words, *s_keys = s_bins + kBins;
-  float2 *score = CS ? reinterpret_cast<float2 *>(s_keys) - j0
-                     : w.score + (static_cast<int64_t>(blockIdx.x) * p.hkv + kvh) * w.width;
+  float *score = w.score + (static_cast<int64_t>(blockIdx.x) * p.hkv + kvh) * 2 * w.width;
   const bool kept = CS > 0 || n <= kKeys;
-  const auto key_at = [&](int i) { return kept ? s_keys[i] : key_of(score[j0 + i].x); };
+  const auto key_at = [&](int i) { return kept ? s_keys[i] : key_of(score[j0 + i]); };
   uint32_t lo = ~0u, hi = 0u;
   float size = 0.f;
   if constexpr (CS > 0) {
@@ -538,12 +560,16 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
     if (threadIdx.x == 0) s_size = 0.f;
     Block<T, D, P> b;
     int at = j0 + rank * kPages;
-    if (at < j1 && want > 0) b.fetch(w, row.seq, kvh, at, j1);
+    const int end = want > 0 ? j1 : 0;
+    b.look(w, row.seq, at, end);  // on their way during the sums
     __syncthreads();
-    add_size<D>(sum_heads<T, D>(p, row_i, kvh, s_sums), &s_size);
+    const float sizes = sum_heads<T, D>(p, row_i, kvh, s_sums);
+    b.fetch(w, kvh, at, end);
+    b.look(w, row.seq, at + CS * kPages, end);
+    add_size<D>(sizes, &s_size);
     __syncthreads();
     if (CS > 1) cluster_wait();  // the first block is there
-    for (; at < j1 && want > 0; at += CS * kPages) {
+    for (; at < end; at += CS * kPages) {
       b.sizes();
       float s[P];
       b.score(s_sums, s);
@@ -559,7 +585,8 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
         else
           s_keys[i] = key;
       }
-      if (at + CS * kPages < j1) b.fetch(w, row.seq, kvh, at + CS * kPages, j1);
+      b.fetch(w, kvh, at + CS * kPages, end);
+      b.look(w, row.seq, at + 2 * CS * kPages, end);
     }
     size *= s_size;
   }
@@ -580,11 +607,13 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
   if (CS == 0 && want > 0) {
 #pragma unroll 8
     for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float2 s = score[j0 + i];
-      const uint32_t key = key_of(s.x);
+      const uint32_t key = key_of(score[j0 + i]);
       if (kept) s_keys[i] = key;
       lo = min(lo, key), hi = max(hi, key);
-      size = s.y <= size ? size : s.y;
+    }
+    for (int i = j0 / 16 + threadIdx.x; i <= (j1 - 1) / 16; i += kThreads) {
+      const float s = score[w.width + i];
+      size = s <= size ? size : s;  // (a NaN stays)
     }
   }
   // sizes are positive or NaN: their order is that of their bits
@@ -731,7 +760,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
       } else {
         // Many pages with the same score but for rounding.  Their fp64 keys take the scores' place, and
         // the need-th largest is found bit by bit.
-        uint64_t *key = reinterpret_cast<uint64_t *>(score);
+        uint64_t *key = CS ? reinterpret_cast<uint64_t *>(s_keys) - j0 : reinterpret_cast<uint64_t *>(score);
         for (int i = warp; any && i < words; i += kN)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
             const int j = 32 * i + __ffs(m) - 1;
@@ -852,7 +881,8 @@ static cudaError_t launch_select(Select w, const SelectPlan &plan, cudaStream_t 
   cudaError_t e = limit.set(reinterpret_cast<const void *>(pick), smem(kMaxPages));
   if (e != cudaSuccess) return e;
   constexpr int kPages = kTurns * kPagesATurn;
-  w.error = (2 * D + 64 + p.group) * 1.2e-7f;  // (the split counts 32 truncations, the sums' group of them)
+  // truncations of 2^-23: 32 of products, as many for the split in two of bf16, 2 D / 32 + 2 of sums, group of Q's
+  w.error = (32 + (Half<T>::kRow > 0.f ? 0 : 32) + 2 * D / 32 + 4 + p.group) * 1.2e-7f;
   for (; w.row0 < p.n_rows; w.row0 += plan.rows) {
     w.rows = std::min(plan.rows, p.n_rows - w.row0);
     if (p.table_width > w.n_select) {  // (otherwise every page of every row is selected)
@@ -923,7 +953,7 @@ extern "C" int moe_select_pages(const moe_kv_cache *cache, const moe_attention *
   if (rc != MOE_OK) return rc;
   if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MOE_ERR_INVALID_ARG;
   w.bounds = bounds;
-  w.score = static_cast<float2 *>(workspace);
+  w.score = static_cast<float *>(workspace);
   w.out = pages;
   w.width = w.p.table_width;
   w.n_select = n_select;
