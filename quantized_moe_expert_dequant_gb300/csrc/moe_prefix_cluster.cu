@@ -19,8 +19,8 @@ int takes_prefix_clusters(const moe_kv_cache *c, const Params &p, bool *takes) {
   Plan plan;
   const int rc = make_plan(c, p, p.n_seqs, p.n_rows, rows, positions, &plan);
   // (304 CTAs in clusters of 8 are not all resident at once: 38 drafts of 4 behind 4000 positions, one key/value
-  // head: 33.7 us, 25.3 on the tiles; 256 are)
-  *takes = rc == MOE_OK && plan.cluster > 0 && 4 * static_cast<int64_t>(plan.grid) <= 7 * plan.sms &&
+  // head: 33.7 us, 25.3 on the tiles; 288 are: 18 tokens, 2 heads, 15.9 and 27.8)
+  *takes = rc == MOE_OK && plan.cluster > 0 && 10 * static_cast<int64_t>(plan.grid) <= 19 * plan.sms &&
            (plan.cluster == 16 || positions <= (rows <= 16 ? kFewRows : kMoreRows));
   return rc;
 }
