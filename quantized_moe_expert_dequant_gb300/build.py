@@ -27,7 +27,7 @@ SOURCES = ["moe_kernels_g4.cu", "moe_kernels_g6.cu", "moe_kernels_g8.cu", "moe_g
            "moe_grouped_g6.cu", "moe_grouped_g8.cu", "moe_cols_g4.cu", "moe_cols_g6.cu",
            "moe_cols_g8.cu", "moe_kernels.cu", "moe_mma.cu",
            "moe_api.cu", "moe_pack.cpp", "synth.cu", "gemv.cu", "moe_rope.cu",
-           "moe_prompt.cu", "moe_prompt_tree.cu", "moe_prompt_shared.cu", "moe_prefix_cluster.cu",
+           "moe_prompt.cu", "moe_prompt_tree.cu", "moe_prompt_shared.cu", "moe_prefix_tree.cu",
            "moe_tree.cu", "moe_tree_cluster.cu", "moe_pages.cu", "moe_sparse.cu",
            "moe_sparse_cluster.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

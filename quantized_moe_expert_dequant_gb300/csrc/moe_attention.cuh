@@ -382,11 +382,11 @@ struct SmemLimit {
 // Limit of the tiles' waits in cycles; 0: the usual one (moe_debug_attention_wait_cycles).
 inline std::atomic<int64_t> debug_wait_cycles{0};
 
-// moe_prefix_attention of few and short sequences, each by a cluster of CTAs (moe_prefix_cluster.cu): whether it
-// takes a batch, or an error; and the call.
-int takes_prefix_clusters(const moe_kv_cache *cache, const Params &p, bool *takes);
-int run_prefix_clusters(const moe_kv_cache *cache, const Params &p, const Prefixes &g,
-                        cudaStream_t stream);
+// moe_prefix_attention of short sequences in the form of moe_tree_attention (moe_prefix_tree.cu): whether it takes a
+// batch and its workspace, or an error; and the call.
+int prefix_tree_workspace(const moe_kv_cache *cache, const Params &p, bool *takes, int64_t *bytes);
+int run_prefix_tree(const moe_kv_cache *cache, const Params &p, const Prefixes &g, void *workspace,
+                    int64_t workspace_bytes, cudaStream_t stream);
 
 // Attention in tiles of 128 rows on the 5th-generation tensor cores: causal, or by p.mask
 // (moe_prompt.cu, moe_prompt_tree.cu).

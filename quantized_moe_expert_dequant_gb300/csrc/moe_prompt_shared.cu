@@ -31,9 +31,9 @@ extern "C" int moe_prefix_attention_workspace(const moe_kv_cache *cache, const m
   if (!bytes) return MOE_ERR_INVALID_ARG;
   *bytes = 0;
   if (p.n_seqs == 0 || p.n_rows == 0) return MOE_OK;
-  bool clusters;
-  int err = attn::takes_prefix_clusters(cache, p, &clusters);
-  if (err != MOE_OK || clusters) return err;
+  bool tree;
+  int err = attn::prefix_tree_workspace(cache, p, &tree, bytes);
+  if (err != MOE_OK || tree) return err;
   attn::PromptPlan plan;
   err = attn::make_plan(cache, p, &plan, n_groups);
   if (err == MOE_OK) *bytes = plan.bytes;
@@ -54,10 +54,13 @@ extern "C" int moe_prefix_attention(const moe_kv_cache *cache, const moe_attenti
   if (n_groups > 0 && (!cu_group || !prefix_len)) return MOE_ERR_INVALID_ARG;
   p.mask = tree_mask;
   const attn::Prefixes g = {cu_group, prefix_len, n_groups};
-  bool clusters;
-  int err = attn::takes_prefix_clusters(cache, p, &clusters);
+  bool tree;
+  int64_t bytes;
+  int err = attn::prefix_tree_workspace(cache, p, &tree, &bytes);
   if (err != MOE_OK) return err;
-  if (clusters) return attn::run_prefix_clusters(cache, p, g, static_cast<cudaStream_t>(stream));
+  if (tree)
+    return attn::run_prefix_tree(cache, p, g, workspace, workspace_bytes,
+                                 static_cast<cudaStream_t>(stream));
   attn::PromptPlan plan;
   err = attn::make_plan(cache, p, &plan, n_groups);
   if (err != MOE_OK) return err;

@@ -248,7 +248,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 template <typename T, int D, int WR, int CS, int ITEMS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w) {
   constexpr bool SPARSE = ITEMS == kListed;
-  static_assert(ITEMS != kGrouped || CS > 0, "one item a CTA");
   constexpr int kTile = Tree<D>::kTile;
   constexpr int ROWS = 16 * WR, WT = 4 / WR, TW = kTile / WT;  // TW positions of a warp per tile
   constexpr int kStages = Tree<D>::kStages, kTileBytes = Tree<D>::kTileBytes;
@@ -348,6 +347,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     bool ready;        // the next tile's entries have been read
     const int32_t *first;  // grouped: the pages of positions before `limit`
   } ld;
+  const auto look_up_group = [&](int ctx) {
+    int index;
+    const Group group = group_of(p, w.g, ld.seq, &index);
+    ld.limit = shared_by(group, ctx);
+    ld.first = ld.limit ? p.table + group.begin * p.table_stride : ld.pages;
+  };
   const auto look_up = [&]() {
     if constexpr (SPARSE) {
       if (!ld.ready) load_entries<kTile>(p, ld.pages, ld.len, ld.t, ld.list);
@@ -374,12 +379,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     } else {
       ld.pages = p.table + ld.seq * p.table_stride;
     }
-    if constexpr (ITEMS == kGrouped) {
-      int index;
-      const Group group = group_of(p, w.g, ld.seq, &index);
-      ld.limit = shared_by(group, q.ctx);
-      ld.first = ld.limit ? p.table + group.begin * p.table_stride : ld.pages;
-    }
+    if constexpr (ITEMS == kGrouped) look_up_group(q.ctx);
     ld.head_off = ld.kvh * p.head_stride;
     look_up();
     ld.next = load(min(ld.seq + 1, n_items - 1), false);
@@ -392,7 +392,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
     ld.kvh = 0;
     ld.head_off = 0;
     bool empty = true;  // sequences without rows have no tiles
+    int ctx = 0;
     while (empty && ++ld.seq < n_items) {
+      ctx = ld.next.ctx;
       ld.len = ld.next.len, ld.nt = (ld.len + kTile - 1) / kTile;
       empty = ld.next.nq == 0;
       if constexpr (SPARSE) ld.limit = ld.next.ctx, ld.table = ld.next.seq;
@@ -403,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const Work w
       ld.pages = w.list + static_cast<int64_t>(ld.seq) * p.hkv * w.n_list;
     else
       ld.pages = p.table + ld.seq * p.table_stride;
+    if constexpr (ITEMS == kGrouped)
+      if (!empty) look_up_group(ctx);
   };
   const auto copy_next = [&]() {
     if (ld.left > 0) {
@@ -725,7 +729,7 @@ constexpr int64_t kClusterPositions = 16384;  // up to which a cluster takes an 
 // Of n items a key/value head with up to `rows` rows and `positions` positions each; `most_items` of them
 // at most can have any.
 inline int make_plan(const moe_kv_cache *c, const Params &p, int64_t n, int64_t most_items,
-                     int64_t rows, int64_t positions, Plan *plan) {
+                     int64_t rows, int64_t positions, Plan *plan, bool clusters_too = true) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -739,7 +743,7 @@ inline int make_plan(const moe_kv_cache *c, const Params &p, int64_t n, int64_t 
   plan->cluster = 0;
   plan->part = plan->ml = plan->shared = plan->bytes = 0;
   const int64_t clusters = n * p.hkv;
-  if (positions <= kClusterPositions)
+  if (clusters_too && positions <= kClusterPositions)
     plan->cluster = clusters * 16 <= sms ? 16 : clusters * 8 <= sms * kCtasPerSm ? 8 : 0;
   plan->grid = static_cast<int>(clusters) * plan->cluster;
   if (plan->cluster) return MOE_OK;

@@ -59,6 +59,33 @@ def test_single_tokens(dtype, Hq, Hkv, D, page):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_single_tokens_on_the_tiles(dtype, Hq, Hkv, D):
+    """The same with room for more tokens a sequence, and more rows than the other forms take."""
+    n = 14
+    after = [(i * 53) % 300 for i in range(n)]
+    G = Groups(Hq + D, [1, 8, 12], [1500, 777], [1] * n, after, Hq, Hkv, D, 64, dtype)
+    ref, tol = G.b.reference(D ** -0.5)
+    C.assert_within(G.run(64), ref, tol)
+    short = Groups(Hq + D, [0, 5, 14], [130, 64], [1] * n, after, Hq, Hkv, D, 64, dtype)
+    ref, tol = short.b.reference(D ** -0.5)
+    C.assert_within(short.run(64), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(8, 2, 128, 90), (6, 1, 64, 150), (16, 16, 64, 20)])
+def test_many_short_sequences(dtype, Hq, Hkv, D, n):
+    """All CTAs share the items of many sequences; groups of one and of none, sequences without rows."""
+    lens = [(i * 7 + 3) % 4 for i in range(n)]
+    cu = [0, 1, 1, n // 3, n // 2, n - 2]
+    G = Groups(Hq + n, cu, [48, 100, 333, 64, 16], lens, [(i * 31) % 150 for i in range(n)], Hq, Hkv, D, 16,
+               dtype)
+    masks = tree_masks(n, lens)
+    ref, tol = G.b.reference(0.2, masks)
+    C.assert_within(G.run(3, masks, 0.2), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
 @pytest.mark.parametrize("ancestors", [True, False])
 def test_trees(dtype, Hq, Hkv, D, ancestors):
     lens = [1, 64, 0, 3, 17, 33, 48, 2, 0]
