@@ -48,7 +48,8 @@ __device__ __forceinline__ int touched(const Params &p, const Seq &s) {
 }
 
 // One block a touched page (blockIdx.x, counted over all sequences) and key/value head: D / 8 threads side
-// by side read a position, so that a page of 64 is four loads a thread, all under way at once.
+// by side read a position, so that a page of 64 is four loads a thread, all under way at once.  A launch and three
+// dependent loads: 32 tokens, 8 heads of 128 (2.3 MB) 3.5 us, prompts of 9230 tokens, 2 heads of 64 (2.7 MB) 4.9 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bounds) {
   constexpr int kChunks = D / 8, kRows = kBlock / kChunks;
@@ -464,7 +465,6 @@ __device__ __forceinline__ uint64_t key_of(double s) {
 }
 
 // Sum over the block, for every thread.
-template <int WARPS>
 __device__ __forceinline__ int block_sum(int v, int *s_sum) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
@@ -472,11 +472,10 @@ __device__ __forceinline__ int block_sum(int v, int *s_sum) {
   __syncthreads();
   int all = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) all += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) all += s_sum[w];
   return all;
 }
 // Sum over the threads before this one.
-template <int WARPS>
 __device__ __forceinline__ int block_below(int v, int *s_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -490,7 +489,7 @@ __device__ __forceinline__ int block_below(int v, int *s_sum) {
   __syncthreads();
   int base = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w)
+  for (int w = 0; w < kWarps; ++w)
     if (w < warp) base += s_sum[w];
   return base + x - v;
 }
@@ -512,15 +511,16 @@ __device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
       : "memory");
 }
 
-constexpr int kFewThreads = 256;
-
 // The pages of a row and key/value head.  CS = 0: one block, the scores are in w.score.  CS > 0: a cluster of
-// CS blocks scores the pages, and its first takes all scores in its shared memory and chooses.
+// CS blocks scores the pages, and its first takes all scores in its shared memory and chooses.  The k-th score is
+// found by bins between the least and the largest, mostly one pass, and by rank among the few in its bin.  Bound by
+// latency: of 9.7 us for one token, 2047 pages and 8 heads, 3 are the loads of the row, its queries and bounds, 1.2 the
+// scores, 0.9 the cluster's barrier, 1 each the bins and the masks of those chosen.  (32 tokens, 500 pages: 12.6 us,
+// 17.9 with the scores in a kernel of their own; CS = 0, 512 rows, 2 heads, 2000 pages: 20 us behind 20 of scores.)
 template <typename T, int D, int CS>
-__global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const Select w) {
-  constexpr int kThreads = CS ? kBlock : kFewThreads, kN = kThreads / 32;
+__global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
   extern __shared__ __align__(16) uint32_t s_dyn[];
-  __shared__ int s_sum[kN], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
+  __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
   __shared__ uint32_t s_range[3 * (CS ? CS : 1)];  // of each block's part: least and largest key, largest size
   __shared__ double s_q[2 * D], s_exact[kFew];
   __shared__ float s_edge[2];
@@ -533,14 +533,14 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
   if (!behind) pdl_wait();
   pdl_launch();
   if (blockIdx.x == 0 && row_i == 0 && kvh == 0)
-    for (int i = threadIdx.x; i < p.n_seqs; i += kThreads) load_seq(p, i, true);
+    for (int i = threadIdx.x; i < p.n_seqs; i += kBlock) load_seq(p, i, true);
   const Row row = load_row(p, row_i, 1);
   const int pages = row.nq ? ((row.ctx - 1) >> p.page_shift) + 1 : 0;
   int32_t *out = w.out + (static_cast<int64_t>(row_i) * p.hkv + kvh) * w.n_select;
   if (pages <= w.n_select) {
     if (behind) pdl_wait();
     if (row.nq && rank == 0)
-      for (int i = threadIdx.x; i < w.n_select; i += kThreads) out[i] = i < pages ? i : -1;
+      for (int i = threadIdx.x; i < w.n_select; i += kBlock) out[i] = i < pages ? i : -1;
     return;
   }
   const int words = (pages + 31) / 32, j0 = w.sink, j1 = pages - w.recent, n = j1 - j0;
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
     size *= s_size;
   }
   if (rank == 0) {
-    for (int i = threadIdx.x; i < words; i += kThreads) {
+    for (int i = threadIdx.x; i < words; i += kBlock) {
       // all 32 bits from bit 32 i on that are before j0 or from j1 to the end
       uint32_t m = 0;
       const int from = 32 * i;
@@ -600,18 +600,18 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
       if (from + 32 > pages) m &= (1u << (pages - from)) - 1;
       s_sel[i] = m, s_mid[i] = 0u;
     }
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s_bins[i] = 0u;
+    for (int i = threadIdx.x; i < kBins; i += kBlock) s_bins[i] = 0u;
     if (threadIdx.x == 0) s_count = s_in = s_mid_count = 0;
   }
   if (behind) pdl_wait();
   if (CS == 0 && want > 0) {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += kBlock) {
       const uint32_t key = key_of(score[j0 + i]);
       if (kept) s_keys[i] = key;
       lo = min(lo, key), hi = max(hi, key);
     }
-    for (int i = j0 / 16 + threadIdx.x; i <= (j1 - 1) / 16; i += kThreads) {
+    for (int i = j0 / 16 + threadIdx.x; i <= (j1 - 1) / 16; i += kBlock) {
       const float s = score[w.width + i];
       size = s <= size ? size : s;  // (a NaN stays)
     }
@@ -619,11 +619,11 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
   // sizes are positive or NaN: their order is that of their bits
   lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
   uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
-  __shared__ uint32_t s_part[3][kN];
+  __shared__ uint32_t s_part[3][kWarps];
   if (lane == 0) s_part[0][warp] = lo, s_part[1][warp] = hi, s_part[2][warp] = most;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < kN; ++v)
+  for (int v = 0; v < kWarps; ++v)
     lo = min(lo, s_part[0][v]), hi = max(hi, s_part[1][v]), most = max(most, s_part[2][v]);
   if constexpr (CS > 1) {
     if (threadIdx.x == 0) {
@@ -647,18 +647,18 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
     while (lo < hi && inside > kFew / 4) {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
 #pragma unroll 4
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+      for (int i = threadIdx.x; i < n; i += kBlock) {
         const uint32_t key = key_at(i);
         if (lo <= key && key <= hi) atomicAdd(&s_bins[(key - lo) >> shift], 1u);
       }
       __syncthreads();
       // bins from the largest keys down, some a thread
-      constexpr int kEach = kBins / kThreads;
+      constexpr int kEach = kBins / kBlock;
       uint32_t c[kEach];
       int sum = 0;
 #pragma unroll
       for (int e = 0; e < kEach; ++e) c[e] = s_bins[kBins - 1 - kEach * threadIdx.x - e], sum += c[e];
-      int before = above + block_below<kN>(sum, s_sum);
+      int before = above + block_below(sum, s_sum);
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
         if (before < want && want <= before + static_cast<int>(c[e]))
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
     const float t_hi = score_of(hi) + error, t_lo = score_of(lo) - error;
     int in = 0, mid = 0;
 #pragma unroll 4
-    for (int i = warp; i < words; i += kN) {
+    for (int i = warp; i < words; i += kWarps) {
       const int j = 32 * i + lane;
       bool is_in = false, is_mid = false;
       if (j >= j0 && j < j1) {
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
     // that is taken.
     const bool told = need >= mid;
     if (told) {
-      for (int i = threadIdx.x; i < words; i += kThreads) s_sel[i] |= s_mid[i];
+      for (int i = threadIdx.x; i < words; i += kBlock) s_sel[i] |= s_mid[i];
     } else if (mid <= kFew) {
       float s = 0.f;
       int j = 0, ahead = 0;
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
       sum_heads<T, D>(p, row_i, kvh, s_q);
       __syncthreads();
       bool any = false;
-      for (int d = threadIdx.x; d < 2 * D; d += kThreads) any |= s_q[d] != 0.;
+      for (int d = threadIdx.x; d < 2 * D; d += kBlock) any |= s_q[d] != 0.;
       any = __syncthreads_or(any);  // without (a row of padding), all scores are 0
       const auto exact = [&](int j) {  // a whole warp
         const int page = p.table[row.seq * p.table_stride + j];
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
         return x == x ? x : -__builtin_huge_val();
       };
       if (any && mid <= kFew) {
-        for (int i = warp; i < mid; i += kN) {
+        for (int i = warp; i < mid; i += kWarps) {
           const double x = exact(s_at[i]);
           if (lane == 0) s_exact[i] = x;
         }
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
         // Many pages with the same score but for rounding.  Their fp64 keys take the scores' place, and
         // the need-th largest is found bit by bit.
         uint64_t *key = CS ? reinterpret_cast<uint64_t *>(s_keys) - j0 : reinterpret_cast<uint64_t *>(score);
-        for (int i = warp; any && i < words; i += kN)
+        for (int i = warp; any && i < words; i += kWarps)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
             const int j = 32 * i + __ffs(m) - 1;
             const double x = exact(j);
@@ -770,21 +770,21 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
         __syncthreads();
         const auto count = [&](uint64_t least) {
           int c = 0;
-          for (int i = threadIdx.x; i < words; i += kThreads)
+          for (int i = threadIdx.x; i < words; i += kBlock)
             for (uint32_t m = s_mid[i]; m; m &= m - 1) c += key[32 * i + __ffs(m) - 1] >= least;
-          return block_sum<kN>(c, s_sum);
+          return block_sum(c, s_sum);
         };
         uint64_t last = 0;
         for (int b = 63; any && b >= 0; --b)
           if (count(last | 1ull << b) >= need) last |= 1ull << b;
         const int ties = any ? need - count(last + 1) : need;  // the lower pages
-        const int each = (words + kThreads - 1) / kThreads;
+        const int each = (words + kBlock - 1) / kBlock;
         const int i0 = min(words, static_cast<int>(threadIdx.x) * each), i1 = min(words, i0 + each);
         int mine = 0;
         for (int i = i0; i < i1; ++i)
           for (uint32_t m = s_mid[i]; m; m &= m - 1)
             mine += !any || key[32 * i + __ffs(m) - 1] == last;
-        int before = block_below<kN>(mine, s_sum);
+        int before = block_below(mine, s_sum);
         for (int i = i0; i < i1; ++i)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
             const uint64_t x = any ? key[32 * i + __ffs(m) - 1] : last;
@@ -796,13 +796,13 @@ __global__ void __launch_bounds__(CS ? kBlock : kFewThreads) pick_kernel(const S
   __syncthreads();
   // the pages in order
   int done = 0;
-  for (int b = 0; b < words; b += kThreads) {
+  for (int b = 0; b < words; b += kBlock) {
     const int i = b + threadIdx.x;
     const uint32_t mine = i < words ? s_sel[i] : 0u;
-    int at = done + block_below<kN>(__popc(mine), s_sum);
+    int at = done + block_below(__popc(mine), s_sum);
     for (uint32_t m = mine; m; m &= m - 1, ++at)
       if (at < w.n_select) out[at] = 32 * i + __ffs(m) - 1;
-    if (b + kThreads < words) done += block_sum<kN>(__popc(mine), s_sum);
+    if (b + kBlock < words) done += block_sum(__popc(mine), s_sum);
   }
 }
 
@@ -890,7 +890,7 @@ static cudaError_t launch_select(Select w, const SelectPlan &plan, cudaStream_t 
       e = launch_early(score_kernel<T, D>, grid, kBlock, 0, stream, w);
       if (e != cudaSuccess) return e;
     }
-    e = launch_early(pick, dim3(w.rows, p.hkv), kFewThreads, smem(w.width), stream, w);
+    e = launch_early(pick, dim3(w.rows, p.hkv), kBlock, smem(w.width), stream, w);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -1,5 +1,6 @@
 // moe_tree.cuh -- attention of decoded tokens, or of trees of drafted tokens, over the pages of a
-// cache (moe_tree_attention; instantiated by moe_tree.cu and moe_tree_cluster.cu).
+// cache (moe_tree_attention; instantiated by moe_tree.cu and moe_tree_cluster.cu), over pages that are listed
+// for each row (moe_sparse.cu, moe_sparse_cluster.cu), and with a group's first pages (moe_prefix_tree.cu).
 //
 //   out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale * q_r . k_j - m_r)  over the positions j
 //   that row r sees, m_r their largest score: one pass over K and V with the running maximum and
