@@ -27,9 +27,9 @@ static int plan_prefix(const moe_kv_cache *c, const Params &p, bool *takes, Plan
   if (rows > 32) return MOE_OK;
   const int64_t most = static_cast<int64_t>(p.n_rows) * p.group / (rows <= 16 ? 16 : 32) + p.n_seqs;
   int rc = make_plan(c, p, p.n_seqs, most, rows, positions, plan);
-  // (304 CTAs in clusters of 8 are not all resident at once: 38 drafts of 4 behind 4000 positions, one key/value
-  // head: 33.7 us, 25.3 on the tiles; 288 are: 18 tokens, 2 heads, 15.9 and 27.8)
-  if (rc == MOE_OK && plan->cluster > 0 && 10 * static_cast<int64_t>(plan->grid) <= 19 * plan->sms &&
+  // (38 drafts of 4 behind 4000 positions, one key/value head, 304 CTAs in clusters: 33.7 us, 25.3 on the tiles; 18
+  // tokens, 2 heads, 288 CTAs: 15.9, 27.8)
+  if (rc == MOE_OK && plan->cluster > 0 && resident(*plan) &&
       (plan->cluster == 16 || positions <= (rows <= 16 ? kFewRows : kMoreRows))) {
     *takes = true;
     return rc;

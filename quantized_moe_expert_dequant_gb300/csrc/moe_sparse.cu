@@ -12,7 +12,9 @@ namespace attn {
 
 static int plan_sparse(const moe_kv_cache *c, const Params &p, int n_list, Plan *plan) {
   const int64_t pages = std::min<int64_t>(p.table_width, n_list);
-  return make_plan(c, p, p.n_rows, p.n_rows, p.group, pages << p.page_shift, plan);
+  const int rc = make_plan(c, p, p.n_rows, p.n_rows, p.group, pages << p.page_shift, plan);
+  if (rc != MOE_OK || !plan->cluster || resident(*plan)) return rc;
+  return make_plan(c, p, p.n_rows, p.n_rows, p.group, pages << p.page_shift, plan, false);
 }
 
 template <typename T, int D>

@@ -762,6 +762,9 @@ inline int make_plan(const moe_kv_cache *c, const Params &p, int64_t n, int64_t 
   return MOE_OK;
 }
 
+// Whether the CTAs of clusters of 8 are all resident at once: 288 are, 304 are not.
+inline bool resident(const Plan &plan) { return 10 * static_cast<int64_t>(plan.grid) <= 19 * plan.sms; }
+
 inline void use_workspace(const Plan &plan, void *workspace, Work *w) {
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   w->part = reinterpret_cast<float *>(ws + plan.part);
