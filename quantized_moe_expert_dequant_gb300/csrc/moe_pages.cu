@@ -368,17 +368,18 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
       size += __shfl_xor_sync(0xffffffffu, size, o);
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    // fp16: the largest is brought to 2^14 .. 2^15
-    int exponent = 0;
-    if (sizeof(T) == 2 && Half<T>::kRow > 0.f && top > 0.f && top < 3e38f)
-      frexpf(top, &exponent), exponent -= 15;
-    if (lane == 0) s_size[r] = size, s_scale[r] = ldexpf(1.f, exponent);
+    // fp16: the largest (2^-24 .. 2^22) is brought to 2^14 .. 2^15
+    float scale = 1.f, back = 1.f;
+    if (Half<T>::kRow > 0.f && top > 0.f && top < 1e30f) {
+      const int shift = 127 + 14 - static_cast<int>(__float_as_uint(top) >> 23);
+      scale = __uint_as_float((127 + shift) << 23), back = __uint_as_float((127 - shift) << 23);
+    }
+    if (lane == 0) s_size[r] = size, s_scale[r] = back;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int v = 0; v < V; v += 2) {
-        const float x = ldexpf(s ? up[v] : down[v], -exponent);
-        const float y = ldexpf(s ? up[v + 1] : down[v + 1], -exponent);
+        const float x = (s ? up[v] : down[v]) * scale, y = (s ? up[v + 1] : down[v + 1]) * scale;
         const uint32_t large = Half<T>::pack(x, y);
         const float2 f = Half<T>::unpack(large);
         const uint32_t small = Half<T>::pack(x - f.x, y - f.y);
@@ -430,13 +431,19 @@ __global__ void __launch_bounds__(kBlock) score_kernel(const Select w) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const bool none = !there[t];
         most[t] = none ? 0.f : top;
+        const bool none0 = __shfl_sync(0xffffffffu, none, 8 * q4), none1 = __shfl_sync(0xffffffffu, none, 8 * q4 + 4);
+        const int j = at + 8 * t + 2 * q4;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // row g or g + 8, page 2 q4 or 2 q4 + 1
-          const bool left = __shfl_sync(0xffffffffu, none, 4 * (2 * q4 + (c & 1)));
-          const int r = g + 8 * (c >> 1), j = at + 8 * t + 2 * q4 + (c & 1);
-          if (r >= r0 && r < r1 && j < s_count[r])
-            w.score[(static_cast<int64_t>(blockIdx.x * kRowTile + r) * p.hkv + kvh) * 2 * w.width + j] =
-                left ? kNegInf : (sum[t][c] + small[t][c]) * s_scale[r];
+        for (int c = 0; c < 4; c += 2) {  // row g or g + 8, pages j and j + 1
+          const int r = g + 4 * c;
+          if (r < r0 || r >= r1 || j >= s_count[r]) continue;
+          float *dst = w.score + (static_cast<int64_t>(blockIdx.x * kRowTile + r) * p.hkv + kvh) * 2 * w.width + j;
+          const float s0 = none0 ? kNegInf : (sum[t][c] + small[t][c]) * s_scale[r];
+          const float s1 = none1 ? kNegInf : (sum[t][c + 1] + small[t][c + 1]) * s_scale[r];
+          if (j + 1 < s_count[r])
+            *reinterpret_cast<float2 *>(dst) = make_float2(s0, s1);
+          else
+            *dst = s0;
         }
       }
       float size = fmaxf(most[0], most[1]);
