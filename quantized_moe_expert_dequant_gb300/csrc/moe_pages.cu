@@ -523,9 +523,12 @@ __device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
 // found by bins between the least and the largest, mostly one pass, and by rank among the few in its bin.  Bound by
 // latency: of 9.7 us for one token, 2047 pages and 8 heads, 3 are the loads of the row, its queries and bounds, 1.2 the
 // scores, 0.9 the cluster's barrier, 1 each the bins and the masks of those chosen.  (32 tokens, 500 pages: 12.6 us,
-// 17.9 with the scores in a kernel of their own; CS = 0, 512 rows, 2 heads, 2000 pages: 20 us behind 20 of scores.)
+// 17.9 with the scores in a kernel of their own.)  CS = 0 is bound by its barriers, so eight blocks an SM, in 32
+// registers: 512 rows, 2 heads, 2000 pages, all 1024 blocks at once, 35.2 us with the scores; 38.4 with six in 40, no
+// better than without a limit (47, 37.8), although 32 spill some words.  (Apart and cold: 23.4 the scores, 24.2 this.)
+// A least number for CS > 0 too lets the compiler take up to 205 registers: 12.9 us for the one token, 9.7 without.
 template <typename T, int D, int CS>
-__global__ void __launch_bounds__(kBlock) pick_kernel(const Select w) {
+__global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w) {
   extern __shared__ __align__(16) uint32_t s_dyn[];
   __shared__ int s_sum[kWarps], s_bin, s_above, s_in_bin, s_count, s_in, s_mid_count, s_at[kFew];
   __shared__ uint32_t s_range[3 * (CS ? CS : 1)];  // of each block's part: least and largest key, largest size
