@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
       __syncthreads();
       bool any = false;
       for (int d = threadIdx.x; d < 2 * D; d += kBlock) any |= s_q[d] != 0.;
-      any = __syncthreads_or(any);  // without (a row of padding), all scores are 0
+      any = __syncthreads_or(any);  // without (a row of padding), fp32 scores are exact: 0, or the lowest
       const auto exact = [&](int j) {  // a whole warp
         const int page = p.table[row.seq * p.table_stride + j];
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages))
@@ -754,9 +754,9 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         return x == x ? x : -__builtin_huge_val();
       };
-      if (any && mid <= kFew) {
+      if (mid <= kFew) {
         for (int i = warp; i < mid; i += kWarps) {
-          const double x = exact(s_at[i]);
+          const double x = any ? exact(s_at[i]) : score_of(key_at(s_at[i] - j0));
           if (lane == 0) s_exact[i] = x;
         }
         __syncthreads();
@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
         }
       } else {
         // Many pages with the same score but for rounding.  Their fp64 keys take the scores' place, and
-        // the need-th largest is found bit by bit.
+        // the need-th largest is found bit by bit.  (Without `any` they have the same: the bins have told 0 and
+        // the lowest apart.)
         uint64_t *key = CS ? reinterpret_cast<uint64_t *>(s_keys) - j0 : reinterpret_cast<uint64_t *>(score);
         for (int i = warp; any && i < words; i += kWarps)
           for (uint32_t m = s_mid[i]; m; m &= m - 1) {
