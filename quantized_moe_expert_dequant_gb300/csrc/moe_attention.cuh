@@ -96,11 +96,13 @@ struct Group {
   int begin, end;  // sequences
   int shared;      // positions, whole pages only (the page that a prefix ends in is each sequence's own); -1 when
                    // the description is out of range
+  int prefix;      // positions as described, those on that page too
 };
 
 __device__ __forceinline__ Group group_at(const Params &p, const Prefixes &g, int i) {
   Group r;
   const int before = g.cu[max(i - 1, 0)], after = g.cu[min(i + 2, g.n_groups)], len = g.len[i];
+  r.prefix = len;
   r.begin = g.cu[i], r.end = g.cu[i + 1];
   // (beside a group whose end is before its beginning, the bounds mean nothing either)
   const bool ok = r.begin >= 0 && r.begin <= r.end && r.end <= p.n_seqs && len >= 0 &&
@@ -112,7 +114,7 @@ __device__ __forceinline__ Group group_at(const Params &p, const Prefixes &g, in
 
 // The group of a sequence; one of no positions for a sequence without.
 __device__ __forceinline__ Group group_of(const Params &p, const Prefixes &g, int s, int *index) {
-  Group r = {0, 0, 0};
+  Group r = {};
   *index = 0;
   if (g.n_groups == 0) return r;
   int lo = 0, hi = g.n_groups;  // the last group that begins at s or before
@@ -128,7 +130,7 @@ __device__ __forceinline__ Group group_of(const Params &p, const Prefixes &g, in
 
 // The positions that a sequence shares: none when the prefix is longer than what it has before its queries.
 __device__ __forceinline__ int shared_by(const Group &g, int ctx) {
-  return g.shared > 0 && g.shared <= ctx ? g.shared : 0;
+  return g.shared > 0 && g.prefix <= ctx ? g.shared : 0;
 }
 
 // A group's rows over its prefix.

@@ -1,17 +1,19 @@
 """Where the calls that do not read the whole cache meet the borders of what they promise: rows of zeros beside pages
-outside the cache."""
+outside the cache, prefixes that end behind a sequence's context."""
 import math
 
 import pytest
 import torch
 
+from quantized_moe_expert_dequant_gb300 import binding as Bn
 from tests import attention_cases as C
 from tests import sparse_cases as S
 from tests.test_gpu_pages import random_bounds, run_select
 
 pytestmark = pytest.mark.gpu
 
-BF16 = torch.bfloat16
+BF16, F16 = torch.bfloat16, torch.float16
+i32 = dict(dtype=torch.int32, device="cuda")
 
 
 def select_without(b, bnd, gone, n_select, sink, recent):
@@ -48,3 +50,23 @@ def test_rows_of_zeros_beside_pages_outside_the_cache(lens, pages, gone, n_selec
     b.table[:, gone] = b.k.shape[0] + 3
     got, err = run_select(b, bnd, n_select)
     assert err == 1 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,max_q", [(5, 2), (60, 2), (60, 64)])  # clusters, all CTAs, tiles of 128 rows
+def test_prefixes_that_end_behind_a_sequences_context(n, max_q, dtype):
+    """A sequence with fewer positions before its queries than the prefix has is computed by itself, also when it has
+    the prefix's whole pages: what its own pages hold there is its own."""
+    prefix, page = 130, 16
+    lens = [1 + i % 2 for i in range(n)]
+    ctxs = [[130, 129, 128, 131, 127][i % 5] for i in range(n)]
+    b = C.batch(n + max_q, lens, ctxs, 4, 2, 64, page, dtype)
+    for i in range(1, n):
+        if ctxs[i] >= prefix:
+            b.table[i, :prefix // page] = b.table[0, :prefix // page]
+    err = torch.zeros(1, **i32)
+    got = Bn.prefix_attention(Bn.KvCache(b.k, b.v), b.q, b.cu, b.ctx, b.table, torch.tensor([0, n], **i32),
+                              torch.tensor([prefix], **i32), max_q, scale=0.2, device_error=err)
+    ref, tol = b.reference(0.2)
+    C.assert_within(got, ref, tol)
+    assert int(err) == 0
