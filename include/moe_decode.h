@@ -441,8 +441,10 @@ int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *args, void *
  *   pages   int32 [n_rows][n_kv_heads][n_select] device: places in the sequence's page table,
  *           ascending, -1 behind the last; rows of no sequence are not written
  * 0 <= sink, 1 <= recent, sink + recent <= n_select; at most 65536 pages a sequence (MOE_ERR_UNSUPPORTED
- * beyond).  A page outside the cache has the lowest score.  Of args, out, its strides and scale are not
- * used.  workspace as for moe_tree_attention, of moe_select_pages_workspace bytes. */
+ * beyond).  A page outside the cache has the lowest score, and so has one whose score is no number: the
+ * positive and the negative q_d of the heads are summed first, and an infinite bound may meet a sum of zero.
+ * Of args, out, its strides and scale are not used.  workspace as for moe_tree_attention, of
+ * moe_select_pages_workspace bytes. */
 int moe_select_pages_workspace(const moe_kv_cache *cache, const moe_attention *args, int64_t *bytes);
 int moe_select_pages(const moe_kv_cache *cache, const moe_attention *args, const void *bounds,
                      int32_t n_select, int32_t sink, int32_t recent, int32_t *pages, void *workspace,

@@ -561,12 +561,13 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
   const bool kept = CS > 0 || n <= kKeys;
   const auto key_at = [&](int i) { return kept ? s_keys[i] : key_of(score[j0 + i]); };
   uint32_t lo = ~0u, hi = 0u;
-  float size = 0.f;
+  uint32_t most = 0u;  // the largest size, which is positive or NaN: the order is that of the bits, and a NaN stays
   if constexpr (CS > 0) {
     constexpr int P = 4, kPages = P * (kBlock / 8);
     __shared__ __align__(16) float s_sums[2 * D];
     __shared__ float s_size;
     if (CS > 1) cluster_arrive();
+    float size = 0.f;
     if (threadIdx.x == 0) s_size = 0.f;
     Block<T, D, P> b;
     int at = j0 + rank * kPages;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
         if ((threadIdx.x & 7) != 0 || i >= n) continue;
         const uint32_t key = key_of(s[t]);
         lo = min(lo, key), hi = max(hi, key);
-        size = b.top[t] <= size ? size : b.top[t];  // (a NaN stays)
+        size = fmaxf(size, b.top[t]);
         if (CS > 1)
           store_first(smem_u32(s_keys + i), key);
         else
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
       b.fetch(w, kvh, at + CS * kPages, end);
       b.look(w, row.seq, at + 2 * CS * kPages, end);
     }
-    size *= s_size;
+    most = __float_as_uint(size * s_size);
   }
   if (rank == 0) {
     for (int i = threadIdx.x; i < words; i += kBlock) {
@@ -621,14 +622,11 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
       if (kept) s_keys[i] = key;
       lo = min(lo, key), hi = max(hi, key);
     }
-    for (int i = j0 / 16 + threadIdx.x; i <= (j1 - 1) / 16; i += kBlock) {
-      const float s = score[w.width + i];
-      size = s <= size ? size : s;  // (a NaN stays)
-    }
+    for (int i = j0 / 16 + threadIdx.x; i <= (j1 - 1) / 16; i += kBlock)
+      most = max(most, __float_as_uint(score[w.width + i]));
   }
-  // sizes are positive or NaN: their order is that of their bits
   lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
-  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+  most = __reduce_max_sync(0xffffffffu, most);
   __shared__ uint32_t s_part[3][kWarps];
   if (lane == 0) s_part[0][warp] = lo, s_part[1][warp] = hi, s_part[2][warp] = most;
   __syncthreads();
@@ -649,7 +647,7 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
       lo = min(lo, s_range[3 * v]), hi = max(hi, s_range[3 * v + 1]), most = max(most, s_range[3 * v + 2]);
   }
   if (want > 0) {
-    size = __uint_as_float(most);
+    float size = __uint_as_float(most);
     if (!(size <= 3e38f)) size = -kNegInf;
     const float error = 2.f * w.error * size + 1e-40f;  // (products below fp32's range)
     // [lo, hi]: keys among which the want-th largest is; `above` keys are larger than those
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w
     if (!told && need > 0) {
       sum_heads<T, D>(p, row_i, kvh, s_q);
       __syncthreads();
-      bool any = false;
+      bool any = !(error <= 3e38f);  // (zeros times bounds that are infinite are NaN, which has the lowest score)
       for (int d = threadIdx.x; d < 2 * D; d += kBlock) any |= s_q[d] != 0.;
       any = __syncthreads_or(any);  // without (a row of padding), fp32 scores are exact: 0, or the lowest
       const auto exact = [&](int j) {  // a whole warp

@@ -1,5 +1,5 @@
 """Where the calls that do not read the whole cache meet the borders of what they promise: rows of zeros beside pages
-outside the cache, prefixes that end behind a sequence's context."""
+outside the cache or bounds that are infinite, prefixes that end behind a sequence's context."""
 import math
 
 import pytest
@@ -50,6 +50,32 @@ def test_rows_of_zeros_beside_pages_outside_the_cache(lens, pages, gone, n_selec
     b.table[:, gone] = b.k.shape[0] + 3
     got, err = run_select(b, bnd, n_select)
     assert err == 1 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens", [[1], [1] * 40, [1] * 200, [7], [16, 1, 13]])
+@pytest.mark.parametrize("pages", [100, 5000])
+def test_rows_of_zeros_beside_infinite_bounds(lens, pages, dtype):
+    """Zero times infinity is no number: such a page comes last, with those outside the cache, and changes nothing about
+    the others."""
+    lens = lens[:60] if pages > 1000 else lens
+    ctx = [16 * 99] * len(lens)
+    b = C.batch(1, lens, ctx, 4, 2, 64, 16, dtype)
+    b.table = b.table[:, torch.arange(pages) % 100].contiguous()  # (pages may be there more than once)
+    b.ctxs = [16 * (pages - 1)] * len(lens)
+    b.ctx[:] = 16 * (pages - 1)
+    bnd = random_bounds(b, 1)
+    b.q.zero_()
+    gone = [2, 3, 50, 97]
+    for i in range(len(lens)):
+        bnd[int(b.table[i, 4]), :, 1, 9] = float("inf")
+    worst = gone + list(range(4, pages, 100))
+    b.table[:, gone] = b.k.shape[0] + 3
+    free = [j for j in range(1, pages - 1) if j not in worst] + sorted(worst)
+    for n_select in (10, 70, pages - 3):
+        want = sorted([0, pages - 1] + free[:n_select - 2])
+        got, err = run_select(b, bnd, n_select)
+        assert err == 1 and bool((got == torch.tensor(want, dtype=torch.int32)).all())
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
