@@ -428,7 +428,8 @@ int moe_prefix_attention(const moe_kv_cache *cache, const moe_attention *args,
  * .. ctx_len[s] + rows - 1 of sequence s), each key/value head and dimension the least and the largest
  * key over the positions 0 .. ctx_len[s] + rows - 1 on it.  To be called when their keys are in the cache.
  *   bounds  [n_pages][n_kv_heads][2][head_dim] device, cache dtype, 16-byte aligned: least, largest.
- *           Other pages' bounds are left as they are.
+ *           A key that is no number shows in both bounds of its dimension.  Other pages' bounds are left as
+ *           they are; two sequences with new positions on one page write its bounds both, in no order.
  * Of args, q, out, their strides, n_q_heads and scale are not used; n_rows bounds the rows. */
 int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *args, void *bounds, void *stream);
 

@@ -28,12 +28,20 @@ struct Pair<__half> {
   using V = __half2;
   static constexpr uint32_t kMost = 0x7c007c00u, kLeast = 0xfc00fc00u;
 };
+// The lesser and the larger of two pairs; a NaN stays (bounds of a page's keys).
 template <typename T>
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   using V = typename Pair<T>::V;
-  const V r = __hmin2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+  const V r = __hmin2_nan(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+template <typename T>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  using V = typename Pair<T>::V;
+  const V r = __hmax2_nan(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+// The larger of two pairs without NaN (sizes: what bounds the error of the scores that are numbers).
 template <typename T>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   using V = typename Pair<T>::V;
@@ -107,14 +115,14 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
     const uint4 x = load16(k + r * p.tok_stride);
     const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lo[e] = min2<T>(lo[e], y[e]), hi[e] = max2<T>(hi[e], y[e]);
+    for (int e = 0; e < 4; ++e) lo[e] = min2_nan<T>(lo[e], y[e]), hi[e] = max2_nan<T>(hi[e], y[e]);
   }
 #pragma unroll
   for (int o = kChunks; o < 32; o <<= 1)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      lo[e] = min2<T>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-      hi[e] = max2<T>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+      lo[e] = min2_nan<T>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+      hi[e] = max2_nan<T>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
     }
   if (lane < kChunks) {
     s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -127,10 +135,10 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) {
     const uint4 x = top ? s_hi[w][c] : s_lo[w][c];
-    v.x = top ? max2<T>(v.x, x.x) : min2<T>(v.x, x.x);
-    v.y = top ? max2<T>(v.y, x.y) : min2<T>(v.y, x.y);
-    v.z = top ? max2<T>(v.z, x.z) : min2<T>(v.z, x.z);
-    v.w = top ? max2<T>(v.w, x.w) : min2<T>(v.w, x.w);
+    v.x = top ? max2_nan<T>(v.x, x.x) : min2_nan<T>(v.x, x.x);
+    v.y = top ? max2_nan<T>(v.y, x.y) : min2_nan<T>(v.y, x.y);
+    v.z = top ? max2_nan<T>(v.z, x.z) : min2_nan<T>(v.z, x.z);
+    v.w = top ? max2_nan<T>(v.w, x.w) : min2_nan<T>(v.w, x.w);
   }
   T *dst = bounds + ((static_cast<int64_t>(page) * p.hkv + blockIdx.y) * 2 + top) * D + 8 * c;
   *reinterpret_cast<uint4 *>(dst) = v;

@@ -1,5 +1,6 @@
 """Where the calls that do not read the whole cache meet the borders of what they promise: rows of zeros beside pages
-outside the cache or bounds that are infinite, prefixes that end behind a sequence's context."""
+outside the cache or bounds that are infinite, prefixes that end behind a sequence's context, keys and bounds that are no
+numbers."""
 import math
 
 import pytest
@@ -8,7 +9,7 @@ import torch
 from quantized_moe_expert_dequant_gb300 import binding as Bn
 from tests import attention_cases as C
 from tests import sparse_cases as S
-from tests.test_gpu_pages import random_bounds, run_select
+from tests.test_gpu_pages import random_bounds, run_bounds, run_select, shape
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,50 @@ def test_prefixes_that_end_behind_a_sequences_context(n, max_q, dtype):
     ref, tol = b.reference(0.2)
     C.assert_within(got, ref, tol)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (64, 1024)])
+def test_bounds_of_keys_that_are_no_numbers(dtype, D, page):
+    """They show in both bounds of their dimension, wherever on the page they are, and in no other's."""
+    lens, ctxs = [1, 300, 2 * page], [0, 7, page - 1]
+    b = C.batch(D, lens, ctxs, 4, 2, D, page, dtype)
+    for i, at, h, d in ((0, 0, 0, 3), (1, 20, 1, D - 1), (2, 3 * page - 2, 0, 8), (2, page + 9, 1, 0)):
+        b.k[int(b.table[i, at // page]), h, at % page, d] = float("nan")
+    b.k[int(b.table[1, 16 // page]), 0, :, 17] = float("nan")  # all of a dimension's
+    before = random_bounds(b, 1)
+    got, err = run_bounds(b, before)
+    want = S.bounds(b, before)
+    assert err == 0 and int(want.isnan().sum()) == 10
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
+    # such a page has the lowest score
+    i, page_i = 1, int(b.table[1, 20 // page])
+    rows = b.q[1:2]
+    if page == 16:
+        ctx = torch.tensor([16 * 18], **i32)
+        picked = Bn.select_pages(Bn.KvCache(b.k, b.v), got, rows, torch.tensor([0, 1], **i32), ctx, b.table[1:2], 18, 0)
+        lost = [j for j in range(19) if j not in picked[0, 1].tolist()]
+        assert lost == [20 // page] and int(b.table[1, lost[0]]) == page_i
+
+
+def test_pages_that_are_no_numbers_hide_no_sizes():
+    """What fp32 scores may be off goes by the largest bounds of all pages, whichever order a thread meets them in: pages
+    that only exact sums tell apart, then some of NaN, then some of zeros."""
+    pages = 16 * 128 + 3
+    b = C.batch(8, [1], [16 * (pages - 1)], 2, 1, 64, 16, F16)
+    b.q[:] = torch.tensor([1.0, -1.0], device="cuda")[None, :, None].to(F16) * 2.0 ** -6
+    b.q[:, :, 0] = 1024.0
+    gen = torch.Generator().manual_seed(9)
+    bnd = torch.randint(-3, 4, shape(b), generator=gen).sort(2).values.to(F16).cuda() / 16
+    bnd[..., 0] = 512.0
+    place = torch.arange(pages - 2) % 128  # of the pages that are scored, from the second on
+    of = b.table[0, 1:pages - 1].long().cpu()
+    bnd[of[(place >= 32) & (place < 64)]] = float("nan")
+    bnd[of[place >= 64]] = 0.0
+    s = S.scores(b, bnd, 0, 0, 0, pages)[1:-1]
+    key = s.masked_fill(s.isnan(), -math.inf).tolist()
+    order = sorted(range(len(key)), key=lambda j: (-key[j], j))
+    for n_select in (12, 200, 400):
+        want = sorted([0, pages - 1] + [1 + j for j in order[:n_select - 2]])
+        got, err = run_select(b, bnd, n_select)
+        assert err == 0 and got[0, 0].tolist() == want
