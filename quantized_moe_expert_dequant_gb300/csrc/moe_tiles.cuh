@@ -1378,10 +1378,10 @@ static int make_plan(const moe_kv_cache *c, const Params &p, PromptPlan *plan, i
   plan->grid = sms < kMaxCtas ? sms : kMaxCtas;
   plan->ml = plan->share = plan->bytes = 0;
   const int64_t len = static_cast<int64_t>(p.table_width) << p.page_shift;  // of a sequence at most
-  // the line's length times the CTAs stays inside 64 bits
+  // the line's length times the CTAs stays inside 64 bits (kShared counts kBothTiles a position and whole steps)
   double items = static_cast<double>(p.n_rows) / (2 * (128 / p.group)) + p.n_seqs;
-  if (n_groups >= 0) items = 2 * items + n_groups;
-  if (items * (static_cast<double>(len) + kItemCost) * p.hkv * sms > 4e18) return MOE_ERR_UNSUPPORTED;
+  if (n_groups >= 0) items = kBothTiles * (2 * items + n_groups);
+  if (items * (static_cast<double>(len) + kPos + kItemCost) * p.hkv * sms > 4e18) return MOE_ERR_UNSUPPORTED;
   plan->split = (len + kPos - 1) / kPos >= kShareSteps;
   if (!plan->split && n_groups < 0) return MOE_OK;
   plan->ml = 4ll * 2 * plan->grid * 256 * c->head_dim;

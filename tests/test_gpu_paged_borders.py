@@ -1,6 +1,7 @@
 """Where the calls that do not read the whole cache meet the borders of what they promise: rows of zeros beside pages
 outside the cache or bounds that are infinite, prefixes that end behind a sequence's context, keys and bounds that are no
-numbers."""
+numbers, batches beyond 64 bits."""
+import ctypes
 import math
 
 import pytest
@@ -9,6 +10,7 @@ import torch
 from quantized_moe_expert_dequant_gb300 import binding as Bn
 from tests import attention_cases as C
 from tests import sparse_cases as S
+from tests.test_attention_host import attention, cache
 from tests.test_gpu_pages import random_bounds, run_bounds, run_select, shape
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +146,16 @@ def test_pages_that_are_no_numbers_hide_no_sizes():
         want = sorted([0, pages - 1] + [1 + j for j in order[:n_select - 2]])
         got, err = run_select(b, bnd, n_select)
         assert err == 0 and got[0, 0].tolist() == want
+
+
+def test_batches_beyond_64_bits_are_refused():
+    """The tiles' line counts eight units a position and item, and its length times the CTAs has to fit.  (The question
+    for the workspace is all that is asked here: 2^30 positions in each of a million sequences.)"""
+    L, n = Bn.lib(), ctypes.c_int64()
+    c = cache(page_size=1024, head_dim=128, n_pages=2 ** 20, n_kv_heads=8, head_stride=1024 * 128, token_stride=128,
+              page_stride=8 * 1024 * 128)
+    many = dict(table_width=2 ** 20, table_stride=2 ** 20, n_q_heads=8)
+    ask = lambda seqs: L.moe_prefix_attention_workspace(
+        ctypes.byref(c), ctypes.byref(attention(n_seqs=seqs, n_rows=seqs, **many)), 1, 64, ctypes.byref(n))
+    assert ask(10 ** 6) == Bn.MOE_ERR_UNSUPPORTED
+    assert ask(10 ** 5) == Bn.MOE_OK and n.value > 0
