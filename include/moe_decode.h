@@ -438,7 +438,10 @@ int moe_page_bounds(const moe_kv_cache *cache, const moe_attention *args, void *
  * them, all; else the first `sink`, the last `recent`, and of the others those with the largest
  *   score = sum over the query heads of the key/value head of sum_d max(q_d least_d, q_d largest_d),
  * an upper bound of the sum of q . k over those heads for each key on the page; of equal scores the
- * lower page's first.  The comparison is that of exact scores (fp64).
+ * lower page's first.  What is compared are sums in fp64.  With g query heads a key/value head these are
+ * exact while no product of a q_d and a bound is more than 2^(29 - log2(g head_dim)) (fp16; bf16: 2^(35 - ..))
+ * times the smallest that is not 0; beyond that, scores that differ by less than 2^-45 of their
+ * terms' sizes may be taken in either order, but pages with the same bounds are always equal.
  *   pages   int32 [n_rows][n_kv_heads][n_select] device: places in the sequence's page table,
  *           ascending, -1 behind the last; rows of no sequence are not written
  * 0 <= sink, 1 <= recent, sink + recent <= n_select; at most 65536 pages a sequence (MOE_ERR_UNSUPPORTED

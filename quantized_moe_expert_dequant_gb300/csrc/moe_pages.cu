@@ -147,9 +147,17 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(const Params p, T *bound
 // ------------------------------------------------------------------ selection
 // The order of two pages may hang on the last bit of their scores, so it is decided in two steps: fp32 scores
 // with a bound on their error tell which pages are certainly among the k best and which are certainly
-// not; what lies between is compared by scores in fp64 (exact but for bounds and queries that differ by more
-// than 2^30).  A score is the fp32 sum of terms Q b, Q a sum over the heads of numbers of one sign.  It is off by
-// less than `error` times the sum of the terms' sizes, and that is at most max_d |b_d| times sum_d |Q_d|.
+// not; what lies between is compared by scores in fp64.  A score is the fp32 sum of terms Q b, Q a sum over the heads of
+// numbers of one sign.  It is off by less than `error` times the sum of the terms' sizes, and that is at most
+// max_d |b_d| times sum_d |Q_d|.
+//
+// When sums in fp64 are exact: of g heads and D dimensions a score has g D products q b (each meets one of its two
+// bounds).  Of a product in [2^s, 2^(s+2)) the last bit is at least 2^(s-20) (two numbers of 11 bits; bf16, 8 bits: 2^(s-14)),
+// the sum of all is below g D 2^(S+2), S that of the largest, and fp64 holds 53 bits: so while S - s <= 31 - log2(g D)
+// (bf16: 37), that is, while the largest product is not 2^(29 - log2(g D)) (2^(35 - ...)) times the least one that is
+// not 0, every partial sum of Q and of the terms is exact, in any order.  4 heads of 128: 2^20 and 2^26; 64: 2^16 and 2^22.
+// Beyond that they are sums of g + 2 D / 32 + 5 roundings in an order that is the same for all pages: pages with the
+// same bounds still tie, others that are equal but for these roundings may not.
 constexpr int kMaxPages = 65536;     // of a sequence: a bit each in shared memory
 constexpr int kKeys = 8192;          // scores that are kept in shared memory
 constexpr int kBins = 1024;
@@ -170,8 +178,7 @@ __device__ __forceinline__ bool better(double a, int i, double b, int j) {
   return a > b || (a == b && i < j);
 }
 
-// Q- and Q+ of a row and key/value head, side by side as the bounds are; in fp64 the sum of up to 64 values of
-// 16 bits is exact but for values that differ by more than 2^40.  Returns this thread's sum of sizes.
+// Q- and Q+ of a row and key/value head, side by side as the bounds are.  Returns this thread's sum of sizes.
 template <typename T, int D, typename V>
 __device__ __forceinline__ V sum_heads(const Params &p, int row, int kvh, V *s_q) {
   const T *q = static_cast<const T *>(p.q) + row * p.q_row +
@@ -534,6 +541,9 @@ __device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
 // 17.9 with the scores in a kernel of their own.)  CS = 0 is bound by its barriers, so eight blocks an SM, in 32
 // registers: 512 rows, 2 heads, 2000 pages, all 1024 blocks at once, 35.2 us with the scores; 38.4 with six in 40, no
 // better than without a limit (47, 37.8), although 32 spill some words.  (Apart and cold: 23.4 the scores, 24.2 this.)
+// So too where they are more than fit: us with eight, six, no limit, 2048 rows, 2 heads, 2000 pages 109, 116, 114; 2048
+// rows, 8 heads of 128, 2048 pages 471, 496, 492; 4096 rows, 4 heads, 2000 pages 402, 443, 437.  One token each of 16
+// sequences, 8 heads, 9376 pages 194, 196, 192.
 // A least number for CS > 0 too lets the compiler take up to 205 registers: 12.9 us for the one token, 9.7 without.
 template <typename T, int D, int CS>
 __global__ void __launch_bounds__(kBlock, CS ? 0 : 8) pick_kernel(const Select w) {
